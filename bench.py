@@ -127,9 +127,12 @@ def _code_only(text: str) -> str:
 
 
 def kernel_source_hash() -> str:
+    """Hash of the verification kernels' sources (the paged-cache operators
+    are another translation unit with a header of its own)."""
     h = hashlib.sha256()
     src = ROOT / "speculative_decoding_verification_75_gb300" / "csrc"
-    for f in sorted(src.glob("*")) + sorted((ROOT / "include").glob("*.h")):
+    headers = [f for f in sorted((ROOT / "include").glob("*.h")) if f.name != "sv_paged.h"]
+    for f in sorted(src.glob("*")) + headers:
         h.update(f.name.encode())
         h.update(_code_only(f.read_text()).encode())
     return h.hexdigest()[:16]

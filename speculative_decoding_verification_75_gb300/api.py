@@ -35,10 +35,12 @@ SV_BAD_U_SAMPLE = 0x10
 SV_BAD_NORMALISER = 0x20
 SV_FAULT_TIMEOUT = 0x10000
 
-# Every symbol include/spec_verify.h declares.
+# Every symbol the headers in include/ declare.
 EXPORTS = ("sv_workspace_bytes", "spec_verify", "spec_verify_diag",
            "sv_last_error", "sv_status_string", "spec_verify_noalloc", "sv_kv_rollback",
-           "sv_selftest_wait_timeout", "sv_set_small_batch_path")
+           "sv_selftest_wait_timeout", "sv_set_small_batch_path",
+           "sv_kv_write", "sv_kv_read", "sv_kv_compact", "sv_tree_attention",
+           "sv_tree_attention_workspace_bytes")
 
 # Bits of the status word of sv_kv_rollback (include/spec_verify.h).
 SV_KV_FREE_LIST_FULL = 0x1
@@ -99,6 +101,12 @@ def load_library():
     lib.sv_selftest_wait_timeout.argtypes = [_P, _P, ctypes.c_uint, _P]
     lib.sv_kv_rollback.restype = _I
     lib.sv_kv_rollback.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _P, _P]
+    for name in ("sv_kv_write", "sv_kv_read", "sv_kv_compact", "sv_tree_attention"):
+        fn = getattr(lib, name)
+        fn.restype = _I
+        fn.argtypes = [ctypes.c_char_p, _P]  # a packed argument struct, the stream
+    lib.sv_tree_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.sv_tree_attention_workspace_bytes.argtypes = [ctypes.c_int64] * 5
     _lib = lib
     return lib
 

@@ -1,10 +1,12 @@
 """Build ``lib/libspecverify.so`` (the CUDA verification library) in-tree.
 
-One translation unit, compiled for sm_103a only.  The result is git-ignored;
-every machine that runs the library builds it from source.
+Two translation units (the verification step, the paged KV cache), compiled
+in parallel for sm_103a only and linked.  The result is git-ignored; every
+machine that runs the library builds it from source.
 """
 from __future__ import annotations
 
+import concurrent.futures as cf
 import os
 import shutil
 import subprocess
@@ -14,12 +16,14 @@ PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 SRC_DIR = PKG / "csrc"
 MAIN = SRC_DIR / "spec_verify.cu"
+PAGED_DIR = PKG / "paged"
+UNITS = [MAIN, PAGED_DIR / "sv_paged.cu"]
 INCLUDE = ROOT / "include"
 LIB = PKG / "lib" / "libspecverify.so"
 
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo",
               "-gencode", "arch=compute_103a,code=sm_103a",
-              "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
+              "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 
 
 def nvcc() -> str:
@@ -30,7 +34,8 @@ def nvcc() -> str:
 
 
 def sources():
-    return [MAIN, *sorted(SRC_DIR.glob("*.cuh")), INCLUDE / "spec_verify.h"]
+    return [*UNITS, *sorted(SRC_DIR.glob("*.cuh")), *sorted(PAGED_DIR.glob("*.cuh")),
+            *sorted(INCLUDE.glob("*.h"))]
 
 
 def is_stale() -> bool:
@@ -40,9 +45,13 @@ def is_stale() -> bool:
     return any(s.stat().st_mtime > t for s in sources())
 
 
-def build_command(out: Path, defines=()):
-    return [nvcc(), *NVCC_FLAGS, *[f"-D{d}" for d in defines], f"-I{INCLUDE}", str(MAIN),
-            "-o", str(out)]
+def compile_command(unit: Path, out: Path, defines=()):
+    return [nvcc(), *NVCC_FLAGS, *[f"-D{d}" for d in defines], f"-I{INCLUDE}", f"-I{SRC_DIR}",
+            "-c", str(unit), "-o", str(out)]
+
+
+def link_command(objects, out: Path):
+    return [nvcc(), *NVCC_FLAGS, "-shared", *[str(o) for o in objects], "-o", str(out)]
 
 
 def build(force: bool = False, verbose: bool = False) -> Path:
@@ -50,12 +59,24 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     if not force and not is_stale():
         return LIB
     LIB.parent.mkdir(parents=True, exist_ok=True)
-    tmp = LIB.with_name(f".{LIB.name}.tmp{os.getpid()}")
-    cmd = build_command(tmp)
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    tag = f"tmp{os.getpid()}"
+    tmp = LIB.with_name(f".{LIB.name}.{tag}")
+    objects = [LIB.parent / f".{u.stem}.{tag}.o" for u in UNITS]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd))
+        subprocess.run(cmd, check=True)
+
+    try:
+        with cf.ThreadPoolExecutor(len(UNITS)) as ex:
+            for f in [ex.submit(run, compile_command(u, o)) for u, o in zip(UNITS, objects)]:
+                f.result()
+        run(link_command(objects, tmp))
+        os.replace(tmp, LIB)
+    finally:
+        for o in objects:
+            o.unlink(missing_ok=True)
     return LIB
 
 

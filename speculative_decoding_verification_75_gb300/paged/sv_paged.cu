@@ -1,0 +1,269 @@
+// sv_paged.cu -- C ABI of the paged-cache operators (include/sv_paged.h):
+// argument checks, the choice of a kernel and the launches.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "sv_paged.h"
+#include "sv_paged_common.cuh"
+#include "sv_paged_cache.cuh"
+#include "sv_attn_general.cuh"
+
+namespace svp {
+namespace {
+
+bool aligned(const void *p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+int elem_bytes(int64_t dtype) {
+  return dtype == SV_F32 ? 4 : dtype == SV_BF16 || dtype == SV_F16 ? 2 : dtype == SV_E4M3 ? 1 : 0;
+}
+
+constexpr int64_t kMaxStride = int64_t{1} << 46;  // elements; far past any memory
+
+// Checks a cache and its block tables (B rows) and lays it out in bytes.
+sv_status take_cache(const sv_kv_cache &c, int64_t B, bool layered, Cache &o) {
+  if (c.dtype != SV_BF16 && c.dtype != SV_F16 && c.dtype != SV_E4M3)
+    return SV_ERR_UNSUPPORTED_DTYPE;
+  const bool f8 = c.dtype == SV_E4M3;
+  const int64_t esz = elem_bytes(c.dtype);
+  if (c.num_blocks < 0 || c.num_blocks > INT_MAX || c.num_kv_heads < 1 ||
+      c.num_kv_heads > 65536 || c.block_size < 1 || c.block_size > (1 << 20) ||
+      c.head_dim < 8 || c.head_dim > SV_KV_MAX_HEAD_DIM || c.head_dim % (f8 ? 32 : 8) ||
+      c.num_layers < 1 || c.num_layers > (layered ? 65536 : 1) || c.max_blocks < 0 ||
+      c.max_blocks > INT_MAX)
+    return SV_ERR_INVALID_ARG;
+  const int64_t rows = c.num_kv_heads * c.block_size;
+  if (rows * c.head_dim > INT_MAX || c.max_blocks * c.block_size > INT_MAX) return SV_ERR_INVALID_ARG;
+  // A pool or a table may be empty (then every position is reported missing).
+  if ((c.num_blocks > 0 && (!c.k || !c.v || (f8 && (!c.k_scale || !c.v_scale)))) ||
+      (c.max_blocks > 0 && B > 0 && !c.block_tables))
+    return SV_ERR_INVALID_ARG;
+  if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.block_tables, 4)) return SV_ERR_INVALID_ARG;
+  const auto stride_ok = [](int64_t s, int64_t least, int64_t unit, bool used) {
+    return !used || (s >= least && s <= kMaxStride && s % unit == 0);
+  };
+  const bool many = c.num_blocks > 1, deep = c.num_layers > 1;
+  if (!stride_ok(c.block_stride, rows * c.head_dim, 16 / esz, many) ||
+      !stride_ok(c.layer_stride, rows * c.head_dim, 16 / esz, deep))
+    return SV_ERR_INVALID_ARG;
+  if (f8) {
+    if (!aligned(c.k_scale, 16) || !aligned(c.v_scale, 16) ||
+        !stride_ok(c.scale_block_stride, rows * c.head_dim / SV_KV_GROUP, 1, many) ||
+        !stride_ok(c.scale_layer_stride, rows * c.head_dim / SV_KV_GROUP, 1, deep))
+      return SV_ERR_INVALID_ARG;
+  }
+  o.k = static_cast<uint8_t *>(c.k);
+  o.v = static_cast<uint8_t *>(c.v);
+  o.ks = f8 ? c.k_scale : nullptr;
+  o.vs = f8 ? c.v_scale : nullptr;
+  o.block_bytes = many ? c.block_stride * esz : 0;
+  o.layer_bytes = deep ? c.layer_stride * esz : 0;
+  o.sblock_bytes = f8 && many ? c.scale_block_stride : 0;
+  o.slayer_bytes = f8 && deep ? c.scale_layer_stride : 0;
+  o.tables = c.block_tables;
+  o.num_layers = static_cast<int>(c.num_layers);
+  o.num_blocks = static_cast<int>(c.num_blocks);
+  o.heads = static_cast<int>(c.num_kv_heads);
+  o.bs = static_cast<int>(c.block_size);
+  o.D = static_cast<int>(c.head_dim);
+  o.max_blocks = static_cast<int>(c.max_blocks);
+  return SV_OK;
+}
+
+// Strides of a dense side [B, T, heads, D] with dense rows, in bytes.
+bool take_strides(const int64_t (&s)[3], int esz, int64_t &b, int64_t &t, int64_t &h) {
+  for (int64_t x : s)
+    if (x < 0 || x > kMaxStride) return false;
+  b = s[0] * esz;
+  t = s[1] * esz;
+  h = s[2] * esz;
+  return true;
+}
+
+bool batch_ok(int64_t B, int64_t T) {
+  return B >= 0 && T >= 0 && B <= INT_MAX && T <= INT_MAX && (B == 0 || T <= INT_MAX / B);
+}
+
+template <typename K, typename P>
+sv_status launch(K kernel, dim3 grid, int threads, size_t smem, sv_stream_t stream, const P &p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+// The dense side of kv_write and kv_read and their grid.
+sv_status take_move(MoveParams &p, const void *key, const void *value, const int64_t (&ks)[3],
+                    const int64_t (&vs)[3], int64_t B, int64_t T, int esz, dim3 &grid) {
+  if (!key || !value || !aligned(key, esz) || !aligned(value, esz)) return SV_ERR_INVALID_ARG;
+  p.key = static_cast<uint8_t *>(const_cast<void *>(key));
+  p.value = static_cast<uint8_t *>(const_cast<void *>(value));
+  if (!take_strides(ks, esz, p.ksb, p.kst, p.ksh) || !take_strides(vs, esz, p.vsb, p.vst, p.vsh))
+    return SV_ERR_INVALID_ARG;
+  // Strides of dimensions of one element are never used.
+  const int64_t used = (B > 1 ? p.ksb | p.vsb : 0) | (T > 1 ? p.kst | p.vst : 0) |
+                       (p.c.heads > 1 ? p.ksh | p.vsh : 0);
+  p.vec = aligned(key, 16) && aligned(value, 16) && used % 16 == 0;
+  p.groups = static_cast<int>((T + kMoveTokens - 1) / kMoveTokens);
+  const int64_t blocks = B * p.groups;
+  const int64_t cols = 2ll * p.c.heads * (p.c.D / 8);
+  const int64_t gy = (cols + kMoveThreads - 1) / kMoveThreads;
+  if (blocks > INT_MAX || gy > 65535) return SV_ERR_INVALID_ARG;
+  grid = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(gy));
+  return SV_OK;
+}
+
+sv_status kv_write(const sv_kv_write_args *a, sv_stream_t stream) {
+  if (!a || a->struct_bytes != sizeof *a || !batch_ok(a->B, a->T)) return SV_ERR_INVALID_ARG;
+  if (a->dtype != SV_BF16 && a->dtype != SV_F16) return SV_ERR_UNSUPPORTED_DTYPE;
+  MoveParams p = {};
+  if (const sv_status s = take_cache(a->cache, a->B, false, p.c)) return s;
+  if (a->cache.dtype != SV_E4M3 && a->cache.dtype != a->dtype) return SV_ERR_UNSUPPORTED_DTYPE;
+  if (a->B == 0 || a->T == 0) return SV_OK;
+  if (!a->seq_lens) return SV_ERR_INVALID_ARG;
+  p.bt = Batch{a->seq_lens, a->new_lens, static_cast<int>(a->B), static_cast<int>(a->T), a->status};
+  dim3 grid;
+  if (const sv_status s = take_move(p, a->key, a->value, a->key_stride, a->value_stride, a->B,
+                                    a->T, 2, grid))
+    return s;
+  if (a->cache.dtype != SV_E4M3)  // a copy: the two 16-bit types are one
+    return launch(sv_kv_write_kernel<BF16, BF16>, grid, kMoveThreads, 0, stream, p);
+  return a->dtype == SV_BF16
+             ? launch(sv_kv_write_kernel<BF16, E4M3>, grid, kMoveThreads, 0, stream, p)
+             : launch(sv_kv_write_kernel<F16, E4M3>, grid, kMoveThreads, 0, stream, p);
+}
+
+template <typename C>
+sv_status read_as(int64_t dtype, dim3 grid, sv_stream_t stream, const MoveParams &p) {
+  if (dtype == SV_BF16) return launch(sv_kv_read_kernel<C, BF16>, grid, kMoveThreads, 0, stream, p);
+  if (dtype == SV_F16) return launch(sv_kv_read_kernel<C, F16>, grid, kMoveThreads, 0, stream, p);
+  return launch(sv_kv_read_kernel<C, F32>, grid, kMoveThreads, 0, stream, p);
+}
+
+sv_status kv_read(const sv_kv_read_args *a, sv_stream_t stream) {
+  if (!a || a->struct_bytes != sizeof *a || !batch_ok(a->B, a->T)) return SV_ERR_INVALID_ARG;
+  if (a->dtype != SV_BF16 && a->dtype != SV_F16 && a->dtype != SV_F32)
+    return SV_ERR_UNSUPPORTED_DTYPE;
+  MoveParams p = {};
+  if (const sv_status s = take_cache(a->cache, a->B, false, p.c)) return s;
+  if (a->B == 0 || a->T == 0) return SV_OK;
+  if (!a->lens) return SV_ERR_INVALID_ARG;
+  p.starts = a->starts;
+  p.bt = Batch{nullptr, a->lens, static_cast<int>(a->B), static_cast<int>(a->T), a->status};
+  dim3 grid;
+  if (const sv_status s = take_move(p, a->key, a->value, a->key_stride, a->value_stride, a->B,
+                                    a->T, elem_bytes(a->dtype), grid))
+    return s;
+  if (a->cache.dtype == SV_BF16) return read_as<BF16>(a->dtype, grid, stream, p);
+  if (a->cache.dtype == SV_F16) return read_as<F16>(a->dtype, grid, stream, p);
+  return read_as<E4M3>(a->dtype, grid, stream, p);
+}
+
+sv_status kv_compact(const sv_kv_compact_args *a, sv_stream_t stream) {
+  if (!a || a->struct_bytes != sizeof *a || !batch_ok(a->B, a->P)) return SV_ERR_INVALID_ARG;
+  CompactParams p = {};
+  if (const sv_status s = take_cache(a->cache, a->B, true, p.c)) return s;
+  if (a->B == 0) return SV_OK;
+  if (!a->num_accepted || !a->seq_lens || (a->P > 0 && !a->path)) return SV_ERR_INVALID_ARG;
+  p.path = a->path;
+  p.num_accepted = a->num_accepted;
+  p.seq_lens = a->seq_lens;
+  p.B = static_cast<int>(a->B);
+  p.P = static_cast<int>(a->P);
+  p.esz = elem_bytes(a->cache.dtype);
+  p.status = a->status;
+  const int64_t units = 2ll * p.c.heads * (p.c.D * p.esz / 16 + (p.esz == 1 ? p.c.D / SV_KV_GROUP : 0));
+  const int64_t blocks = a->B * p.c.num_layers, gy = (units + kMoveThreads - 1) / kMoveThreads;
+  if (blocks > INT_MAX || gy > 65535) return SV_ERR_INVALID_ARG;
+  return launch(sv_kv_compact_kernel,
+                dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(gy)), kMoveThreads, 0,
+                stream, p);
+}
+
+template <typename Q>
+sv_status attn_general(int64_t cache_dtype, const AttnParams &p, sv_stream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.bt.B) * p.bt.T * p.Hq;
+  if (rows > INT_MAX) return SV_ERR_INVALID_ARG;
+  const dim3 grid(static_cast<unsigned>(rows));
+  return cache_dtype == SV_E4M3
+             ? launch(sv_attn_general_kernel<Q, E4M3>, grid, 32 * kGenWarps, 0, stream, p)
+             : launch(sv_attn_general_kernel<Q, Q>, grid, 32 * kGenWarps, 0, stream, p);
+}
+
+bool attn_sizes_ok(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
+  return batch_ok(B, T) && Hkv >= 1 && Hkv <= 65536 && Hq >= Hkv && Hq <= 65536 && Hq % Hkv == 0 &&
+         D >= 8 && D <= SV_KV_MAX_HEAD_DIM && D % 8 == 0 && (B * T == 0 || Hq <= INT_MAX / (B * T));
+}
+
+sv_status tree_attention(const sv_tree_attention_args *a, sv_stream_t stream) {
+  if (!a || a->struct_bytes != sizeof *a || !batch_ok(a->B, a->T)) return SV_ERR_INVALID_ARG;
+  if (a->dtype != SV_BF16 && a->dtype != SV_F16) return SV_ERR_UNSUPPORTED_DTYPE;
+  AttnParams p = {};
+  if (const sv_status s = take_cache(a->cache, a->B, false, p.c)) return s;
+  if (a->cache.dtype != SV_E4M3 && a->cache.dtype != a->dtype) return SV_ERR_UNSUPPORTED_DTYPE;
+  if (!attn_sizes_ok(a->B, a->T, a->num_heads, p.c.heads, p.c.D) || !std::isfinite(a->scale))
+    return SV_ERR_INVALID_ARG;
+  const double sl2 = a->scale * 1.4426950408889634;
+  if (std::fabs(sl2) > 3.4e38) return SV_ERR_INVALID_ARG;
+  if (a->B == 0 || a->T == 0) return SV_OK;
+  if (!a->seq_lens || !a->query || !a->out || !a->workspace) return SV_ERR_INVALID_ARG;
+  if (!aligned(a->query, 2) || !aligned(a->out, 16) || !aligned(a->workspace, 256) ||
+      !aligned(a->lse, 4) || a->mask_batch_stride < 0)
+    return SV_ERR_INVALID_ARG;
+  if (a->workspace_bytes < sv_tree_attention_workspace_bytes(a->B, a->T, a->num_heads, p.c.heads, p.c.D))
+    return SV_ERR_WORKSPACE_TOO_SMALL;
+  p.bt = Batch{a->seq_lens, a->new_lens, static_cast<int>(a->B), static_cast<int>(a->T), a->status};
+  p.q = static_cast<const uint8_t *>(a->query);
+  if (!take_strides(a->query_stride, 2, p.qsb, p.qst, p.qsh)) return SV_ERR_INVALID_ARG;
+  const int64_t used = (a->B > 1 ? p.qsb : 0) | (a->T > 1 ? p.qst : 0) | (a->num_heads > 1 ? p.qsh : 0);
+  p.qvec = aligned(a->query, 16) && used % 16 == 0;
+  p.mask = a->tree_mask;
+  p.msb = a->mask_batch_stride;
+  p.out = static_cast<uint8_t *>(a->out);
+  p.lse = a->lse;
+  p.scale_log2 = static_cast<float>(sl2);
+  p.Hq = static_cast<int>(a->num_heads);
+  p.G = p.Hq / p.c.heads;
+  return a->dtype == SV_BF16 ? attn_general<BF16>(a->cache.dtype, p, stream)
+                             : attn_general<F16>(a->cache.dtype, p, stream);
+}
+
+}  // namespace
+}  // namespace svp
+
+extern "C" {
+
+sv_status sv_kv_write(const sv_kv_write_args *args, sv_stream_t stream) {
+  return svp::kv_write(args, stream);
+}
+
+sv_status sv_kv_read(const sv_kv_read_args *args, sv_stream_t stream) {
+  return svp::kv_read(args, stream);
+}
+
+sv_status sv_kv_compact(const sv_kv_compact_args *args, sv_stream_t stream) {
+  return svp::kv_compact(args, stream);
+}
+
+sv_status sv_tree_attention(const sv_tree_attention_args *args, sv_stream_t stream) {
+  return svp::tree_attention(args, stream);
+}
+
+size_t sv_tree_attention_workspace_bytes(int64_t B, int64_t T, int64_t num_heads,
+                                         int64_t num_kv_heads, int64_t head_dim) {
+  if (!svp::attn_sizes_ok(B, T, num_heads, num_kv_heads, head_dim)) return 0;
+  return 256;
+}
+
+}  // extern "C"
