@@ -148,9 +148,9 @@ SV_API sv_status sv_kv_compact(const sv_kv_compact_args *args, sv_stream_t strea
  *   num_kv_heads).
  * Visible to new token i of request b: every j < L, and j = L + c with c < n
  * and tree_mask[b, i, c] != 0 (no mask: c <= i, a chain or a prompt).  What is
- * not visible has no influence, whatever it holds.  A row that sees nothing
- * is 0, its lse -inf.  A row that sees a NaN or an infinity follows the
- * formula in IEEE arithmetic.
+ * not visible has no influence, whatever it holds.  A row that sees nothing,
+ * or nothing but scores of -inf, is 0, its lse -inf.  A row that sees another
+ * NaN or infinity follows the formula in IEEE arithmetic.
  *
  *   query     [B, T, num_heads, head_dim] of `dtype` (SV_BF16 or SV_F16; the
  *             cache's own type, or any of the two for SV_E4M3), strides as in

@@ -2,6 +2,8 @@
 // argument checks, the choice of a kernel and the launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -10,6 +12,7 @@
 #include "sv_paged_common.cuh"
 #include "sv_paged_cache.cuh"
 #include "sv_attn_general.cuh"
+#include "sv_attn_tc.cuh"
 
 namespace svp {
 namespace {
@@ -201,6 +204,147 @@ sv_status attn_general(int64_t cache_dtype, const AttnParams &p, sv_stream_t str
              : launch(sv_attn_general_kernel<Q, Q>, grid, 32 * kGenWarps, 0, stream, p);
 }
 
+// ------------------------------------------- tensor-core attention ----
+
+constexpr int kMaxDevices = 64;
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once per process.
+EncodeTiled encode_tiled() {
+  static std::atomic<void *> fn{nullptr};
+  void *f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeTiled>(f);
+}
+
+// A cache side as [block][head][row][element]; boxes of `box` rows, 128
+// bytes wide for 16-bit types (swizzled, as the tensor cores read them), a
+// whole row for e4m3.
+bool make_map(CUtensorMap &m, const Cache &c, const void *base, int64_t dtype, int box) {
+  const EncodeTiled enc = encode_tiled();
+  if (!enc) return false;
+  const bool f8 = dtype == SV_E4M3;
+  const cuuint64_t esz = f8 ? 1 : 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.bs),
+                              static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.num_blocks)};
+  const cuuint64_t row = c.D * esz, head = row * c.bs;
+  const cuuint64_t strides[3] = {row, head,
+                                 c.block_bytes ? static_cast<cuuint64_t>(c.block_bytes) : head * c.heads};
+  const cuuint32_t boxes[4] = {f8 ? static_cast<cuuint32_t>(c.D) : 64u, static_cast<cuuint32_t>(box), 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return enc(&m,
+             f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                : dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             4, const_cast<void *>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace of the tensor-core path.
+struct TcLayout {
+  size_t head, pre, dirty, slots, total;
+  int MP, slot_rows, slot_floats;
+};
+
+TcLayout tc_layout(int64_t B, int64_t T, int64_t G, int64_t heads, int64_t D) {
+  const auto up = [](size_t x, size_t a) { return (x + a - 1) / a * a; };
+  TcLayout w;
+  const int64_t rows = T * G;
+  const int64_t unit = rows > kTile ? 2 * kTile : kTile;
+  w.MP = static_cast<int>(std::max<int64_t>((rows + unit - 1) / unit, 1));
+  w.slot_rows = static_cast<int>(up(std::min<int64_t>(std::max<int64_t>(rows, 1), unit), 32));
+  w.slot_floats = static_cast<int>(up((D + 2) * w.slot_rows + 1, 32));
+  w.head = 0;
+  w.pre = 256;
+  w.dirty = w.pre + up(4 * (B + 1), 256);
+  w.slots = w.dirty + up(B * heads * w.MP, 256);
+  w.total = w.slots + up(static_cast<size_t>(kMaxGrid) * 2 * w.slot_floats * 4, 256);
+  return w;
+}
+
+// What the tensor-core kernel takes: whole 8-row swizzle atoms per page, 16-
+// bit tiles of the query's own type (an e4m3 code times its scale is a bf16
+// number, but not always an fp16 one), sizes within TMA's and int32's.
+bool tc_takes(const sv_tree_attention_args *a, const AttnParams &p, const TcLayout &w) {
+  if (p.c.D != 64 && p.c.D != 128) return false;
+  if (p.c.bs % 8 || p.c.num_blocks < 1) return false;
+  if (a->cache.dtype == SV_E4M3 && (a->dtype != SV_BF16 || p.c.sblock_bytes % 16)) return false;
+  if (p.c.block_bytes >= (int64_t{1} << 40)) return false;
+  const int64_t tiles = std::max<int64_t>((static_cast<int64_t>(p.c.max_blocks) * p.c.bs + kTile - 1) / kTile, 1);
+  const int64_t units = static_cast<int64_t>(p.bt.B) * p.c.heads * w.MP;
+  return units <= INT_MAX / tiles && static_cast<int64_t>(p.bt.T) * p.G <= INT_MAX / 2;
+}
+
+template <typename Q, typename C, int D, bool kPair>
+sv_status tc_launch(const TcParams &p, int nsm, int dev, sv_stream_t stream) {
+  using S = Shape<Q, C, D, kPair>;
+  static std::atomic<uint64_t> done{0};
+  auto *k = sv_attn_tc_kernel<Q, C, D, kPair>;
+  const uint64_t bit = 1ull << (dev % kMaxDevices);
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
+      return SV_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int grid = std::min(nsm, kMaxGrid);
+  if (const sv_status s = launch(k, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, stream, p))
+    return s;
+  const int rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.a.bt.T) * p.a.G, S::kRows));
+  const int64_t units = static_cast<int64_t>(p.a.bt.B) * p.a.c.heads * p.MP;
+  return launch(sv_attn_join_kernel<Q, C, D, kPair>,
+                dim3(static_cast<unsigned>(units),
+                     static_cast<unsigned>((rows * (D / 4) + kJoinThreads - 1) / kJoinThreads)),
+                kJoinThreads, 0, stream, p);
+}
+
+template <typename Q, typename C>
+sv_status tc_pick(const TcParams &p, bool pair, int nsm, int dev, sv_stream_t stream) {
+  if (p.a.c.D == 64)
+    return pair ? tc_launch<Q, C, 64, true>(p, nsm, dev, stream) : tc_launch<Q, C, 64, false>(p, nsm, dev, stream);
+  return pair ? tc_launch<Q, C, 128, true>(p, nsm, dev, stream) : tc_launch<Q, C, 128, false>(p, nsm, dev, stream);
+}
+
+sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const TcLayout &w,
+                  sv_stream_t stream) {
+  int dev = 0, nsm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SV_ERR_CUDA;
+  TcParams p = {};
+  p.a = ap;
+  uint8_t *ws = static_cast<uint8_t *>(a->workspace);
+  p.head = reinterpret_cast<int32_t *>(ws + w.head);
+  p.err = a->status ? a->status : reinterpret_cast<uint32_t *>(ws + w.head) + 1;
+  p.pre = reinterpret_cast<int32_t *>(ws + w.pre);
+  p.dirty = ws + w.dirty;
+  p.slots = reinterpret_cast<float *>(ws + w.slots);
+  p.slot_rows = w.slot_rows;
+  p.slot_floats = w.slot_floats;
+  p.MP = w.MP;
+  p.box = 8;
+  while (p.box < kTile && ap.c.bs % (2 * p.box) == 0) p.box *= 2;
+  p.c = std::max(std::fabs(ap.scale_log2), 1e-30f);
+  p.negate = ap.scale_log2 < 0.f;
+  if (!make_map(p.kmap, ap.c, ap.c.k, a->cache.dtype, p.box) ||
+      !make_map(p.vmap, ap.c, ap.c.v, a->cache.dtype, p.box))
+    return SV_ERR_CUDA;
+  const bool pair = static_cast<int64_t>(ap.bt.T) * ap.G > kTile;
+  if (a->cache.dtype == SV_E4M3) return tc_pick<BF16, E4M3>(p, pair, nsm, dev, stream);
+  return a->dtype == SV_BF16 ? tc_pick<BF16, BF16>(p, pair, nsm, dev, stream)
+                             : tc_pick<F16, F16>(p, pair, nsm, dev, stream);
+}
+
 bool attn_sizes_ok(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
   return batch_ok(B, T) && Hkv >= 1 && Hkv <= 65536 && Hq >= Hkv && Hq <= 65536 && Hq % Hkv == 0 &&
          D >= 8 && D <= SV_KV_MAX_HEAD_DIM && D % 8 == 0 && (B * T == 0 || Hq <= INT_MAX / (B * T));
@@ -235,6 +379,8 @@ sv_status tree_attention(const sv_tree_attention_args *a, sv_stream_t stream) {
   p.scale_log2 = static_cast<float>(sl2);
   p.Hq = static_cast<int>(a->num_heads);
   p.G = p.Hq / p.c.heads;
+  const TcLayout w = tc_layout(a->B, a->T, p.G, p.c.heads, p.c.D);
+  if (tc_takes(a, p, w)) return attn_tc(a, p, w, stream);
   return a->dtype == SV_BF16 ? attn_general<BF16>(a->cache.dtype, p, stream)
                              : attn_general<F16>(a->cache.dtype, p, stream);
 }
@@ -263,7 +409,7 @@ sv_status sv_tree_attention(const sv_tree_attention_args *args, sv_stream_t stre
 size_t sv_tree_attention_workspace_bytes(int64_t B, int64_t T, int64_t num_heads,
                                          int64_t num_kv_heads, int64_t head_dim) {
   if (!svp::attn_sizes_ok(B, T, num_heads, num_kv_heads, head_dim)) return 0;
-  return 256;
+  return svp::tc_layout(B, T, num_heads / num_kv_heads, num_kv_heads, head_dim).total;
 }
 
 }  // extern "C"

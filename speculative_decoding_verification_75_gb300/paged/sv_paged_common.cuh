@@ -21,8 +21,8 @@ namespace svp {
 using sv::kFull;
 
 // Element tags.
-struct BF16 { using raw = __nv_bfloat16; static constexpr int kBytes = 2; };
-struct F16 { using raw = __half; static constexpr int kBytes = 2; };
+struct BF16 { using raw = __nv_bfloat16; static constexpr int kBytes = 2; static constexpr bool kIsBf16 = true; };
+struct F16 { using raw = __half; static constexpr int kBytes = 2; static constexpr bool kIsBf16 = false; };
 struct F32 { using raw = float; static constexpr int kBytes = 4; };
 struct E4M3 { using raw = uint8_t; static constexpr int kBytes = 1; };
 
