@@ -3,7 +3,7 @@
 //
 // Rows.  All n new tokens and the G query heads that share a KV head form one
 // matrix of n * G rows, row r = token r / G, head r % G, so that a key is read
-// once for all of them.  S = Q K^T and O = P V run as M = 128 row tiles with
+// once for all of them; a tile takes as many whole tokens as fit 128 rows.  S = Q K^T and O = P V run as M = 128 row tiles with
 // 128 keys a step; S and O live in tensor memory (TMEM: lane = row, one
 // thread per row), P overwrites half of its S as the 16-bit A operand.
 //
@@ -46,7 +46,7 @@ constexpr int kTile = 128;      // keys per step, rows per tile
 constexpr int kSegRing = 8;
 
 struct TcParams {
-  CUtensorMap kmap, vmap;
+  CUtensorMap kmap, vmap, qmap;
   AttnParams a;
   uint32_t *err;       // SV_FAULT_TIMEOUT goes here
   int32_t *head;       // [0] tiles per range
@@ -56,9 +56,11 @@ struct TcParams {
   int slot_rows;       // rows of a slot
   int slot_floats;
   int MP;              // row-tile groups per (request, head), at most
-  int box;             // rows of a TMA box
+  int box;             // rows of a TMA box of the cache
+  int TT;              // tokens of a row tile: its rows are TT * G <= 128
+  int qbox;            // tokens of a TMA box of the queries
   float c;             // |scale| * log2(e), at least 1e-30
-  int negate;          // scale < 0: Q's signs are flipped
+  int negate;          // scale < 0: the signs of S are flipped
 };
 
 // ------------------------------------------------------------- tcgen05 ----
@@ -77,6 +79,14 @@ __device__ __forceinline__ void tc_fence_before() {
 }
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// One lane of a converged warp, the same one each time.  (Selected this way the
+// descriptors stay in uniform registers; under `lane == 0` every product took
+// ~120 cycles to issue, twice its execution time.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred P; elect.sync _|P, 0xffffffff; selp.u32 %0, 1, 0, P; }" : "=r"(p));
+  return p != 0;
 }
 // Completion of every tcgen05.mma this thread has issued, on an mbarrier.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
@@ -126,16 +136,19 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r) {
       SVP_W8(r, 0), SVP_W8(r, 8), SVP_W8(r, 16), SVP_W8(r, 24)
       : "memory");
 }
-// The loaded registers are tied to the wait, so that no use moves before it.
-__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      SVP_W8(r, 0), SVP_W8(r, 8)
+      : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld2(uint32_t (&r)[64]) {
+// The loaded registers are tied to the wait, so that no use moves before it.
+template <int N>
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -226,18 +239,20 @@ struct Shape {
   static constexpr bool kRaw = C::kBytes == 1;      // e4m3: widened on chip
   static constexpr int kHalves = D / 64;
   static constexpr int kStageBytes = kTile * D * 2;
-  static constexpr int kQTiles = kPair ? 2 : 1;
-  static constexpr int kQBytes = kQTiles * kStageBytes;
+  // Q: one tile per stream, or one for both and room for the next segment's.
+  static constexpr int kQBufs = kPair ? 1 : 2;
+  static constexpr int kQBytes = 2 * kStageBytes;
   static constexpr int kRawData = kTile * D, kRawScale = kTile * (D / SV_KV_GROUP);
   static constexpr int kRawBytes = kRawData + kRawScale;
   // Ring sizes: as many stages as 227 KB hold (about 200 KB where tiles are
   // small); raw stages first, they are what is in flight.
-  static constexpr int kStages = kRaw ? 3 : D == 128 ? (kPair ? 5 : 6) : (kPair ? 11 : 12);
-  static constexpr int kRawStages = kRaw ? (D == 128 ? (kPair ? 3 : 5) : 10) : 0;
-  static constexpr int kHelpers = kRaw ? 4 : 2;     // warps
+  static constexpr int kStages = kRaw ? 3 : D == 128 ? 5 : 11;
+  static constexpr int kRawStages = kRaw ? (D == 128 ? 3 : 10) : 0;
+  static constexpr int kHelpers = kRaw ? 6 : 2;     // warps: 3 or 4 per scheduler in all
   static constexpr int kWarps = 10 + kHelpers;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kRows = kPair ? 256 : 128;   // rows of a unit
+  static constexpr int kChunk = kRaw ? 32 : 64;     // S columns in registers at once
+  static constexpr int kTilesPerUnit = kPair ? 2 : 1;
   static constexpr int kSmem = kQBytes + kStages * kStageBytes + kRawStages * kRawBytes;
 };
 
@@ -247,26 +262,39 @@ constexpr uint32_t kPOff = 64;              // P in the upper half of its S
 
 struct Bars {
   uint64_t full[12], empty[12], fixed[12], rfull[10], rempty[10];
-  uint64_t s_full[2], p_ready[2], o_done[2], q_ready, drain;
+  uint64_t s_full[2], p_ready[2], o_done[2], q_full[2], q_empty[2], drain;
 };
 
 // ----------------------------------------------------------------- work ----
 
 struct Req {
-  int L, n, rows, mp, kv_end, kt, weight;
+  int L, n, mp, kv_end, kt, weight;
 };
 
-// Tiles of a request: its units (KV head, row-tile group) times its key tiles.
-__device__ __forceinline__ Req request(const AttnParams &p, int rows_per_unit, int b, uint32_t &st) {
+// Tiles of a request: its units (KV head, group of row tiles) times its key
+// tiles.  upt: new tokens of a unit.
+__device__ __forceinline__ Req make_request(const AttnParams &p, int upt, int L, int n) {
   Req r;
-  lengths(p.bt, b, r.L, r.n, st);
-  r.rows = r.n * p.G;
-  r.mp = (r.rows + rows_per_unit - 1) / rows_per_unit;
-  r.kv_end = min(r.L + r.n, p.c.max_blocks * p.c.bs);
+  r.L = L;
+  r.n = n;
+  r.mp = (n + upt - 1) / upt;
+  r.kv_end = min(L + n, p.c.max_blocks * p.c.bs);
   r.kt = max(1, (r.kv_end + kTile - 1) / kTile);
   r.weight = p.c.heads * r.mp * r.kt;
   return r;
 }
+__device__ __forceinline__ Req request(const AttnParams &p, int upt, int b, uint32_t &st) {
+  int L, n;
+  lengths(p.bt, b, L, n, st);
+  return make_request(p, upt, L, n);
+}
+
+// Lengths of the requests from a range's first one on, in shared memory.
+constexpr int kReqCache = 32;
+struct ReqCache {
+  int b0;
+  int2 len[kReqCache];
+};
 
 // A run of key tiles [t0, t1) of one unit.
 struct Seg {
@@ -279,16 +307,24 @@ struct Walk {
   int b, unit, tile, left;
   Req r;
 
-  __device__ __forceinline__ void start(const AttnParams &p, int rpu, int b0, int rem, int count) {
+  __device__ __forceinline__ Req fetch(const AttnParams &p, int upt, const ReqCache &rc) const {
+    if (b - rc.b0 < kReqCache) {
+      const int2 v = rc.len[b - rc.b0];
+      return make_request(p, upt, v.x, v.y);
+    }
     uint32_t st = 0;
-    b = b0;
+    return request(p, upt, b, st);
+  }
+  __device__ __forceinline__ void start(const AttnParams &p, int upt, const ReqCache &rc, int rem,
+                                        int count) {
     left = count;
     if (left <= 0) return;
-    r = request(p, rpu, b, st);
+    b = rc.b0;
+    r = fetch(p, upt, rc);
     unit = rem / r.kt;
     tile = rem - unit * r.kt;
   }
-  __device__ __forceinline__ bool next(const AttnParams &p, int rpu, Seg &s) {
+  __device__ __forceinline__ bool next(const AttnParams &p, int upt, const ReqCache &rc, Seg &s) {
     if (left <= 0) return false;
     s.b = b;
     s.r = r;
@@ -304,10 +340,9 @@ struct Walk {
       if (++unit == p.c.heads * r.mp) {
         unit = 0;
         if (left > 0) {
-          uint32_t st = 0;
           do {
             ++b;
-            r = request(p, rpu, b, st);
+            r = fetch(p, upt, rc);
           } while (r.weight == 0);
         }
       }
@@ -336,7 +371,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];   // swizzle atoms: 1024 bytes
   __shared__ Bars bars;
   __shared__ uint32_t tmem_slot;
-  __shared__ int sh_start[2];                 // request and offset of this range
+  __shared__ ReqCache rc;                     // rc.b0: the range's first request
+  __shared__ int sh_rem;                      // tiles of it before the range
   __shared__ int sh_scan[S::kWarps + 1];
   __shared__ int seg_bad[kSegRing];
   __shared__ int failed;                      // a softmax warp's wait gave up
@@ -366,8 +402,9 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       sv::mbar_init(sv::smem_addr(&bars.s_full[s]), 1);
       sv::mbar_init(sv::smem_addr(&bars.p_ready[s]), 4);
       sv::mbar_init(sv::smem_addr(&bars.o_done[s]), 1);
+      sv::mbar_init(sv::smem_addr(&bars.q_full[s]), 1);
+      sv::mbar_init(sv::smem_addr(&bars.q_empty[s]), 1);
     }
-    sv::mbar_init(sv::smem_addr(&bars.q_ready), 8);
     sv::mbar_init(sv::smem_addr(&bars.drain), 1);
     for (int i = 0; i < kSegRing; ++i) seg_bad[i] = 0;
     failed = 0;
@@ -376,40 +413,30 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   if (tid == 32) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.kmap) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.vmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.qmap) : "memory");
   }
   const AttnParams &a = p.a;
   const int B = a.bt.B;
   sv::pdl_wait();
   sv::pdl_launch_dependents();
 
-  // This block's range of the tile sequence.
-  int total = 0;
-  for (int c = 0; c < B; c += S::kThreads) {
-    uint32_t st = 0;
-    const int b = c + tid;
-    total += b < B ? request(a, S::kRows, b, st).weight : 0;
-    if (blockIdx.x == 0) report(a.bt.status, st);
-  }
-  total = __reduce_add_sync(kFull, total);
-  if (lane == 0) sh_scan[warp] = total;
-  __syncthreads();
-  total = 0;
-  for (int w = 0; w < S::kWarps; ++w) total += sh_scan[w];
-  const int quota = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-  const int64_t begin64 = static_cast<int64_t>(blockIdx.x) * quota;
-  const int begin = begin64 < total ? static_cast<int>(begin64) : total;
-  const int count = min(quota, total - begin);
-  {
+  // This block's range of the tile sequence: all requests' tiles are summed
+  // and scanned by the block, in one go for up to kThreads requests.
+  const int upt = p.TT * S::kTilesPerUnit;
+  int total = 0, quota = 0, begin = 0, count = 0;
+  const bool once = B <= S::kThreads;
+  for (int pass = once ? 1 : 0; pass < 2; ++pass) {
     int base = 0;
     for (int c = 0; c < B; c += S::kThreads) {
       uint32_t st = 0;
       const int b = c + tid;
-      const int w = b < B ? request(a, S::kRows, b, st).weight : 0;
+      const int w = b < B ? request(a, upt, b, st).weight : 0;
+      if (blockIdx.x == 0 && pass == 1) report(a.bt.status, st);
       int incl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += t;
+        const int v = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += v;
       }
       __syncthreads();
       if (lane == 31) sh_scan[warp] = incl;
@@ -419,25 +446,36 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         if (k < warp) before += sh_scan[k];
         all += sh_scan[k];
       }
-      const int excl = before + incl - w;
-      if (w > 0 && begin >= excl && begin < excl + w) {
-        sh_start[0] = b;
-        sh_start[1] = begin - excl;
-      }
-      if (blockIdx.x == 0 && b < B) p.pre[b] = excl;
       base += all;
+      if (once) total = all;
+      if (pass == 1) {
+        quota = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+        begin = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * quota, static_cast<int64_t>(total)));
+        const int excl = before + incl - w;
+        if (w > 0 && begin >= excl && begin < excl + w) {
+          rc.b0 = b;
+          sh_rem = begin - excl;
+        }
+        if (blockIdx.x == 0 && b < B) p.pre[b] = excl;
+      }
     }
-    if (blockIdx.x == 0 && tid == 0) {
-      p.pre[B] = total;
-      p.head[0] = quota;
-    }
+    if (pass == 0) total = base;
+  }
+  count = min(quota, total - begin);
+  if (blockIdx.x == 0 && tid == 0) p.head[0] = quota;
+  __syncthreads();
+  if (count > 0 && tid < kReqCache && rc.b0 + tid < B) {
+    uint32_t st = 0;
+    int L, n;
+    lengths(a.bt, rc.b0 + tid, L, n, st);
+    rc.len[tid] = make_int2(L, n);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   Walk walk;
-  walk.start(a, S::kRows, count > 0 ? sh_start[0] : 0, count > 0 ? sh_start[1] : 0, count);
+  walk.start(a, upt, rc, count > 0 ? sh_rem : 0, count);
   uint32_t *const err = p.err;
   Seg sg;
   bool ok = true;
@@ -451,102 +489,66 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const int my = wq * 32 + lane;           // row of the 128-row tile
     uint32_t ph_s = 0, ph_o = 0;
     int seg = 0;
-    for (; ok && walk.next(a, S::kRows, sg); ++seg) {
+    for (; ok && walk.next(a, upt, rc, sg); ++seg) {
       const Req &r = sg.r;
       const int nt = sg.t1 - sg.t0, nsteps = steps_of<kPair>(nt, s);
-      const int m0 = sg.mp * S::kRows;                       // first row of the unit
-      const int rows = min(S::kRows, r.rows - m0);           // rows of the unit
-      const int base_row = kPair ? s * kTile : 0;
-      const int tile_rows = min(max(rows - base_row, 0), kTile);
-      // Q: the tile's rows, 16 bytes at a time, into the swizzled layout.
-      {
-        const int lt = kPair ? tid & 127 : tid;
-        const int nthr = kPair ? 128 : 256;
-        uint8_t *dst = sq + (kPair ? s * S::kStageBytes : 0);
-        const uint8_t *qb = a.q + sg.b * a.qsb + static_cast<int64_t>(sg.h) * a.G * a.qsh;
-        const uint32_t flip = p.negate ? 0x80008000u : 0u;
-        for (int i = lt; i < tile_rows * (D / 8); i += nthr) {
-          const int row = i / (D / 8), ch = i % (D / 8);
-          const int rr = m0 + base_row + row, t = rr / a.G, g = rr - t * a.G;
-          const uint8_t *src = qb + t * a.qst + g * a.qsh + ch * 16;
-          uint4 w;
-          if (a.qvec) {
-            w = ld128(src);
-          } else {
-            uint32_t u[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) u[k] = ld16(src + 4 * k) | (ld16(src + 4 * k + 2) << 16);
-            w = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-          w.x ^= flip;
-          w.y ^= flip;
-          w.z ^= flip;
-          w.w ^= flip;
-          *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kTile * 128) + row * 128 +
-                                     (((ch & 7) ^ (row & 7)) << 4)) = w;
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) sv::mbar_arrive(sv::smem_addr(&bars.q_ready));
-      }
-      // Blocks that are not there: the unit is recomputed.
-      {
-        uint32_t st = r.kv_end < r.L + r.n ? SV_KV_TABLE_SHORT : 0u;
-        const int lo = sg.t0 * kTile / a.c.bs;
-        const int hi = (min(sg.t1 * kTile, r.kv_end) + a.c.bs - 1) / a.c.bs;
-        uint32_t bad = 0;
-        for (int j = lo + tid; j < hi; j += 256) {
-          const int id = ld32(a.c.tables + static_cast<size_t>(sg.b) * a.c.max_blocks + j);
-          if (id < 0 || id >= a.c.num_blocks) bad |= id == -1 ? SV_KV_MISSING_BLOCK : SV_KV_BAD_BLOCK;
-        }
-        if (bad) seg_bad[seg % kSegRing] = 1;
-        st |= bad;
-        if (st && (bad || tid == 0)) report(a.bt.status, st);
-      }
-
+      // Tokens and rows of this stream's tile.
+      const int tok0 = sg.mp * upt + (kPair ? s * p.TT : 0);
+      const int tile_rows = min(max(r.n - tok0, 0), p.TT) * a.G;
       const bool active = wq * 32 < tile_rows;               // warp-uniform
-      const int t_row = (m0 + base_row + min(my, max(tile_rows - 1, 0))) / a.G;
+      const int t_row = tok0 + min(my, max(tile_rows - 1, 0)) / a.G;
       const int full_end = min(r.L, r.kv_end);               // every row sees these
       const uint8_t *mrow = a.mask ? a.mask + sg.b * a.msb + static_cast<int64_t>(t_row) * a.bt.T : nullptr;
       float m_ref = -INFINITY, mc = 0.f, l = 0.f;            // mc = m_ref * c, 0 before a key is seen
       for (int j = 0; j < nsteps; ++j) {
+        // Which of the tile's keys the row sees, while S is being computed.
+        const int k0 = (sg.t0 + (kPair ? j : 2 * j + s)) * kTile;
+        const bool masked = k0 + kTile > full_end;
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+        if (masked && active) {
+          const int lim = min(r.kv_end, mrow ? r.L : r.L + t_row + 1) - k0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int n = min(max(lim - 32 * w, 0), 32);
+            vis[w] = n == 32 ? ~0u : (1u << n) - 1u;
+          }
+          if (mrow) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int c0 = max(max(r.L - k0, 0), 32 * w), c1 = min(min(r.kv_end - k0, kTile), 32 * w + 32);
+#pragma unroll 8
+              for (int c = c0; c < c1; ++c)
+                vis[w] |= (ld8(mrow + (k0 + c - r.L)) ? 1u : 0u) << (c & 31);
+            }
+          }
+        }
         if (!(ok = wait_warp(&bars.s_full[s], ph_s++, err))) break;
         if (active) {
           tc_fence_after();
-          const int k0 = (sg.t0 + (kPair ? j : 2 * j + s)) * kTile;
-          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-          const bool masked = k0 + kTile > full_end;
-          if (masked) {
-            const int lim = min(r.kv_end, mrow ? r.L : r.L + t_row + 1) - k0;
+          // A chunk of S; the last one of the first pass stays in registers.
+          constexpr int W = S::kChunk;
+          uint32_t x[W];
+          const auto load_s = [&](int ch) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int n = min(max(lim - 32 * w, 0), 32);
-              vis[w] = n == 32 ? ~0u : (1u << n) - 1u;
+            for (int k = 0; k < W; k += 32) tc_ld32(col_s + ch * W + k, x + k);
+            tc_wait_ld(x);
+            if (p.negate) {
+#pragma unroll
+              for (int k = 0; k < W; ++k) x[k] ^= 0x80000000u;
             }
-            if (mrow) {
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                const int c0 = max(max(r.L - k0, 0), 32 * w), c1 = min(min(r.kv_end - k0, kTile), 32 * w + 32);
-                for (int c = c0; c < c1; ++c)
-                  if (ld8(mrow + (k0 + c - r.L))) vis[w] |= 1u << (c & 31);
-              }
-            }
-          }
-          uint32_t x[64];
-          float mt = -INFINITY;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            tc_ld32(col_s + 64u * half, x);
-            tc_ld32(col_s + 64u * half + 32u, x + 32);
-            tc_wait_ld2(x);
             if (masked) {
 #pragma unroll
-              for (int k = 0; k < 64; ++k)
-                if (!((vis[2 * half + (k >> 5)] >> (k & 31)) & 1u)) x[k] = 0xff800000u;
+              for (int k = 0; k < W; ++k)
+                if (!((vis[(ch * W + k) >> 5] >> (k & 31)) & 1u)) x[k] = 0xff800000u;
             }
+          };
+          float mt = -INFINITY;
+#pragma unroll
+          for (int ch = 0; ch < kTile / W; ++ch) {
+            load_s(ch);
             float q0 = -INFINITY, q1 = -INFINITY, q2 = -INFINITY, q3 = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 64; k += 4) {
+            for (int k = 0; k < W; k += 4) {
               q0 = fmaxf(q0, __uint_as_float(x[k]));
               q1 = fmaxf(q1, __uint_as_float(x[k + 1]));
               q2 = fmaxf(q2, __uint_as_float(x[k + 2]));
@@ -580,23 +582,14 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           }
           const uint64_t c2 = f2_pack(p.c, p.c), nm2 = f2_pack(-mc, -mc);
           uint64_t l2a = 0, l2b = 0;
-          // The upper half first: it is in registers, and P's columns are
-          // the upper half of S.
+          // The last chunk first: it is in registers, and P's columns are the
+          // upper half of S, where a chunk's P covers only S already taken.
 #pragma unroll
-          for (int half = 1; half >= 0; --half) {
-            if (half == 0) {
-              tc_ld32(col_s, x);
-              tc_ld32(col_s + 32u, x + 32);
-              tc_wait_ld2(x);
-              if (masked) {
+          for (int ch = kTile / W - 1; ch >= 0; --ch) {
+            if (ch < kTile / W - 1) load_s(ch);
+            uint32_t pk[W / 2];
 #pragma unroll
-                for (int k = 0; k < 64; ++k)
-                  if (!((vis[k >> 5] >> (k & 31)) & 1u)) x[k] = 0xff800000u;
-              }
-            }
-            uint32_t pk[32];
-#pragma unroll
-            for (int k = 0; k < 64; k += 2) {
+            for (int k = 0; k < W; k += 2) {
               const uint64_t y =
                   f2_fma(f2_pack(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, nm2);
               float y0, y1;
@@ -607,7 +600,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
               else l2b = f2_add(l2b, f2_pack(y0, y1));
               pk[k >> 1] = pack2<Q>(y0, y1);
             }
-            tc_st32(col_s + kPOff + 32u * half, pk);
+            if constexpr (W == 64) tc_st32(col_s + kPOff + ch * (W / 2), pk);
+            else tc_st16(col_s + kPOff + ch * (W / 2), pk);
           }
           float e0, e1, e2, e3;
           f2_unpack(l2a, e0, e1);
@@ -639,13 +633,14 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         f1 = sv::ex2(a1 - mb);
         lsum = sh_l[0][my] * f0 + sh_l[1][my] * f1;
       }
+      const int base_row = kPair ? s * kTile : 0;            // of the slot
       const bool two = !kPair && nt > 1;
       const bool mine = my < tile_rows;
       float *slot = nullptr;
       uint8_t *orow = nullptr;
       float inv = 1.f;
       if (whole) {
-        const int rr = m0 + base_row + my, t = rr / a.G, g = rr - t * a.G;
+        const int t = tok0 + my / a.G, g = my % a.G;
         const int64_t row = (static_cast<int64_t>(sg.b) * a.bt.T + t) * a.Hq + sg.h * a.G + g;
         orow = a.out + row * (D * 2);
         inv = lsum == 0.f ? 0.f : 1.f / lsum;
@@ -715,13 +710,39 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     constexpr int kRing = S::kRaw ? S::kRawStages : S::kStages;
     uint64_t *const fullb = S::kRaw ? bars.rfull : bars.full;
     uint64_t *const emptyb = S::kRaw ? bars.rempty : bars.empty;
-    int it = 0;
-    // Block and row of this lane's box in a tile; -2 behind the last token.
+    int it = 0, seg = 0, q_issued = 0;
+    // Block of this lane's box in a tile; -2 behind the last token.  A block
+    // that is not there marks the segment, whose unit is recomputed; any block
+    // is loaded in its place.
     auto lookup = [&](const Seg &g, int tile) {
       const int pos = tile * kTile + bi * p.box;
       if (!lane_on || tile >= g.t1 || pos >= g.r.kv_end) return -2;
-      const int id = ld32(a.c.tables + static_cast<size_t>(g.b) * a.c.max_blocks + pos / a.c.bs);
-      return id < 0 || id >= a.c.num_blocks ? 0 : id;    // the softmax warps report it
+      int id = ld32(a.c.tables + static_cast<size_t>(g.b) * a.c.max_blocks + pos / a.c.bs);
+      if (id < 0 || id >= a.c.num_blocks) {
+        report(a.bt.status, id == -1 ? SV_KV_MISSING_BLOCK : SV_KV_BAD_BLOCK);
+        seg_bad[seg % kSegRing] = 1;
+        id = 0;
+      }
+      return id;
+    };
+    // A segment's queries: whole tokens, G heads each, in the swizzled layout.
+    auto load_q = [&](const Seg &g) {
+      const int qb = seg % S::kQBufs, use = seg / S::kQBufs;
+      if (use > 0 && !wait_warp(&bars.q_empty[qb], (use - 1) & 1, err)) return false;
+      const uint32_t bar = sv::smem_addr(&bars.q_full[qb]);
+      const uint32_t bytes = S::kTilesPerUnit * S::kHalves * p.qbox * a.G * 128;
+      if (elect_one()) {
+        sv::mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+        for (int i = 0; i < S::kTilesPerUnit; ++i)
+#pragma unroll
+          for (int hf = 0; hf < S::kHalves; ++hf)
+            tma_4d(sv::smem_addr(sq) + (kPair ? i : qb) * S::kStageBytes + hf * (kTile * 128), &p.qmap,
+                   hf * 64, g.h * a.G, g.mp * upt + i * p.TT, g.b, bar);
+      }
+      __syncwarp();
+      ++q_issued;
+      return true;
     };
     auto load = [&](const Seg &g, int tile, int id, bool is_v) {
       const int st = it % kRing;
@@ -750,13 +771,17 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       ++it;
       return true;
     };
-    while (ok && walk.next(a, S::kRows, sg)) {
+    for (; ok && walk.next(a, upt, rc, sg); ++seg) {
+      if (lane == 0 && sg.r.kv_end < sg.r.L + sg.r.n) report(a.bt.status, SV_KV_TABLE_SHORT);
       int id = lookup(sg, sg.t0), before = -2;
+      if (!kPair) ok = load_q(sg);
       for (int t = sg.t0; ok && t < sg.t1; ++t) {
         const int next = lookup(sg, t + 1);
         ok = load(sg, t, id, false);
         if (kPair) {
           ok = ok && load(sg, t, id, true);
+          // One buffer: the first tiles are on their way before it is free.
+          if (t == sg.t0) ok = ok && load_q(sg);
         } else {
           if (t > sg.t0) ok = ok && load(sg, t - 1, before, true);
           before = id;
@@ -765,14 +790,18 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       }
       if (!kPair) ok = ok && load(sg, sg.t1 - 1, before, true);
     }
-    if (!ok)  // every copy in flight lands before the block ends
+    if (!ok) {  // every copy in flight lands before the block ends
       for (int k = max(0, it - kRing); k < it; ++k) wait_warp(&fullb[k % kRing], (k / kRing) & 1, err);
+      for (int k = max(0, seg - S::kQBufs); k <= seg; ++k)
+        if (q_issued > k) wait_warp(&bars.q_full[k % S::kQBufs], (k / S::kQBufs) & 1, err);
+    }
   } else if (warp == 9) {
     // --------------------------------------------------------------- MMA ----
     constexpr uint32_t kQK = mma_desc<Q>(kTile, false), kPV = mma_desc<Q>(D, true);
-    const uint32_t q_addr = sv::smem_addr(sq), ring_addr = sv::smem_addr(ring);
-    int it = 0;                    // stages taken, in load order
-    uint32_t ph_p[2] = {0, 0}, ph_q = 0, fix = 0;  // fix: per stage, parity of its repairs
+    const uint64_t q_desc = smem_desc(sv::smem_addr(sq), 16), k_desc = smem_desc(sv::smem_addr(ring), 16);
+    const uint64_t v_desc = smem_desc(sv::smem_addr(ring), kTile * 128);
+    int it = 0, seg = 0;           // stages taken, in load order
+    uint32_t ph_p[2] = {0, 0}, fix = 0;  // fix: per stage, parity of its repairs
     auto take = [&](int k0, int full_end, bool is_v) {
       const int st = it % S::kStages;
       bool good = wait_warp(&bars.full[st], (it / S::kStages) & 1, err);
@@ -784,38 +813,39 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       return good;
     };
     auto release = [&]() {
-      if (lane == 0) tc_commit(sv::smem_addr(&bars.empty[it % S::kStages]));
+      if (elect_one()) tc_commit(sv::smem_addr(&bars.empty[it % S::kStages]));
       ++it;
     };
     auto qk = [&](int s) {
-      if (lane == 0) {
-        const uint32_t qa = q_addr + (kPair ? s * S::kStageBytes : 0);
-        const uint32_t ka = ring_addr + (it % S::kStages) * S::kStageBytes;
+      const uint64_t qd = q_desc + (kPair ? s : seg % S::kQBufs) * (S::kStageBytes >> 4);
+      const uint64_t kd = k_desc + (it % S::kStages) * (S::kStageBytes >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * (kTile * 128) + (k & 3) * 32;
-          tc_mma_ss(tmem + kColS + 128u * s, smem_desc(qa + off, 16), smem_desc(ka + off, 16), kQK, k > 0);
+          const uint32_t off = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
+          tc_mma_ss(tmem + kColS + 128u * s, qd + off, kd + off, kQK, k > 0);
         }
       }
       __syncwarp();
     };
     auto pv = [&](int s, bool first) {
-      if (lane == 0) {
-        const uint32_t va = ring_addr + (it % S::kStages) * S::kStageBytes;
+      const uint64_t vd = v_desc + (it % S::kStages) * (S::kStageBytes >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           tc_mma_ts(tmem + kColO + 128u * s, tmem + kColS + 128u * s + kPOff + 8u * k,
-                    smem_desc(va + k * 2048, kTile * 128), kPV, !first || k > 0);
+                    vd + k * (2048 >> 4), kPV, !first || k > 0);
       }
       __syncwarp();
     };
     auto commit = [&](uint64_t *bar) {
-      if (lane == 0) tc_commit(sv::smem_addr(bar));
+      if (elect_one()) tc_commit(sv::smem_addr(bar));
     };
-    while (ok && walk.next(a, S::kRows, sg)) {
+    for (; ok && walk.next(a, upt, rc, sg); ++seg) {
       const int nt = sg.t1 - sg.t0, full_end = min(sg.r.L, sg.r.kv_end);
       const auto key0 = [&](int t) { return (sg.t0 + t) * kTile; };
-      if (!(ok = wait_warp(&bars.q_ready, ph_q++, err))) break;
+      uint64_t *const q_free = &bars.q_empty[seg % S::kQBufs];
+      if (!(ok = wait_warp(&bars.q_full[seg % S::kQBufs], seg / S::kQBufs, err))) break;
       tc_fence_after();
       if (kPair) {
         // Stages in order K0 V0 K1 V1 ...
@@ -825,6 +855,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         qk(1);
         commit(&bars.s_full[1]);
         release();
+        if (nt == 1) commit(q_free);
         for (int t = 0; ok && t < nt; ++t) {
           ok = wait_warp(&bars.p_ready[0], ph_p[0]++, err) && take(key0(t), full_end, true);
           if (!ok) break;
@@ -852,6 +883,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             qk(1);
             commit(&bars.s_full[1]);
             release();                               // K
+            if (t + 2 == nt) commit(q_free);
           }
         }
       } else {
@@ -862,6 +894,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           commit(&bars.s_full[t]);
           release();
         }
+        if (ok && nt <= 2) commit(q_free);
         for (int t = 0; ok && t < nt; ++t) {
           const int s = t & 1;
           ok = wait_warp(&bars.p_ready[s], ph_p[s]++, err) && take(key0(t), full_end, true);
@@ -874,6 +907,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             qk(s);
             commit(&bars.s_full[s]);
             release();
+            if (t + 3 == nt) commit(q_free);
           } else {
             commit(&bars.o_done[s]);
           }
@@ -881,7 +915,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       }
     }
     if (!ok) {  // issued products end before TMEM is freed
-      if (lane == 0) tc_commit(sv::smem_addr(&bars.drain));
+      if (elect_one()) tc_commit(sv::smem_addr(&bars.drain));
       __syncwarp();
       wait_warp(&bars.drain, 0, err);
     }
@@ -991,7 +1025,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       ++it;
       return true;
     };
-    for (; ok && walk.next(a, S::kRows, sg); ++seg) {
+    for (; ok && walk.next(a, upt, rc, sg); ++seg) {
       for (int t = sg.t0; ok && t < sg.t1; ++t) {
         ok = stage(sg, t, false);
         if (kPair) ok = ok && stage(sg, t, true);
@@ -1015,7 +1049,6 @@ constexpr int kJoinThreads = 256;
 // ones.  Grid: (units, parts of a unit's rows x D / 4 columns).
 template <typename Q, typename C, int D, bool kPair>
 __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid_constant__ TcParams p) {
-  constexpr int kRows = kPair ? 256 : 128;
   __shared__ float qs[kJoinThreads / 32][D];
   const AttnParams &a = p.a;
   const int per_b = a.c.heads * p.MP;
@@ -1023,9 +1056,10 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
   sv::pdl_wait();
   sv::pdl_launch_dependents();
   uint32_t st = 0;
-  const Req r = request(a, kRows, b, st);
+  const int upt = p.TT * (kPair ? 2 : 1);
+  const Req r = request(a, upt, b, st);
   if (mp >= r.mp) return;
-  const int rows = min(kRows, r.rows - mp * kRows);
+  const int tok0 = mp * upt, rows = min(upt, r.n - tok0) * a.G;
   const int quota = ld32(p.head), start = ld32(p.pre + b) + (h * r.mp + mp) * r.kt;
   const int c0 = start / quota, c1 = (start + r.kt - 1) / quota;
   auto slot_of = [&](int c) {
@@ -1040,14 +1074,14 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
       bad |= ld32(reinterpret_cast<const int32_t *>(slot_of(c)) + (D + 2) * p.slot_rows);
   }
   const auto out_row = [&](int row) {
-    const int rr = mp * kRows + row, t = rr / a.G, g = rr - t * a.G;
+    const int t = tok0 + row / a.G, g = row % a.G;
     return (static_cast<int64_t>(b) * a.bt.T + t) * a.Hq + h * a.G + g;
   };
   if (bad) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < rows;
          row += gridDim.y * (kJoinThreads / 32)) {
-      const int rr = mp * kRows + row, t = rr / a.G, g = rr - t * a.G;
+      const int t = tok0 + row / a.G, g = row % a.G;
       const uint8_t *q = a.q + b * a.qsb + t * a.qst + static_cast<int64_t>(h * a.G + g) * a.qsh;
       __syncwarp();
       for (int d = lane; d < D; d += 32) {
@@ -1069,17 +1103,19 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
   const int i = blockIdx.y * kJoinThreads + threadIdx.x;
   if (i >= rows * (D / 4)) return;
   const int row = i % rows, d4 = i / rows;
+  // Rows of the second tile start at row 128 of a slot.
+  const int tile_rows = p.TT * a.G, srow = row < tile_rows ? row : kTile + row - tile_rows;
   float m = -INFINITY;
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(slot_of(c) + D * p.slot_rows + row));
+  for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(slot_of(c) + D * p.slot_rows + srow));
   const float mb = m == -INFINITY ? 0.f : m;
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int c = c0; c <= c1; ++c) {
     const float *s = slot_of(c);
-    const float f = sv::ex2(__ldcg(s + D * p.slot_rows + row) - mb);
-    l += __ldcg(s + (D + 1) * p.slot_rows + row) * f;
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(s) + static_cast<size_t>(d4) * p.slot_rows + row);
+    const float f = sv::ex2(__ldcg(s + D * p.slot_rows + srow) - mb);
+    l += __ldcg(s + (D + 1) * p.slot_rows + srow) * f;
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(s) + static_cast<size_t>(d4) * p.slot_rows + srow);
     o.x += v.x * f;
     o.y += v.y * f;
     o.z += v.z * f;

@@ -251,19 +251,40 @@ bool make_map(CUtensorMap &m, const Cache &c, const void *base, int64_t dtype, i
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as [request][token][head][element]; boxes of `tokens` tokens of
+// the G heads that share a KV head, 64 elements wide.
+bool make_query_map(CUtensorMap &m, const AttnParams &p, int64_t dtype, int tokens) {
+  const EncodeTiled enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.c.D), static_cast<cuuint64_t>(p.Hq),
+                              static_cast<cuuint64_t>(p.bt.T), static_cast<cuuint64_t>(p.bt.B)};
+  const cuuint64_t row = p.c.D * 2;  // stands for strides that are never used
+  const cuuint64_t strides[3] = {p.Hq > 1 ? static_cast<cuuint64_t>(p.qsh) : row,
+                                 p.bt.T > 1 ? static_cast<cuuint64_t>(p.qst) : row,
+                                 p.bt.B > 1 ? static_cast<cuuint64_t>(p.qsb) : row};
+  const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(tokens), 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return enc(&m, dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<uint8_t *>(p.q), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Workspace of the tensor-core path.
 struct TcLayout {
   size_t head, pre, dirty, slots, total;
-  int MP, slot_rows, slot_floats;
+  int TT, MP, slot_rows, slot_floats;
 };
 
 TcLayout tc_layout(int64_t B, int64_t T, int64_t G, int64_t heads, int64_t D) {
   const auto up = [](size_t x, size_t a) { return (x + a - 1) / a * a; };
   TcLayout w;
-  const int64_t rows = T * G;
-  const int64_t unit = rows > kTile ? 2 * kTile : kTile;
-  w.MP = static_cast<int>(std::max<int64_t>((rows + unit - 1) / unit, 1));
-  w.slot_rows = static_cast<int>(up(std::min<int64_t>(std::max<int64_t>(rows, 1), unit), 32));
+  w.TT = static_cast<int>(std::max<int64_t>(kTile / G, 1));  // tokens of a row tile
+  const bool pair = T > w.TT;
+  const int64_t unit = pair ? 2 * w.TT : w.TT;
+  w.MP = static_cast<int>(std::max<int64_t>((T + unit - 1) / unit, 1));
+  w.slot_rows = pair ? 2 * kTile
+                     : static_cast<int>(up(std::min<int64_t>(std::max<int64_t>(T * G, 1), kTile), 32));
   w.slot_floats = static_cast<int>(up((D + 2) * w.slot_rows + 1, 32));
   w.head = 0;
   w.pre = 256;
@@ -273,17 +294,18 @@ TcLayout tc_layout(int64_t B, int64_t T, int64_t G, int64_t heads, int64_t D) {
   return w;
 }
 
-// What the tensor-core kernel takes: whole 8-row swizzle atoms per page, 16-
-// bit tiles of the query's own type (an e4m3 code times its scale is a bf16
+// What the tensor-core kernel takes: whole 8-row swizzle atoms per page,
+// query rows on 16-byte boundaries and a token's heads within a tile, 16-bit
+// tiles of the query's own type (an e4m3 code times its scale is a bf16
 // number, but not always an fp16 one), sizes within TMA's and int32's.
 bool tc_takes(const sv_tree_attention_args *a, const AttnParams &p, const TcLayout &w) {
   if (p.c.D != 64 && p.c.D != 128) return false;
-  if (p.c.bs % 8 || p.c.num_blocks < 1) return false;
+  if (p.c.bs % 8 || p.c.num_blocks < 1 || p.G > kTile || !p.qvec) return false;
   if (a->cache.dtype == SV_E4M3 && (a->dtype != SV_BF16 || p.c.sblock_bytes % 16)) return false;
   if (p.c.block_bytes >= (int64_t{1} << 40)) return false;
   const int64_t tiles = std::max<int64_t>((static_cast<int64_t>(p.c.max_blocks) * p.c.bs + kTile - 1) / kTile, 1);
   const int64_t units = static_cast<int64_t>(p.bt.B) * p.c.heads * w.MP;
-  return units <= INT_MAX / tiles && static_cast<int64_t>(p.bt.T) * p.G <= INT_MAX / 2;
+  return units <= INT_MAX / tiles;
 }
 
 template <typename Q, typename C, int D, bool kPair>
@@ -300,7 +322,7 @@ sv_status tc_launch(const TcParams &p, int nsm, int dev, sv_stream_t stream) {
   const int grid = std::min(nsm, kMaxGrid);
   if (const sv_status s = launch(k, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, stream, p))
     return s;
-  const int rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.a.bt.T) * p.a.G, S::kRows));
+  const int rows = std::min(p.a.bt.T, p.TT * S::kTilesPerUnit) * p.a.G;
   const int64_t units = static_cast<int64_t>(p.a.bt.B) * p.a.c.heads * p.MP;
   return launch(sv_attn_join_kernel<Q, C, D, kPair>,
                 dim3(static_cast<unsigned>(units),
@@ -316,7 +338,7 @@ sv_status tc_pick(const TcParams &p, bool pair, int nsm, int dev, sv_stream_t st
 }
 
 sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const TcLayout &w,
-                  sv_stream_t stream) {
+                  sv_stream_t stream, bool *taken) {
   int dev = 0, nsm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -336,10 +358,13 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
   while (p.box < kTile && ap.c.bs % (2 * p.box) == 0) p.box *= 2;
   p.c = std::max(std::fabs(ap.scale_log2), 1e-30f);
   p.negate = ap.scale_log2 < 0.f;
-  if (!make_map(p.kmap, ap.c, ap.c.k, a->cache.dtype, p.box) ||
-      !make_map(p.vmap, ap.c, ap.c.v, a->cache.dtype, p.box))
-    return SV_ERR_CUDA;
-  const bool pair = static_cast<int64_t>(ap.bt.T) * ap.G > kTile;
+  p.TT = w.TT;
+  p.qbox = std::min(w.TT, ap.bt.T);
+  *taken = make_map(p.kmap, ap.c, ap.c.k, a->cache.dtype, p.box) &&
+           make_map(p.vmap, ap.c, ap.c.v, a->cache.dtype, p.box) &&
+           make_query_map(p.qmap, ap, a->dtype, p.qbox);
+  if (!*taken) return SV_OK;  // strides that no tensor map describes
+  const bool pair = ap.bt.T > w.TT;
   if (a->cache.dtype == SV_E4M3) return tc_pick<BF16, E4M3>(p, pair, nsm, dev, stream);
   return a->dtype == SV_BF16 ? tc_pick<BF16, BF16>(p, pair, nsm, dev, stream)
                              : tc_pick<F16, F16>(p, pair, nsm, dev, stream);
@@ -380,7 +405,11 @@ sv_status tree_attention(const sv_tree_attention_args *a, sv_stream_t stream) {
   p.Hq = static_cast<int>(a->num_heads);
   p.G = p.Hq / p.c.heads;
   const TcLayout w = tc_layout(a->B, a->T, p.G, p.c.heads, p.c.D);
-  if (tc_takes(a, p, w)) return attn_tc(a, p, w, stream);
+  if (tc_takes(a, p, w)) {
+    bool taken = false;
+    const sv_status s = attn_tc(a, p, w, stream, &taken);
+    if (taken || s != SV_OK) return s;
+  }
   return a->dtype == SV_BF16 ? attn_general<BF16>(a->cache.dtype, p, stream)
                              : attn_general<F16>(a->cache.dtype, p, stream);
 }
