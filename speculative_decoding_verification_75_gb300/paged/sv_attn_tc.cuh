@@ -7,19 +7,20 @@
 // 128 keys a step; S and O live in tensor memory (TMEM: lane = row, one
 // thread per row), P overwrites half of its S as the 16-bit A operand.
 //
-// Two streams of such steps alternate, each with a softmax warpgroup of its
-// own, so that the tensor cores work on one while the other takes
-// exponentials: with at most 128 rows both streams work on the same rows,
-// one on the even and one on the odd key tiles of the range, and are joined
-// in the end (kPair = false); with more, each has 128 rows of its own and
-// both use every key tile (kPair = true).
+// Two streams of such steps alternate in a thread block, each with a softmax
+// warpgroup of its own, so that the tensor cores work on one while the other
+// takes exponentials.  With at most 128 rows the streams are independent, each
+// with a range of work of its own (kPair = false): one goes on while the other
+// stores its rows and begins the next unit.  With more rows each has 128 of
+// the unit's and both use every key tile (kPair = true).
 //
 // Work.  The key tiles of all units (request, KV head, row tiles) form one
-// sequence that is cut into equal ranges, one per thread block (one block per
-// SM): ragged lengths are balanced to within a tile.  A unit cut by a range's
-// end leaves partial results (unnormalised O, row maximum and sum) in the
-// workspace, joined by the second kernel in range order, so results do not
-// depend on timing.  The lengths are read on the device; the host never waits.
+// sequence that is cut into equal ranges, one per stream or pair of streams of
+// one block per SM: ragged lengths are balanced to within a tile.  A unit cut
+// by a range's end leaves partial results (unnormalised O, row maximum and
+// sum) in the workspace, joined by the second kernel in range order, so
+// results do not depend on timing.  The lengths are read on the device; the
+// host never waits.
 //
 // Softmax.  One pass: a row keeps a reference m and sums 2^(x - m) in fp32.
 // O is rescaled only when a tile's maximum exceeds m by more than 2^8 (bf16
@@ -49,18 +50,20 @@ struct TcParams {
   CUtensorMap kmap, vmap, qmap;
   AttnParams a;
   uint32_t *err;       // SV_FAULT_TIMEOUT goes here
-  int32_t *head;       // [0] tiles per range
+  int32_t *head;       // [0] tiles of all ranges
   int32_t *pre;        // [B + 1] tiles before each request
   uint8_t *dirty;      // [B * heads * MP] units to recompute (whole ranges)
-  float *slots;        // [grid * 2] partial results
+  float *slots;        // [ranges * 2] partial results
+  int ranges;
   int slot_rows;       // rows of a slot
   int slot_floats;
   int MP;              // row-tile groups per (request, head), at most
   int box;             // rows of a TMA box of the cache
   int TT;              // tokens of a row tile: its rows are TT * G <= 128
   int qbox;            // tokens of a TMA box of the queries
+  int mvec;            // mask rows are whole 4-byte words
   float c;             // |scale| * log2(e), at least 1e-30
-  int negate;          // scale < 0: the signs of S are flipped
+  int negate;          // scale < 0: S is computed with Q's signs flipped
 };
 
 // ------------------------------------------------------------- tcgen05 ----
@@ -158,10 +161,6 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-__device__ __forceinline__ void named_bar(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // Shared-memory operand descriptor: 128-byte swizzle, 8-row groups 1024 bytes
 // apart; `lead`: distance of the next 64 elements along the contiguous
 // dimension where the operand is not K-major.
@@ -171,7 +170,8 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
 }
 
 // Instruction descriptor: fp32 accumulators, M = 128; b_mn: B's N runs
-// contiguously.
+// contiguously.  kNegateA: A's signs are flipped.
+constexpr uint32_t kNegateA = 1u << 13;
 template <typename Q>
 __device__ constexpr uint32_t mma_desc(int n, bool b_mn) {
   const uint32_t fmt = sizeof(Q) && Q::kBytes == 2 && Q::kIsBf16 ? 1u : 0u;
@@ -239,8 +239,7 @@ struct Shape {
   static constexpr bool kRaw = C::kBytes == 1;      // e4m3: widened on chip
   static constexpr int kHalves = D / 64;
   static constexpr int kStageBytes = kTile * D * 2;
-  // Q: one tile per stream, or one for both and room for the next segment's.
-  static constexpr int kQBufs = kPair ? 1 : 2;
+  static constexpr int kStreams = kPair ? 1 : 2;    // ranges of a block
   static constexpr int kQBytes = 2 * kStageBytes;
   static constexpr int kRawData = kTile * D, kRawScale = kTile * (D / SV_KV_GROUP);
   static constexpr int kRawBytes = kRawData + kRawScale;
@@ -262,7 +261,7 @@ constexpr uint32_t kPOff = 64;              // P in the upper half of its S
 
 struct Bars {
   uint64_t full[12], empty[12], fixed[12], rfull[10], rempty[10];
-  uint64_t s_full[2], p_ready[2], o_done[2], q_full[2], q_empty[2], drain;
+  uint64_t s_full[2], p_half[2], p_ready[2], o_done[2], q_full[2], q_empty[2], drain;
 };
 
 // ----------------------------------------------------------------- work ----
@@ -306,56 +305,95 @@ struct Seg {
 struct Walk {
   int b, unit, tile, left;
   Req r;
-
-  __device__ __forceinline__ Req fetch(const AttnParams &p, int upt, const ReqCache &rc) const {
-    if (b - rc.b0 < kReqCache) {
-      const int2 v = rc.len[b - rc.b0];
-      return make_request(p, upt, v.x, v.y);
-    }
-    uint32_t st = 0;
-    return request(p, upt, b, st);
-  }
-  __device__ __forceinline__ void start(const AttnParams &p, int upt, const ReqCache &rc, int rem,
-                                        int count) {
-    left = count;
-    if (left <= 0) return;
-    b = rc.b0;
-    r = fetch(p, upt, rc);
-    unit = rem / r.kt;
-    tile = rem - unit * r.kt;
-  }
-  __device__ __forceinline__ bool next(const AttnParams &p, int upt, const ReqCache &rc, Seg &s) {
-    if (left <= 0) return false;
-    s.b = b;
-    s.r = r;
-    s.unit = unit;
-    s.h = unit / r.mp;
-    s.mp = unit - s.h * r.mp;
-    s.t0 = tile;
-    s.t1 = min(r.kt, tile + left);
-    left -= s.t1 - s.t0;
-    tile = s.t1;
-    if (tile == r.kt) {
-      tile = 0;
-      if (++unit == p.c.heads * r.mp) {
-        unit = 0;
-        if (left > 0) {
-          do {
-            ++b;
-            r = fetch(p, upt, rc);
-          } while (r.weight == 0);
-        }
-      }
-    }
-    return true;
-  }
 };
 
-// Steps of a segment and stream: pair: every tile for both streams;
-// otherwise tile i for stream i & 1.
-template <bool kPair>
-__device__ __forceinline__ int steps_of(int nt, int s) {
-  return kPair ? nt : (nt + 1 - s) >> 1;
+__device__ __forceinline__ Req fetch_request(const AttnParams &p, int upt, const ReqCache &rc, int b) {
+  if (b - rc.b0 < kReqCache) {
+    const int2 v = rc.len[b - rc.b0];
+    return make_request(p, upt, v.x, v.y);
+  }
+  uint32_t st = 0;
+  return request(p, upt, b, st);
+}
+
+// The next segment of a walk, false at its end.  `rem` >= 0 begins the walk:
+// tiles of the first request before the range.  Not inlined: every role of the
+// kernel walks, and the copies together would not fit the instruction cache.
+__device__ __noinline__ bool walk_next(const AttnParams &p, int upt, const ReqCache &rc, Walk &w, Seg &s,
+                                       int rem) {
+  if (w.left <= 0) return false;
+  if (rem >= 0) {
+    w.b = rc.b0;
+    w.r = fetch_request(p, upt, rc, w.b);
+    w.unit = rem / w.r.kt;
+    w.tile = rem - w.unit * w.r.kt;
+  }
+  s.b = w.b;
+  s.r = w.r;
+  s.unit = w.unit;
+  s.h = w.unit / w.r.mp;
+  s.mp = w.unit - s.h * w.r.mp;
+  s.t0 = w.tile;
+  s.t1 = min(w.r.kt, w.tile + w.left);
+  w.left -= s.t1 - s.t0;
+  w.tile = s.t1;
+  if (w.tile == w.r.kt) {
+    w.tile = 0;
+    if (++w.unit == p.c.heads * w.r.mp) {
+      w.unit = 0;
+      if (w.left > 0) {
+        do {
+          ++w.b;
+          w.r = fetch_request(p, upt, rc, w.b);
+        } while (w.r.weight == 0);
+      }
+    }
+  }
+  return true;
+}
+
+// Range i of N <= total over `total` tiles is [start(i), start(i + 1)): none is
+// empty.  Range i belongs to stream i / gridDim.x of block i % gridDim.x, so
+// that few tiles spread over many blocks.
+__device__ __forceinline__ int range_start(int i, int N, int total) {
+  return static_cast<int>(static_cast<int64_t>(i) * total / N);
+}
+__device__ __forceinline__ int range_of(int tile, int N, int total) {
+  return static_cast<int>(((static_cast<int64_t>(tile) + 1) * N - 1) / total);
+}
+
+// A tile step of a walk: where it is and what the roles ask about it.
+struct Cursor {
+  int b, h, mp, t, t0, t1, seg, new0, kv_end;  // new0: keys that every row sees
+  bool on, cut;                                // cut: the table is too short
+
+  __device__ __forceinline__ bool first() const { return t == t0; }
+  __device__ __forceinline__ bool last() const { return t + 1 == t1; }
+};
+
+// begin: to the range's first tile, `rem` tiles into its first request.
+__device__ __forceinline__ void step_to(const AttnParams &p, int upt, const ReqCache &rc, Walk &w, Cursor &c,
+                                        bool begin, int rem) {
+  if (!begin && ++c.t < c.t1) return;
+  Seg s;
+  c.on = walk_next(p, upt, rc, w, s, begin ? rem : -1);
+  c.seg = begin ? 0 : c.seg + 1;
+  if (!c.on) return;
+  c.b = s.b;
+  c.h = s.h;
+  c.mp = s.mp;
+  c.t = c.t0 = s.t0;
+  c.t1 = s.t1;
+  c.kv_end = s.r.kv_end;
+  c.new0 = min(s.r.L, s.r.kv_end);
+  c.cut = s.r.kv_end < s.r.L + s.r.n;
+}
+
+template <typename T>
+__device__ __forceinline__ void swap2(T &a, T &b) {
+  const T c = a;
+  a = b;
+  b = c;
 }
 
 __device__ __forceinline__ bool wait_warp(const uint64_t *bar, uint32_t parity, uint32_t *err) {
@@ -371,12 +409,10 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];   // swizzle atoms: 1024 bytes
   __shared__ Bars bars;
   __shared__ uint32_t tmem_slot;
-  __shared__ ReqCache rc;                     // rc.b0: the range's first request
-  __shared__ int sh_rem;                      // tiles of it before the range
+  __shared__ ReqCache rc[S::kStreams];        // b0: the range's first request
+  __shared__ int sh_rem[S::kStreams];         // tiles of it before the range
   __shared__ int sh_scan[S::kWarps + 1];
-  __shared__ int seg_bad[kSegRing];
-  __shared__ int failed;                      // a softmax warp's wait gave up
-  __shared__ float sh_m[2][kTile], sh_l[2][kTile];
+  __shared__ int seg_bad[S::kStreams][kSegRing];  // holds 1 + a marked segment's number
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t *const sq = smem;
@@ -401,13 +437,16 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       sv::mbar_init(sv::smem_addr(&bars.s_full[s]), 1);
       sv::mbar_init(sv::smem_addr(&bars.p_ready[s]), 4);
+      sv::mbar_init(sv::smem_addr(&bars.p_half[s]), 4);
       sv::mbar_init(sv::smem_addr(&bars.o_done[s]), 1);
       sv::mbar_init(sv::smem_addr(&bars.q_full[s]), 1);
       sv::mbar_init(sv::smem_addr(&bars.q_empty[s]), 1);
     }
     sv::mbar_init(sv::smem_addr(&bars.drain), 1);
-    for (int i = 0; i < kSegRing; ++i) seg_bad[i] = 0;
-    failed = 0;
+    for (int s = 0; s < S::kStreams; ++s) {
+      for (int i = 0; i < kSegRing; ++i) seg_bad[s][i] = 0;
+      sh_rem[s] = 0;   // of a range without tiles
+    }
     sv::fence_mbar_init();
   }
   if (tid == 32) {
@@ -417,13 +456,19 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   }
   const AttnParams &a = p.a;
   const int B = a.bt.B;
+  if (warp == 2) {  // addresses only: the values may still be written
+    const int64_t at = static_cast<int64_t>(lane) * 32 < B ? lane * 32 : 0;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.bt.seq_lens + at));
+    if (a.bt.new_lens) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.bt.new_lens + at));
+    if (a.c.max_blocks > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.tables));
+  }
   sv::pdl_wait();
   sv::pdl_launch_dependents();
 
-  // This block's range of the tile sequence: all requests' tiles are summed
+  // This block's ranges of the tile sequence: all requests' tiles are summed
   // and scanned by the block, in one go for up to kThreads requests.
   const int upt = p.TT * S::kTilesPerUnit;
-  int total = 0, quota = 0, begin = 0, count = 0;
+  int total = 0, begin[S::kStreams], count[S::kStreams];
   const bool once = B <= S::kThreads;
   for (int pass = once ? 1 : 0; pass < 2; ++pass) {
     int base = 0;
@@ -449,36 +494,47 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       base += all;
       if (once) total = all;
       if (pass == 1) {
-        quota = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-        begin = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * quota, static_cast<int64_t>(total)));
-        const int excl = before + incl - w;
-        if (w > 0 && begin >= excl && begin < excl + w) {
-          rc.b0 = b;
-          sh_rem = begin - excl;
+        const int excl = before + incl - w, N = min(p.ranges, total);
+#pragma unroll
+        for (int s = 0; s < S::kStreams; ++s) {
+          const int i = static_cast<int>(blockIdx.x + s * gridDim.x);
+          begin[s] = i < N ? range_start(i, N, total) : total;
+          count[s] = i < N ? range_start(i + 1, N, total) - begin[s] : 0;
+          if (w > 0 && begin[s] >= excl && begin[s] < excl + w) {
+            rc[s].b0 = b;
+            sh_rem[s] = begin[s] - excl;
+          }
         }
         if (blockIdx.x == 0 && b < B) p.pre[b] = excl;
       }
     }
     if (pass == 0) total = base;
   }
-  count = min(quota, total - begin);
-  if (blockIdx.x == 0 && tid == 0) p.head[0] = quota;
+  if (blockIdx.x == 0 && tid == 0) p.head[0] = total;
   __syncthreads();
-  if (count > 0 && tid < kReqCache && rc.b0 + tid < B) {
-    uint32_t st = 0;
-    int L, n;
-    lengths(a.bt, rc.b0 + tid, L, n, st);
-    rc.len[tid] = make_int2(L, n);
+#pragma unroll
+  for (int s = 0; s < S::kStreams; ++s) {
+    const int i = tid - s * kReqCache;
+    if (count[s] > 0 && i >= 0 && i < kReqCache && rc[s].b0 + i < B) {
+      uint32_t st = 0;
+      int L, n;
+      lengths(a.bt, rc[s].b0 + i, L, n, st);
+      rc[s].len[i] = make_int2(L, n);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  Walk walk;
-  walk.start(a, upt, rc, count > 0 ? sh_rem : 0, count);
   uint32_t *const err = p.err;
-  Seg sg;
   bool ok = true;
+  Walk walk[S::kStreams];
+#pragma unroll
+  for (int s = 0; s < S::kStreams; ++s) walk[s].left = count[s];
+  // Steps to the next tile of a stream's range, or (begin) to its first.
+  const auto advance = [&](Cursor &c, int s, bool begin = false) {
+    step_to(a, upt, rc[s], walk[s], c, begin, sh_rem[s]);
+  };
 
   if (warp < 8) {
     // ------------------------------------------------ softmax warpgroups ----
@@ -487,11 +543,16 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t col_s = lanes + kColS + 128u * s, col_o = lanes + kColO + 128u * s;
     const int my = wq * 32 + lane;           // row of the 128-row tile
+    constexpr int kR = S::kStreams - 1;
+    const int rs = s & kR;                   // range of the block
     uint32_t ph_s = 0, ph_o = 0;
     int seg = 0;
-    for (; ok && walk.next(a, upt, rc, sg); ++seg) {
-      const Req &r = sg.r;
-      const int nt = sg.t1 - sg.t0, nsteps = steps_of<kPair>(nt, s);
+    for (; ok; ++seg) {
+      Seg next_seg;
+      if (!walk_next(a, upt, rc[rs], walk[rs], next_seg, seg == 0 ? sh_rem[rs] : -1)) break;
+      const Seg sg = next_seg;
+      const Req r = sg.r;
+      const int nt = sg.t1 - sg.t0;
       // Tokens and rows of this stream's tile.
       const int tok0 = sg.mp * upt + (kPair ? s * p.TT : 0);
       const int tile_rows = min(max(r.n - tok0, 0), p.TT) * a.G;
@@ -500,9 +561,9 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       const int full_end = min(r.L, r.kv_end);               // every row sees these
       const uint8_t *mrow = a.mask ? a.mask + sg.b * a.msb + static_cast<int64_t>(t_row) * a.bt.T : nullptr;
       float m_ref = -INFINITY, mc = 0.f, l = 0.f;            // mc = m_ref * c, 0 before a key is seen
-      for (int j = 0; j < nsteps; ++j) {
+      for (int j = 0; j < nt; ++j) {
         // Which of the tile's keys the row sees, while S is being computed.
-        const int k0 = (sg.t0 + (kPair ? j : 2 * j + s)) * kTile;
+        const int k0 = (sg.t0 + j) * kTile;
         const bool masked = k0 + kTile > full_end;
         uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
         if (masked && active) {
@@ -513,18 +574,59 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             vis[w] = n == 32 ? ~0u : (1u << n) - 1u;
           }
           if (mrow) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int c0 = max(max(r.L - k0, 0), 32 * w), c1 = min(min(r.kv_end - k0, kTile), 32 * w + 32);
-#pragma unroll 8
-              for (int c = c0; c < c1; ++c)
-                vis[w] |= (ld8(mrow + (k0 + c - r.L)) ? 1u : 0u) << (c & 31);
+            // The row's bytes for new tokens [o0, o1), four at a time where
+            // rows are whole words; bit c of the tile is new token k0 + c - L.
+            const int o0 = max(k0 - r.L, 0), o1 = min(min(r.kv_end, k0 + kTile) - r.L, r.n);
+            uint64_t lo = 0, hi = 0;
+            const auto put = [&](uint64_t bits, int c) {
+              if (c < 0) {
+                lo |= bits >> -c;
+              } else if (c < 64) {
+                lo |= bits << c;
+                if (c > 60) hi |= bits >> (64 - c);
+              } else {
+                hi |= bits << (c - 64);
+              }
+            };
+            if (p.mvec) {
+#pragma unroll 4
+              for (int o = o0 & ~3; o < o1; o += 4) {
+                const uint32_t v = static_cast<uint32_t>(ld32(reinterpret_cast<const int32_t *>(mrow + o)));
+                const uint32_t nz = (((v & 0x7f7f7f7fu) + 0x7f7f7f7fu) | v) & 0x80808080u;
+                uint32_t bits = ((nz >> 7) * 0x10204080u) >> 28;   // byte e to bit e
+                if (o1 - o < 4) bits &= (1u << (o1 - o)) - 1u;
+                put(bits, o + r.L - k0);
+              }
+            } else {
+#pragma unroll 4
+              for (int o = o0; o < o1; ++o) put(ld8(mrow + o) != 0, o + r.L - k0);
             }
+            vis[0] |= static_cast<uint32_t>(lo);
+            vis[1] |= static_cast<uint32_t>(lo >> 32);
+            vis[2] |= static_cast<uint32_t>(hi);
+            vis[3] |= static_cast<uint32_t>(hi >> 32);
           }
         }
         if (!(ok = wait_warp(&bars.s_full[s], ph_s++, err))) break;
+        __syncwarp();
         if (active) {
           tc_fence_after();
+          if (masked) {  // scores that the row does not see become -inf, in place
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t bits = w == 0 ? vis[0] : w == 1 ? vis[1] : w == 2 ? vis[2] : vis[3];
+              if (__all_sync(kFull, bits == ~0u)) continue;
+              uint32_t y[32];
+              tc_ld32(col_s + 32u * w, y);
+              tc_wait_ld(y);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((bits >> k) & 1u)) y[k] = 0xff800000u;
+              tc_st32(col_s + 32u * w, y);
+            }
+            tc_wait_st();
+            __syncwarp();
+          }
           // A chunk of S; the last one of the first pass stays in registers.
           constexpr int W = S::kChunk;
           uint32_t x[W];
@@ -532,15 +634,6 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < W; k += 32) tc_ld32(col_s + ch * W + k, x + k);
             tc_wait_ld(x);
-            if (p.negate) {
-#pragma unroll
-              for (int k = 0; k < W; ++k) x[k] ^= 0x80000000u;
-            }
-            if (masked) {
-#pragma unroll
-              for (int k = 0; k < W; ++k)
-                if (!((vis[(ch * W + k) >> 5] >> (k & 31)) & 1u)) x[k] = 0xff800000u;
-            }
           };
           float mt = -INFINITY;
 #pragma unroll
@@ -568,8 +661,9 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
               mc = nmc;
               l *= f;
             }
+            __syncwarp();
             if (j > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
                 tc_ld32(col_o + c, o);
@@ -602,6 +696,13 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             }
             if constexpr (W == 64) tc_st32(col_s + kPOff + ch * (W / 2), pk);
             else tc_st16(col_s + kPOff + ch * (W / 2), pk);
+            if (ch * W == kTile / 2) {  // the upper half of P is complete: its products may start
+              tc_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) sv::mbar_arrive(sv::smem_addr(&bars.p_half[s]));
+              __syncwarp();
+            }
           }
           float e0, e1, e2, e3;
           f2_unpack(l2a, e0, e1);
@@ -609,33 +710,20 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           l += (e0 + e1) + (e2 + e3);
           tc_wait_st();
           tc_fence_before();
+        } else if (lane == 0) {
+          sv::mbar_arrive(sv::smem_addr(&bars.p_half[s]));
         }
         __syncwarp();
         if (lane == 0) sv::mbar_arrive(sv::smem_addr(&bars.p_ready[s]));
       }
-      if (ok && nsteps > 0) ok = wait_warp(&bars.o_done[s], ph_o++, err);
-      // Both streams' sums are final: join and store.
-      if (!ok) failed = 1;
-      sh_m[s][my] = l == 0.f ? -INFINITY : mc;
-      sh_l[s][my] = l;
-      tc_fence_before();
-      named_bar(1, 256);
+      if (!ok || !(ok = wait_warp(&bars.o_done[s], ph_o++, err))) break;
       tc_fence_after();
-      const bool bad = seg_bad[seg % kSegRing] != 0;
-      ok = failed == 0;   // the same for both warpgroups: they leave together
+      const bool bad = seg_bad[rs][seg % kSegRing] == seg + 1;
       const bool whole = sg.t0 == 0 && sg.t1 == r.kt;
-      float f0 = 1.f, f1 = 0.f, lsum = l, mx = sh_m[s][my];
-      if (!kPair) {
-        const float a0 = sh_m[0][my], a1 = sh_m[1][my];
-        mx = fmaxf(a0, a1);
-        const float mb = mx == -INFINITY ? 0.f : mx;
-        f0 = sv::ex2(a0 - mb);
-        f1 = sv::ex2(a1 - mb);
-        lsum = sh_l[0][my] * f0 + sh_l[1][my] * f1;
-      }
       const int base_row = kPair ? s * kTile : 0;            // of the slot
-      const bool two = !kPair && nt > 1;
+      const float mx = l == 0.f ? -INFINITY : mc;
       const bool mine = my < tile_rows;
+      const bool boss = (tid & 127) == 0 && (!kPair || s == 0);
       float *slot = nullptr;
       uint8_t *orow = nullptr;
       float inv = 1.f;
@@ -643,93 +731,94 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         const int t = tok0 + my / a.G, g = my % a.G;
         const int64_t row = (static_cast<int64_t>(sg.b) * a.bt.T + t) * a.Hq + sg.h * a.G + g;
         orow = a.out + row * (D * 2);
-        inv = lsum == 0.f ? 0.f : 1.f / lsum;
-        if (mine && a.lse && !bad && (kPair || s == 0))
-          a.lse[row] = lsum == 0.f ? -INFINITY : mx * kLn2 + logf(lsum);
-        if (tid == 0)
+        inv = l == 0.f ? 0.f : 1.f / l;
+        if (mine && a.lse && !bad) a.lse[row] = l == 0.f ? -INFINITY : mx * kLn2 + logf(l);
+        if (boss)
           p.dirty[(static_cast<int64_t>(sg.b) * a.c.heads + sg.h) * p.MP + sg.mp] = bad ? 1 : 0;
       } else {
         // Slot 0 of the range where the segment starts it, else slot 1.
-        slot = p.slots + (static_cast<size_t>(blockIdx.x) * 2 + (seg == 0 ? 0 : 1)) * p.slot_floats;
-        if (mine && (kPair || s == 0)) {
+        slot = p.slots + (static_cast<size_t>(blockIdx.x + rs * gridDim.x) * 2 + (seg == 0 ? 0 : 1)) *
+                             p.slot_floats;
+        if (mine) {
           slot[D * p.slot_rows + base_row + my] = mx;
-          slot[(D + 1) * p.slot_rows + base_row + my] = lsum;
+          slot[(D + 1) * p.slot_rows + base_row + my] = l;
         }
-        if (tid == 0) reinterpret_cast<int *>(slot)[(D + 2) * p.slot_rows] = bad ? 1 : 0;
+        if (boss) reinterpret_cast<int *>(slot)[(D + 2) * p.slot_rows] = bad ? 1 : 0;
       }
-      if (active && ok && !bad) {
-        // kPair: a warpgroup stores its own rows; otherwise each takes half
-        // of the columns of all rows.
-        constexpr int kCols = kPair ? D : D / 2;
-        const int d0 = kPair ? 0 : s * kCols;
-        const uint32_t o0 = lanes + kColO + (kPair ? 128u * s : 0u) + d0, o1 = lanes + kColO + 128u + d0;
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
+      __syncwarp();
+      if (active && !bad) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
-          tc_ld32(o0 + c, o);
+          tc_ld32(col_o + c, o);
           tc_wait_ld(o);
           float v[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]);
-          if (two) {
-            uint32_t q[32];
-            tc_ld32(o1 + c, q);
-            tc_wait_ld(q);
+          if (mine) {
+            if (whole) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = v[k] * f0 + __uint_as_float(q[k]) * f1;
-          }
-          if (!mine) continue;
-          if (whole) {
+              for (int k = 0; k < 32; k += 8) {
+                uint32_t u[4];
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              uint32_t u[4];
+                for (int e = 0; e < 4; ++e) u[e] = pack2<Q>(v[k + 2 * e] * inv, v[k + 2 * e + 1] * inv);
+                *reinterpret_cast<uint4 *>(orow + (c + k) * 2) = make_uint4(u[0], u[1], u[2], u[3]);
+              }
+            } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                u[e] = pack2<Q>(v[k + 2 * e] * inv, v[k + 2 * e + 1] * inv);
-              *reinterpret_cast<uint4 *>(orow + (d0 + c + k) * 2) = make_uint4(u[0], u[1], u[2], u[3]);
+              for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<float4 *>(slot + (static_cast<size_t>((c + k) >> 2) * p.slot_rows + base_row +
+                                                    my) * 4) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
             }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4 *>(slot + (static_cast<size_t>((d0 + c + k) >> 2) * p.slot_rows +
-                                                  base_row + my) * 4) =
-                  make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
           }
+          __syncwarp();  // the warp's loads from TMEM are executed together
         }
       }
-      tc_fence_before();
-      named_bar(1, 256);
-      tc_fence_after();
-      if (tid == 0) seg_bad[seg % kSegRing] = 0;
+      tc_fence_before();   // O is read before the next P is announced
     }
   } else if (warp == 8) {
     // --------------------------------------------------------- producer ----
-    const int nb = kTile / p.box;                       // boxes per tile (and half)
-    const int half = S::kRaw ? 0 : lane / nb, bi = S::kRaw ? lane : lane - half * nb;
-    const bool lane_on = S::kRaw ? lane < nb : half < S::kHalves;
+    // Lane i looks up box i of a tile, an elected lane issues all copies.
+    const int nb = kTile / p.box;                       // boxes per tile, at most 16
     constexpr int kRing = S::kRaw ? S::kRawStages : S::kStages;
     uint64_t *const fullb = S::kRaw ? bars.rfull : bars.full;
     uint64_t *const emptyb = S::kRaw ? bars.rempty : bars.empty;
-    int it = 0, seg = 0, q_issued = 0;
-    // Block of this lane's box in a tile; -2 behind the last token.  A block
-    // that is not there marks the segment, whose unit is recomputed; any block
-    // is loaded in its place.
-    auto lookup = [&](const Seg &g, int tile) {
-      const int pos = tile * kTile + bi * p.box;
-      if (!lane_on || tile >= g.t1 || pos >= g.r.kv_end) return -2;
-      int id = ld32(a.c.tables + static_cast<size_t>(g.b) * a.c.max_blocks + pos / a.c.bs);
-      if (id < 0 || id >= a.c.num_blocks) {
-        report(a.bt.status, id == -1 ? SV_KV_MISSING_BLOCK : SV_KV_BAD_BLOCK);
-        seg_bad[seg % kSegRing] = 1;
-        id = 0;
+    int it = 0, q_issued[2] = {0, 0};
+    // A step whose block numbers are on their way: fetched a turn before they
+    // are used, for the tables' latency would otherwise bound the loads.
+    struct Step {
+      Cursor c;
+      int id, row;                           // this lane's box; id -2: none
+    };
+    const auto fetch = [&](const Cursor &c) {
+      Step k;
+      k.c = c;
+      k.id = -2;
+      k.row = 0;
+      const int pos = c.t * kTile + lane * p.box;
+      if (c.on && lane < nb && pos < c.kv_end) {
+        const int j = pos / a.c.bs;
+        k.row = pos - j * a.c.bs;
+        k.id = ld32(a.c.tables + static_cast<size_t>(c.b) * a.c.max_blocks + j);
       }
-      return id;
+      return k;
+    };
+    // A block that is not there marks the segment, whose unit is recomputed;
+    // any block is loaded in its place.
+    const auto settle = [&](Step &k, int rs) {
+      const bool box = lane < nb && k.c.t * kTile + lane * p.box < k.c.kv_end;
+      if (box && (k.id < 0 || k.id >= a.c.num_blocks)) {
+        report(a.bt.status, k.id == -1 ? SV_KV_MISSING_BLOCK : SV_KV_BAD_BLOCK);
+        seg_bad[rs][k.c.seg % kSegRing] = k.c.seg + 1;
+        k.id = 0;
+      }
+      if (!box) k.id = -2;
     };
     // A segment's queries: whole tokens, G heads each, in the swizzled layout.
-    auto load_q = [&](const Seg &g) {
-      const int qb = seg % S::kQBufs, use = seg / S::kQBufs;
-      if (use > 0 && !wait_warp(&bars.q_empty[qb], (use - 1) & 1, err)) return false;
-      const uint32_t bar = sv::smem_addr(&bars.q_full[qb]);
+    const auto load_q = [&](const Cursor &c, int rs) {
+      if (lane == 0 && c.cut) report(a.bt.status, SV_KV_TABLE_SHORT);
+      if (c.seg > 0 && !wait_warp(&bars.q_empty[rs], (c.seg - 1) & 1, err)) return false;
+      const uint32_t bar = sv::smem_addr(&bars.q_full[rs]);
       const uint32_t bytes = S::kTilesPerUnit * S::kHalves * p.qbox * a.G * 128;
       if (elect_one()) {
         sv::mbar_arrive_expect_tx(bar, bytes);
@@ -737,75 +826,122 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         for (int i = 0; i < S::kTilesPerUnit; ++i)
 #pragma unroll
           for (int hf = 0; hf < S::kHalves; ++hf)
-            tma_4d(sv::smem_addr(sq) + (kPair ? i : qb) * S::kStageBytes + hf * (kTile * 128), &p.qmap,
-                   hf * 64, g.h * a.G, g.mp * upt + i * p.TT, g.b, bar);
+            tma_4d(sv::smem_addr(sq) + (kPair ? i : rs) * S::kStageBytes + hf * (kTile * 128), &p.qmap,
+                   hf * 64, c.h * a.G, c.mp * upt + i * p.TT, c.b, bar);
       }
       __syncwarp();
-      ++q_issued;
+      ++q_issued[rs];
       return true;
     };
-    auto load = [&](const Seg &g, int tile, int id, bool is_v) {
+    const auto load = [&](const Step &k, bool is_v) {
       const int st = it % kRing;
       if (it >= kRing && !wait_warp(&emptyb[st], (it / kRing) & 1 ? 0u : 1u, err)) return false;
       const uint32_t bar = sv::smem_addr(&fullb[st]);
-      const unsigned on = __ballot_sync(kFull, id >= 0);
-      const uint32_t box_bytes = S::kRaw ? p.box * (D + D / SV_KV_GROUP) : p.box * 128;
-      if (lane == 0) sv::mbar_arrive_expect_tx(bar, __popc(on) * box_bytes);
+      const int boxes = __popc(__ballot_sync(kFull, k.id >= 0));   // the first ones
+      constexpr int srow = D / SV_KV_GROUP;
+      const uint32_t box_bytes = S::kRaw ? p.box * (D + srow) : S::kHalves * p.box * 128;
+      const CUtensorMap *map = is_v ? &p.vmap : &p.kmap;
+      const uint32_t dst =
+          S::kRaw ? sv::smem_addr(raw + st * S::kRawBytes) : sv::smem_addr(ring + st * S::kStageBytes);
+      if (elect_one()) sv::mbar_arrive_expect_tx(bar, boxes * box_bytes);
       __syncwarp();
-      if (id >= 0) {
-        const int row = (tile * kTile + bi * p.box) % a.c.bs;
-        const CUtensorMap *map = is_v ? &p.vmap : &p.kmap;
-        if constexpr (S::kRaw) {
-          const uint32_t dst = sv::smem_addr(raw + st * S::kRawBytes);
-          tma_4d(dst + bi * p.box * D, map, 0, row, g.h, id, bar);
-          constexpr int srow = D / SV_KV_GROUP;
-          bulk_1d(dst + S::kRawData + bi * p.box * srow,
-                  (is_v ? a.c.vs : a.c.ks) + id * a.c.sblock_bytes +
-                      (static_cast<int64_t>(g.h) * a.c.bs + row) * srow,
-                  p.box * srow, bar);
-        } else {
-          tma_4d(sv::smem_addr(ring + st * S::kStageBytes) + half * (kTile * 128) + bi * p.box * 128,
-                 map, half * 64, row, g.h, id, bar);
+      for (int i = 0; i < boxes; ++i) {
+        const int id = __shfl_sync(kFull, k.id, i), row = __shfl_sync(kFull, k.row, i);
+        if (elect_one()) {
+          if constexpr (S::kRaw) {
+            tma_4d(dst + i * p.box * D, map, 0, row, k.c.h, id, bar);
+            bulk_1d(dst + S::kRawData + i * p.box * srow,
+                    (is_v ? a.c.vs : a.c.ks) + id * a.c.sblock_bytes +
+                        (static_cast<int64_t>(k.c.h) * a.c.bs + row) * srow,
+                    p.box * srow, bar);
+          } else {
+#pragma unroll
+            for (int hf = 0; hf < S::kHalves; ++hf)
+              tma_4d(dst + hf * (kTile * 128) + i * p.box * 128, map, hf * 64, row, k.c.h, id, bar);
+          }
         }
+        __syncwarp();
       }
       ++it;
       return true;
     };
-    for (; ok && walk.next(a, upt, rc, sg); ++seg) {
-      if (lane == 0 && sg.r.kv_end < sg.r.L + sg.r.n) report(a.bt.status, SV_KV_TABLE_SHORT);
-      int id = lookup(sg, sg.t0), before = -2;
-      if (!kPair) ok = load_q(sg);
-      for (int t = sg.t0; ok && t < sg.t1; ++t) {
-        const int next = lookup(sg, t + 1);
-        ok = load(sg, t, id, false);
-        if (kPair) {
-          ok = ok && load(sg, t, id, true);
-          // One buffer: the first tiles are on their way before it is free.
-          if (t == sg.t0) ok = ok && load_q(sg);
-        } else {
-          if (t > sg.t0) ok = ok && load(sg, t - 1, before, true);
-          before = id;
-        }
-        id = next;
+    if constexpr (kPair) {
+      // K0 V0 K1 V1 ...; a segment's queries behind its first tiles.
+      Cursor c;
+      advance(c, 0, true);
+      Step next = fetch(c);
+#pragma unroll 1
+      while (ok && next.c.on) {
+        Step k = next;
+        advance(c, 0);
+        next = fetch(c);
+        settle(k, 0);
+#pragma unroll 1
+        for (int v = 0; ok && v < 2; ++v) ok = load(k, v);
+        if (ok && k.c.first()) ok = load_q(k.c, 0);
       }
-      if (!kPair) ok = ok && load(sg, sg.t1 - 1, before, true);
+    } else {
+      // K of both streams, then by turns V and the next K of each.  A new
+      // segment's queries follow the other stream's turn: by then the products
+      // that read the buffer have most likely ended.  One turn's code serves
+      // both streams, whose states change places after it.
+      struct State {
+        Cursor c;
+        Step now, next;
+        bool q_due;
+      } me, other;
+      int s = 0;
+      me.q_due = other.q_due = false;
+      me.now.c.on = other.now.c.on = false;
+#pragma unroll 1
+      for (int turn = 0; ok && (turn < 2 || me.now.c.on || other.now.c.on); ++turn) {
+        if (turn < 2) {
+          advance(me.c, s, true);
+          me.next = fetch(me.c);
+          me.now.c.on = me.next.c.on;
+        } else if (me.now.c.on) {
+          ok = load(me.now, true);
+        }
+        if (ok && me.now.c.on) {
+          me.now = me.next;
+          if (me.now.c.on) {
+            advance(me.c, s);
+            me.next = fetch(me.c);
+            settle(me.now, s);
+            me.q_due = me.now.c.first();
+            ok = load(me.now, false);
+          }
+        }
+        if (ok && other.q_due) {
+          ok = load_q(other.now.c, 1 - s);
+          other.q_due = false;
+        }
+        if (ok && me.q_due && (turn < 2 || !other.now.c.on)) {
+          ok = load_q(me.now.c, s);
+          me.q_due = false;
+        }
+        swap2(me, other);
+        s = 1 - s;
+      }
     }
     if (!ok) {  // every copy in flight lands before the block ends
       for (int k = max(0, it - kRing); k < it; ++k) wait_warp(&fullb[k % kRing], (k / kRing) & 1, err);
-      for (int k = max(0, seg - S::kQBufs); k <= seg; ++k)
-        if (q_issued > k) wait_warp(&bars.q_full[k % S::kQBufs], (k / S::kQBufs) & 1, err);
+#pragma unroll
+      for (int s = 0; s < S::kStreams; ++s)
+        if (q_issued[s] > 0) wait_warp(&bars.q_full[s], (q_issued[s] - 1) & 1, err);
     }
   } else if (warp == 9) {
     // --------------------------------------------------------------- MMA ----
-    constexpr uint32_t kQK = mma_desc<Q>(kTile, false), kPV = mma_desc<Q>(D, true);
+    const uint32_t kQK = mma_desc<Q>(kTile, false) | (p.negate ? kNegateA : 0u);
+    constexpr uint32_t kPV = mma_desc<Q>(D, true);
     const uint64_t q_desc = smem_desc(sv::smem_addr(sq), 16), k_desc = smem_desc(sv::smem_addr(ring), 16);
     const uint64_t v_desc = smem_desc(sv::smem_addr(ring), kTile * 128);
-    int it = 0, seg = 0;           // stages taken, in load order
-    uint32_t ph_p[2] = {0, 0}, fix = 0;  // fix: per stage, parity of its repairs
-    auto take = [&](int k0, int full_end, bool is_v) {
+    int it = 0;                    // stages taken, in load order
+    uint32_t ph_p = 0, fix = 0;    // parities: of P per stream, of its repairs per stage
+    const auto take = [&](const Cursor &c, bool is_v) {
       const int st = it % S::kStages;
       bool good = wait_warp(&bars.full[st], (it / S::kStages) & 1, err);
-      if (!S::kRaw && good && is_v && k0 + kTile > full_end) {
+      if (!S::kRaw && good && is_v && (c.t + 1) * kTile > c.new0) {
         good = wait_warp(&bars.fixed[st], (fix >> st) & 1u, err);
         fix ^= 1u << st;
       }
@@ -817,7 +953,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       ++it;
     };
     auto qk = [&](int s) {
-      const uint64_t qd = q_desc + (kPair ? s : seg % S::kQBufs) * (S::kStageBytes >> 4);
+      const uint64_t qd = q_desc + s * (S::kStageBytes >> 4);
       const uint64_t kd = k_desc + (it % S::kStages) * (S::kStageBytes >> 4);
       if (elect_one()) {
 #pragma unroll
@@ -828,90 +964,95 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       }
       __syncwarp();
     };
+    // Keys 64 .. 127 of the tile first: their P is ready first.
     auto pv = [&](int s, bool first) {
       const uint64_t vd = v_desc + (it % S::kStages) * (S::kStageBytes >> 4);
-      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          tc_mma_ts(tmem + kColO + 128u * s, tmem + kColS + 128u * s + kPOff + 8u * k,
-                    vd + k * (2048 >> 4), kPV, !first || k > 0);
+      for (int half = 1; half >= 0; --half) {
+        if (half == 0) {
+          if (!wait_warp(&bars.p_ready[s], ph_p >> s, err)) return false;
+          ph_p ^= 1u << s;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 4 * half; k < 4 * half + 4; ++k)
+            tc_mma_ts(tmem + kColO + 128u * s, tmem + kColS + 128u * s + kPOff + 8u * k,
+                      vd + k * (2048 >> 4), kPV, !(first && k == 4));
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      return true;
     };
     auto commit = [&](uint64_t *bar) {
       if (elect_one()) tc_commit(sv::smem_addr(bar));
     };
-    for (; ok && walk.next(a, upt, rc, sg); ++seg) {
-      const int nt = sg.t1 - sg.t0, full_end = min(sg.r.L, sg.r.kv_end);
-      const auto key0 = [&](int t) { return (sg.t0 + t) * kTile; };
-      uint64_t *const q_free = &bars.q_empty[seg % S::kQBufs];
-      if (!(ok = wait_warp(&bars.q_full[seg % S::kQBufs], seg / S::kQBufs, err))) break;
-      tc_fence_after();
-      if (kPair) {
-        // Stages in order K0 V0 K1 V1 ...
-        if (!(ok = take(key0(0), full_end, false))) break;
-        qk(0);
-        commit(&bars.s_full[0]);
-        qk(1);
-        commit(&bars.s_full[1]);
-        release();
-        if (nt == 1) commit(q_free);
-        for (int t = 0; ok && t < nt; ++t) {
-          ok = wait_warp(&bars.p_ready[0], ph_p[0]++, err) && take(key0(t), full_end, true);
-          if (!ok) break;
-          tc_fence_after();
-          pv(0, t == 0);
-          const int v_it = it;
-          if (t + 1 == nt) {
-            commit(&bars.o_done[0]);
-          } else {
-            ++it;                                    // K of the next tile
-            ok = take(key0(t + 1), full_end, false);
-            if (!ok) break;
-            qk(0);
-            commit(&bars.s_full[0]);
-            it = v_it;
-          }
-          ok = wait_warp(&bars.p_ready[1], ph_p[1]++, err);
-          if (!ok) break;
-          tc_fence_after();
-          pv(1, t == 0);
-          release();                                 // V
-          if (t + 1 == nt) {
-            commit(&bars.o_done[1]);
-          } else {
-            qk(1);
-            commit(&bars.s_full[1]);
-            release();                               // K
-            if (t + 2 == nt) commit(q_free);
-          }
+    if constexpr (kPair) {
+      // S of both streams for step c, whose K is stage `it`.
+      const auto products = [&](const Cursor &c, int s) {
+        if (s == 0) {
+          if (c.first() && !wait_warp(&bars.q_full[0], c.seg, err)) return false;
+          if (!take(c, false)) return false;
         }
-      } else {
-        // Stages in order K0 K1 V0 K2 V1 ...; tile t belongs to stream t & 1.
-        for (int t = 0; ok && t < min(nt, 2); ++t) {
-          if (!(ok = take(key0(t), full_end, false))) break;
-          qk(t);
-          commit(&bars.s_full[t]);
+        qk(s);
+        commit(&bars.s_full[s]);
+        if (s == 1) {
           release();
+          if (c.last()) commit(&bars.q_empty[0]);
         }
-        if (ok && nt <= 2) commit(q_free);
-        for (int t = 0; ok && t < nt; ++t) {
-          const int s = t & 1;
-          ok = wait_warp(&bars.p_ready[s], ph_p[s]++, err) && take(key0(t), full_end, true);
+        return true;
+      };
+      // One turn is one stream's P V and its next Q K^T; the first two turns
+      // have only the latter.  V's stage is `it`, the next K's the one after.
+      Cursor c, n;
+      advance(n, 0, true);
+      c.on = false;
+#pragma unroll 1
+      for (int turn = 0; ok && (n.on || c.on); ++turn) {
+        const int s = turn & 1;
+        if (turn >= 2) {
+          ok = wait_warp(&bars.p_half[s], ph_p >> s, err) && (s == 1 || take(c, true)) && pv(s, c.first());
           if (!ok) break;
-          tc_fence_after();
-          pv(s, t < 2);
+          if (s == 1) release();                     // V
+          if (c.last()) commit(&bars.o_done[s]);
+          if (n.on) {
+            if (s == 0) ++it;
+            ok = products(n, s);
+            if (s == 0) --it;
+          }
+        } else {
+          ok = products(n, s);
+        }
+        if (s == 1) {                                // both streams have taken the step
+          c = n;
+          if (n.on) advance(n, 0);
+        }
+      }
+    } else {
+      Cursor me, other;
+      int s = 0;
+      me.on = other.on = false;
+#pragma unroll 1
+      for (int turn = 0; ok && (turn < 2 || me.on || other.on); ++turn) {
+        if (turn < 2) {
+          advance(me, s, true);
+        } else if (me.on) {
+          ok = wait_warp(&bars.p_half[s], ph_p >> s, err) && take(me, true) && pv(s, me.first());
           release();
-          if (t + 2 < nt) {
-            if (!(ok = take(key0(t + 2), full_end, false))) break;
+          if (me.last()) commit(&bars.o_done[s]);
+          advance(me, s);
+        }
+        if (ok && me.on) {
+          ok = (!me.first() || wait_warp(&bars.q_full[s], me.seg, err)) && take(me, false);
+          if (ok) {
             qk(s);
             commit(&bars.s_full[s]);
             release();
-            if (t + 3 == nt) commit(q_free);
-          } else {
-            commit(&bars.o_done[s]);
+            if (me.last()) commit(&bars.q_empty[s]);
           }
         }
+        swap2(me, other);
+        s = 1 - s;
       }
     }
     if (!ok) {  // issued products end before TMEM is freed
@@ -923,14 +1064,13 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // ------------------------------------------------------------ helpers ----
     const int ht = tid - 320;                           // helper thread
     constexpr int kHT = S::kHelpers * 32;
-    int it = 0, rit = 0, seg = 0;
+    int it = 0, rit = 0;
     uint32_t found = 0;
     // Not kRaw: V tiles that reach past the committed tokens, in place.
-    auto repair = [&](const Seg &g, int tile) {
+    const auto repair = [&](const Cursor &c) {
       const int st = it % S::kStages;
       uint8_t *base = ring + st * S::kStageBytes;
-      const int k0 = tile * kTile;
-      const int r0 = max(min(g.r.L, g.r.kv_end) - k0, 0), r1 = g.r.kv_end - k0;  // new rows [r0, r1)
+      const int k0 = c.t * kTile, r0 = max(c.new0 - k0, 0), r1 = c.kv_end - k0;  // new rows [r0, r1)
       constexpr int kCh = S::kHalves * 8;
       for (int i = ht + r0 * kCh; i < kTile * kCh; i += kHT) {
         const int row = i / kCh, ch = i % kCh;
@@ -944,7 +1084,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       }
     };
     // kRaw: 16 codes at a time, widened into the swizzled layout.
-    auto widen = [&](const Seg &g, int tile, bool is_v) {
+    const auto widen = [&](const Cursor &c, bool is_v) {
       const int st = it % S::kStages, rs = rit % (S::kRaw ? S::kRawStages : 1);
       if (!wait_warp(&bars.rfull[rs], (rit / (S::kRaw ? S::kRawStages : 1)) & 1, err)) return false;
       if (it >= S::kStages && !wait_warp(&bars.empty[st], (it / S::kStages) & 1 ? 0u : 1u, err)) return false;
@@ -952,9 +1092,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       const uint8_t *sc = src + S::kRawData;
       uint8_t *dst = ring + st * S::kStageBytes;
       constexpr int kCh = D / 16;                       // 16-code chunks per row
-      const int k0 = tile * kTile, r1 = is_v ? g.r.kv_end - k0 : kTile;
-      const bool look = is_v && k0 + kTile > min(g.r.L, g.r.kv_end);
-      const int r0 = max(min(g.r.L, g.r.kv_end) - k0, 0);
+      const int k0 = c.t * kTile, r0 = max(c.new0 - k0, 0), r1 = is_v ? c.kv_end - k0 : kTile;
+      const bool look = is_v && k0 + kTile > c.new0;
 #pragma unroll 4
       for (int i = ht; i < kTile * kCh; i += kHT) {
         const int row = i / kCh, ch = i % kCh;
@@ -991,10 +1130,10 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       return true;
     };
     // One stage of the load order.
-    auto stage = [&](const Seg &g, int tile, bool is_v) {
+    const auto stage = [&](const Cursor &c, bool is_v, int rs) {
       if constexpr (S::kRaw) {
-        if (!widen(g, tile, is_v)) return false;
-        if (found) seg_bad[seg % kSegRing] = 1;
+        if (!widen(c, is_v)) return false;
+        if (found) seg_bad[rs][c.seg % kSegRing] = c.seg + 1;
         found = 0;
         fence_async_smem();
         __syncwarp();
@@ -1009,10 +1148,10 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         // one that fell behind would miss a phase.
         const int st = it % S::kStages;
         if (!wait_warp(&bars.full[st], (it / S::kStages) & 1, err)) return false;
-        const bool fix = is_v && (tile + 1) * kTile > min(g.r.L, g.r.kv_end);
+        const bool fix = is_v && (c.t + 1) * kTile > c.new0;
         if (fix) {
-          repair(g, tile);
-          if (found) seg_bad[seg % kSegRing] = 1;
+          repair(c);
+          if (found) seg_bad[rs][c.seg % kSegRing] = c.seg + 1;
           found = 0;
           fence_async_smem();
         }
@@ -1025,13 +1164,33 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       ++it;
       return true;
     };
-    for (; ok && walk.next(a, upt, rc, sg); ++seg) {
-      for (int t = sg.t0; ok && t < sg.t1; ++t) {
-        ok = stage(sg, t, false);
-        if (kPair) ok = ok && stage(sg, t, true);
-        else if (t > sg.t0) ok = ok && stage(sg, t - 1, true);
+    if constexpr (kPair) {
+      Cursor c;
+      advance(c, 0, true);
+#pragma unroll 1
+      for (int v = 0; ok && c.on; v ^= 1) {
+        ok = stage(c, v, 0);
+        if (v) advance(c, 0);
       }
-      if (!kPair) ok = ok && stage(sg, sg.t1 - 1, true);
+    } else {
+      // K of both streams, then by turns V and the next K of each.
+      Cursor me, other;
+      int s = 0;
+      me.on = other.on = false;
+#pragma unroll 1
+      for (int turn = 0; ok && (turn < 4 || me.on || other.on); ++turn) {
+        const bool v = !(turn & 1);                  // turns 0 and 2 begin a stream instead
+        if (turn < 4 && v) {
+          advance(me, s, true);
+        } else if (me.on) {
+          ok = stage(me, v, s);
+          if (v) advance(me, s);
+        }
+        if (!v) {
+          swap2(me, other);
+          s = 1 - s;
+        }
+      }
     }
   }
 
@@ -1060,10 +1219,12 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
   const Req r = request(a, upt, b, st);
   if (mp >= r.mp) return;
   const int tok0 = mp * upt, rows = min(upt, r.n - tok0) * a.G;
-  const int quota = ld32(p.head), start = ld32(p.pre + b) + (h * r.mp + mp) * r.kt;
-  const int c0 = start / quota, c1 = (start + r.kt - 1) / quota;
+  const int total = ld32(p.head), start = ld32(p.pre + b) + (h * r.mp + mp) * r.kt;
+  const int N = min(p.ranges, total);
+  const int c0 = range_of(start, N, total), c1 = range_of(start + r.kt - 1, N, total);
+  const int late = range_start(c0, N, total) == start ? 0 : 1;  // not the first segment of range c0
   auto slot_of = [&](int c) {
-    return p.slots + (static_cast<size_t>(c) * 2 + (c == c0 && start % quota ? 1 : 0)) * p.slot_floats;
+    return p.slots + (static_cast<size_t>(c) * 2 + (c == c0 ? late : 0)) * p.slot_floats;
   };
   int bad = 0;
   if (c0 == c1) {

@@ -290,7 +290,7 @@ TcLayout tc_layout(int64_t B, int64_t T, int64_t G, int64_t heads, int64_t D) {
   w.pre = 256;
   w.dirty = w.pre + up(4 * (B + 1), 256);
   w.slots = w.dirty + up(B * heads * w.MP, 256);
-  w.total = w.slots + up(static_cast<size_t>(kMaxGrid) * 2 * w.slot_floats * 4, 256);
+  w.total = w.slots + up(static_cast<size_t>(kMaxGrid) * (pair ? 1 : 2) * 2 * w.slot_floats * 4, 256);
   return w;
 }
 
@@ -319,7 +319,7 @@ sv_status tc_launch(const TcParams &p, int nsm, int dev, sv_stream_t stream) {
       return SV_ERR_CUDA;
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  const int grid = std::min(nsm, kMaxGrid);
+  const int grid = p.ranges / S::kStreams;
   if (const sv_status s = launch(k, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, stream, p))
     return s;
   const int rows = std::min(p.a.bt.T, p.TT * S::kTilesPerUnit) * p.a.G;
@@ -365,6 +365,8 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
            make_query_map(p.qmap, ap, a->dtype, p.qbox);
   if (!*taken) return SV_OK;  // strides that no tensor map describes
   const bool pair = ap.bt.T > w.TT;
+  p.ranges = std::min(nsm, kMaxGrid) * (pair ? 1 : 2);
+  p.mvec = ap.mask && ap.bt.T % 4 == 0 && aligned(ap.mask, 4) && ap.msb % 4 == 0;
   if (a->cache.dtype == SV_E4M3) return tc_pick<BF16, E4M3>(p, pair, nsm, dev, stream);
   return a->dtype == SV_BF16 ? tc_pick<BF16, BF16>(p, pair, nsm, dev, stream)
                              : tc_pick<F16, F16>(p, pair, nsm, dev, stream);
