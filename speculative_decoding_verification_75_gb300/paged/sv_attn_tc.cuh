@@ -238,30 +238,42 @@ template <typename Q, typename C, int D, bool kPair>
 struct Shape {
   static constexpr bool kRaw = C::kBytes == 1;      // e4m3: widened on chip
   static constexpr int kHalves = D / 64;
-  static constexpr int kStageBytes = kTile * D * 2;
   static constexpr int kStreams = kPair ? 1 : 2;    // ranges of a block
-  static constexpr int kQBytes = 2 * kStageBytes;
-  static constexpr int kRawData = kTile * D, kRawScale = kTile * (D / SV_KV_GROUP);
+  static constexpr int kQTile = kTile * D * 2;
+  static constexpr int kQBytes = 2 * kQTile;        // a Q tile per stream
+  // Each range has a ring of its own, with one order of loads: a parity tells
+  // two phases of a barrier apart only if no one is a whole round ahead.  Two
+  // rings get half tiles, so that each is deep enough.
+  static constexpr int kKeys = kPair ? kTile : kTile / 2;   // keys of a stage
+  static constexpr int kParts = kTile / kKeys;              // stages of a tile
+  static constexpr int kStageBytes = kKeys * D * 2;
+  static constexpr int kHalf = kKeys * 128;                 // bytes of a stage's 64 columns
+  static constexpr int kRawData = kKeys * D, kRawScale = kKeys * (D / SV_KV_GROUP);
   static constexpr int kRawBytes = kRawData + kRawScale;
-  // Ring sizes: as many stages as 227 KB hold (about 200 KB where tiles are
+  // Stages of a ring: as many as 227 KB hold (about 200 KB where tiles are
   // small); raw stages first, they are what is in flight.
   static constexpr int kStages = kRaw ? 3 : D == 128 ? 5 : 11;
   static constexpr int kRawStages = kRaw ? (D == 128 ? 3 : 10) : 0;
-  static constexpr int kHelpers = kRaw ? 6 : 2;     // warps: 3 or 4 per scheduler in all
-  static constexpr int kWarps = 10 + kHelpers;
-  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kChunk = kRaw ? 32 : 64;     // S columns in registers at once
   static constexpr int kTilesPerUnit = kPair ? 2 : 1;
-  static constexpr int kSmem = kQBytes + kStages * kStageBytes + kRawStages * kRawBytes;
+  // Warps: 8 softmax, 2 producers, 2 for the products, and 4 that widen: 3 or
+  // 4 on each scheduler.
+  static constexpr int kWideners = kRaw ? 4 : 0;
+  static constexpr int kWarps = 12 + kWideners;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kRingWideners = kWideners / kStreams;
+  static constexpr int kSmem = kQBytes + kStreams * (kStages * kStageBytes + kRawStages * kRawBytes);
 };
 
 // TMEM columns.
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream
 constexpr uint32_t kPOff = 64;              // P in the upper half of its S
 
+struct RingBars {
+  uint64_t full[11], empty[11], fixed[11], rfull[10], rempty[10];
+};
 struct Bars {
-  uint64_t full[12], empty[12], fixed[12], rfull[10], rempty[10];
-  uint64_t s_full[2], p_half[2], p_ready[2], o_done[2], q_full[2], q_empty[2], drain;
+  uint64_t s_full[2], p_half[2], p_ready[2], o_done[2], q_full[2], q_empty[2], drain[2];
 };
 
 // ----------------------------------------------------------------- work ----
@@ -272,132 +284,123 @@ struct Req {
 
 // Tiles of a request: its units (KV head, group of row tiles) times its key
 // tiles.  upt: new tokens of a unit.
-__device__ __forceinline__ Req make_request(const AttnParams &p, int upt, int L, int n) {
+__device__ __forceinline__ Req request(const AttnParams &p, int upt, int b, uint32_t &st) {
   Req r;
-  r.L = L;
-  r.n = n;
-  r.mp = (n + upt - 1) / upt;
-  r.kv_end = min(L + n, p.c.max_blocks * p.c.bs);
+  lengths(p.bt, b, r.L, r.n, st);
+  r.mp = (r.n + upt - 1) / upt;
+  r.kv_end = min(r.L + r.n, p.c.max_blocks * p.c.bs);
   r.kt = max(1, (r.kv_end + kTile - 1) / kTile);
   r.weight = p.c.heads * r.mp * r.kt;
   return r;
 }
-__device__ __forceinline__ Req request(const AttnParams &p, int upt, int b, uint32_t &st) {
-  int L, n;
-  lengths(p.bt, b, L, n, st);
-  return make_request(p, upt, L, n);
-}
 
-// Lengths of the requests from a range's first one on, in shared memory.
-constexpr int kReqCache = 32;
-struct ReqCache {
-  int b0;
-  int2 len[kReqCache];
-};
-
-// A run of key tiles [t0, t1) of one unit.
-struct Seg {
-  int b, unit, h, mp, t0, t1;
-  Req r;
-};
-
-// Walks a range of the tile sequence, unit after unit.
-struct Walk {
-  int b, unit, tile, left;
-  Req r;
-};
-
-__device__ __forceinline__ Req fetch_request(const AttnParams &p, int upt, const ReqCache &rc, int b) {
-  if (b - rc.b0 < kReqCache) {
-    const int2 v = rc.len[b - rc.b0];
-    return make_request(p, upt, v.x, v.y);
-  }
-  uint32_t st = 0;
-  return request(p, upt, b, st);
-}
-
-// The next segment of a walk, false at its end.  `rem` >= 0 begins the walk:
-// tiles of the first request before the range.  Not inlined: every role of the
-// kernel walks, and the copies together would not fit the instruction cache.
-__device__ __noinline__ bool walk_next(const AttnParams &p, int upt, const ReqCache &rc, Walk &w, Seg &s,
-                                       int rem) {
-  if (w.left <= 0) return false;
-  if (rem >= 0) {
-    w.b = rc.b0;
-    w.r = fetch_request(p, upt, rc, w.b);
-    w.unit = rem / w.r.kt;
-    w.tile = rem - w.unit * w.r.kt;
-  }
-  s.b = w.b;
-  s.r = w.r;
-  s.unit = w.unit;
-  s.h = w.unit / w.r.mp;
-  s.mp = w.unit - s.h * w.r.mp;
-  s.t0 = w.tile;
-  s.t1 = min(w.r.kt, w.tile + w.left);
-  w.left -= s.t1 - s.t0;
-  w.tile = s.t1;
-  if (w.tile == w.r.kt) {
-    w.tile = 0;
-    if (++w.unit == p.c.heads * w.r.mp) {
-      w.unit = 0;
-      if (w.left > 0) {
-        do {
-          ++w.b;
-          w.r = fetch_request(p, upt, rc, w.b);
-        } while (w.r.weight == 0);
-      }
-    }
-  }
-  return true;
+__device__ __forceinline__ int weight_of(const AttnParams &p, int upt, int b, uint32_t &st) {
+  return b < p.bt.B ? request(p, upt, b, st).weight : 0;
 }
 
 // Range i of N <= total over `total` tiles is [start(i), start(i + 1)): none is
 // empty.  Range i belongs to stream i / gridDim.x of block i % gridDim.x, so
 // that few tiles spread over many blocks.
 __device__ __forceinline__ int range_start(int i, int N, int total) {
-  return static_cast<int>(static_cast<int64_t>(i) * total / N);
-}
-__device__ __forceinline__ int range_of(int tile, int N, int total) {
-  return static_cast<int>(((static_cast<int64_t>(tile) + 1) * N - 1) / total);
+  const int q = total / N;                   // i < N <= 304: no product passes 2^31
+  return i * q + i * (total - q * N) / N;
 }
 
-// A tile step of a walk: where it is and what the roles ask about it.
-struct Cursor {
-  int b, h, mp, t, t0, t1, seg, new0, kv_end;  // new0: keys that every row sees
-  bool on, cut;                                // cut: the table is too short
+// A walk over a range's tiles, unit after unit: where it stands, and the
+// segment (a run of key tiles of one unit) it is in.
+struct Walk {
+  int b, unit, left;      // left: tiles of the range behind this segment
+  Req r;
+  int h, mp, t, t0, t1, seg;
+  bool on;
 
   __device__ __forceinline__ bool first() const { return t == t0; }
   __device__ __forceinline__ bool last() const { return t + 1 == t1; }
+  __device__ __forceinline__ int new0() const { return min(r.L, r.kv_end); }  // keys every row sees
 };
 
-// begin: to the range's first tile, `rem` tiles into its first request.
-__device__ __forceinline__ void step_to(const AttnParams &p, int upt, const ReqCache &rc, Walk &w, Cursor &c,
-                                        bool begin, int rem) {
-  if (!begin && ++c.t < c.t1) return;
-  Seg s;
-  c.on = walk_next(p, upt, rc, w, s, begin ? rem : -1);
-  c.seg = begin ? 0 : c.seg + 1;
-  if (!c.on) return;
-  c.b = s.b;
-  c.h = s.h;
-  c.mp = s.mp;
-  c.t = c.t0 = s.t0;
-  c.t1 = s.t1;
-  c.kv_end = s.r.kv_end;
-  c.new0 = min(s.r.L, s.r.kv_end);
-  c.cut = s.r.kv_end < s.r.L + s.r.n;
+// To the next segment.  Not inlined: every role of the kernel walks, and the
+// copies together would crowd the instruction cache.
+__device__ __noinline__ void next_segment(const AttnParams &p, int upt, Walk &w) {
+  Walk v = w;
+  v.on = v.left > 0;
+  if (v.on) {
+    if (v.seg >= 0 && ++v.unit == p.c.heads * v.r.mp) {
+      v.unit = 0;
+      uint32_t st = 0;
+      do {
+        v.r = request(p, upt, ++v.b, st);
+      } while (v.r.weight == 0);
+    }
+    if (v.seg >= 0) v.t0 = 0;                // a later segment begins a unit
+    v.t1 = min(v.r.kt, v.t0 + v.left);
+    v.left -= v.t1 - v.t0;
+    v.t = v.t0;
+    v.h = v.unit / v.r.mp;
+    v.mp = v.unit - v.h * v.r.mp;
+  }
+  ++v.seg;
+  w = v;
 }
 
-template <typename T>
-__device__ __forceinline__ void swap2(T &a, T &b) {
-  const T c = a;
-  a = b;
-  b = c;
+__device__ __forceinline__ void next_tile(const AttnParams &p, int upt, Walk &w) {
+  if (++w.t == w.t1) next_segment(p, upt, w);
 }
 
+// Range i's first tile.  Called by whole warps: the requests are spread over
+// the lanes, 32 at a time, and `total` is all their tiles.
+__device__ __noinline__ void begin_walk(const AttnParams &p, int upt, int i, int ranges, int total, Walk &w) {
+  const int N = min(ranges, total);
+  w.on = false;
+  w.left = 0;
+  if (i >= N) return;
+  const int begin = range_start(i, N, total);
+  w.left = range_start(i + 1, N, total) - begin;
+  const int lane = threadIdx.x & 31;
+  uint32_t st = 0;
+  int base = 0;
+#pragma unroll 1
+  for (int c = 0; c < p.bt.B; c += 32) {
+    const int x = weight_of(p, upt, c + lane, st);
+    const int sum = __reduce_add_sync(kFull, x);
+    if (begin < base + sum) {
+      int incl = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const int excl = base + incl - x;
+      const int src = __ffs(__ballot_sync(kFull, begin >= excl && begin < excl + x)) - 1;
+      const int rem = begin - __shfl_sync(kFull, excl, src);
+      w.b = c + src;
+      w.r = request(p, upt, w.b, st);
+      w.unit = rem / w.r.kt;
+      w.t0 = rem - w.unit * w.r.kt;
+      w.seg = -1;
+      w.t1 = 0;
+      next_segment(p, upt, w);
+      return;
+    }
+    base += sum;
+  }
+}
+
+// A converged warp's wait for an mbarrier phase; false when it gives up.  It
+// polls: a warp suspended in try_wait was seen to wake a microsecond late when
+// its scheduler is busy, and these waits are links of one chain.  2^25 polls
+// of some 40 cycles end after about a second.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t *err) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 25); ++i)
+    if (__any_sync(kFull, sv::mbar_test_wait(bar, parity))) return true;
+  report(err, SV_FAULT_TIMEOUT);
+  return false;
+}
 __device__ __forceinline__ bool wait_warp(const uint64_t *bar, uint32_t parity, uint32_t *err) {
-  return sv::mbar_wait_warp(sv::smem_addr(bar), parity & 1u, err);
+  const uint32_t at = sv::smem_addr(bar);
+  parity &= 1u;
+  return __any_sync(kFull, sv::mbar_test_wait(at, parity)) || wait_long(at, parity, err);
 }
 
 // ------------------------------------------------------------ main kernel ----
@@ -408,45 +411,43 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   using S = Shape<Q, C, D, kPair>;
   extern __shared__ __align__(1024) uint8_t smem[];   // swizzle atoms: 1024 bytes
   __shared__ Bars bars;
+  __shared__ RingBars rings[S::kStreams];
   __shared__ uint32_t tmem_slot;
-  __shared__ ReqCache rc[S::kStreams];        // b0: the range's first request
-  __shared__ int sh_rem[S::kStreams];         // tiles of it before the range
-  __shared__ int sh_scan[S::kWarps + 1];
   __shared__ int seg_bad[S::kStreams][kSegRing];  // holds 1 + a marked segment's number
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t *const sq = smem;
-  uint8_t *const ring = sq + S::kQBytes;
-  uint8_t *const raw = ring + S::kStages * S::kStageBytes;
+  uint8_t *const ring0 = sq + S::kQBytes;
+  uint8_t *const raw0 = ring0 + S::kStreams * S::kStages * S::kStageBytes;
 
   if (sv::smem_addr(smem) & 1023u) {                    // never: the swizzle would not match
     report(p.err, SV_FAULT_TIMEOUT);
     return;
   }
-  if (warp == 9) tc_alloc(sv::smem_addr(&tmem_slot), 512);
+  if (warp == 11) tc_alloc(sv::smem_addr(&tmem_slot), 512);
   if (tid == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
-      sv::mbar_init(sv::smem_addr(&bars.full[i]), S::kRaw ? S::kHelpers : 1);
-      sv::mbar_init(sv::smem_addr(&bars.empty[i]), S::kRaw ? 1 : 1 + S::kHelpers);
-      sv::mbar_init(sv::smem_addr(&bars.fixed[i]), S::kHelpers);
-    }
-    for (int i = 0; i < S::kRawStages; ++i) {
-      sv::mbar_init(sv::smem_addr(&bars.rfull[i]), 1);
-      sv::mbar_init(sv::smem_addr(&bars.rempty[i]), S::kHelpers);
+    for (int r = 0; r < S::kStreams; ++r) {
+      for (int i = 0; i < S::kStages; ++i) {
+        sv::mbar_init(sv::smem_addr(&rings[r].full[i]), S::kRaw ? S::kRingWideners : 1);
+        sv::mbar_init(sv::smem_addr(&rings[r].empty[i]), kPair ? 2 : 1);
+        sv::mbar_init(sv::smem_addr(&rings[r].fixed[i]), 1);
+      }
+      for (int i = 0; i < S::kRawStages; ++i) {
+        sv::mbar_init(sv::smem_addr(&rings[r].rfull[i]), 1);
+        sv::mbar_init(sv::smem_addr(&rings[r].rempty[i]), S::kRingWideners);
+      }
     }
     for (int s = 0; s < 2; ++s) {
       sv::mbar_init(sv::smem_addr(&bars.s_full[s]), 1);
-      sv::mbar_init(sv::smem_addr(&bars.p_ready[s]), 4);
       sv::mbar_init(sv::smem_addr(&bars.p_half[s]), 4);
+      sv::mbar_init(sv::smem_addr(&bars.p_ready[s]), 4);
       sv::mbar_init(sv::smem_addr(&bars.o_done[s]), 1);
       sv::mbar_init(sv::smem_addr(&bars.q_full[s]), 1);
       sv::mbar_init(sv::smem_addr(&bars.q_empty[s]), 1);
+      sv::mbar_init(sv::smem_addr(&bars.drain[s]), 1);
     }
-    sv::mbar_init(sv::smem_addr(&bars.drain), 1);
-    for (int s = 0; s < S::kStreams; ++s) {
+    for (int s = 0; s < S::kStreams; ++s)
       for (int i = 0; i < kSegRing; ++i) seg_bad[s][i] = 0;
-      sh_rem[s] = 0;   // of a range without tiles
-    }
     sv::fence_mbar_init();
   }
   if (tid == 32) {
@@ -455,87 +456,34 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.qmap) : "memory");
   }
   const AttnParams &a = p.a;
-  const int B = a.bt.B;
   if (warp == 2) {  // addresses only: the values may still be written
-    const int64_t at = static_cast<int64_t>(lane) * 32 < B ? lane * 32 : 0;
+    const int at = lane * 32 < a.bt.B ? lane * 32 : 0;
     asm volatile("prefetch.global.L2 [%0];" ::"l"(a.bt.seq_lens + at));
     if (a.bt.new_lens) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.bt.new_lens + at));
     if (a.c.max_blocks > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.tables));
-  }
-  sv::pdl_wait();
-  sv::pdl_launch_dependents();
-
-  // This block's ranges of the tile sequence: all requests' tiles are summed
-  // and scanned by the block, in one go for up to kThreads requests.
-  const int upt = p.TT * S::kTilesPerUnit;
-  int total = 0, begin[S::kStreams], count[S::kStreams];
-  const bool once = B <= S::kThreads;
-  for (int pass = once ? 1 : 0; pass < 2; ++pass) {
-    int base = 0;
-    for (int c = 0; c < B; c += S::kThreads) {
-      uint32_t st = 0;
-      const int b = c + tid;
-      const int w = b < B ? request(a, upt, b, st).weight : 0;
-      if (blockIdx.x == 0 && pass == 1) report(a.bt.status, st);
-      int incl = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += v;
-      }
-      __syncthreads();
-      if (lane == 31) sh_scan[warp] = incl;
-      __syncthreads();
-      int before = base, all = 0;
-      for (int k = 0; k < S::kWarps; ++k) {
-        if (k < warp) before += sh_scan[k];
-        all += sh_scan[k];
-      }
-      base += all;
-      if (once) total = all;
-      if (pass == 1) {
-        const int excl = before + incl - w, N = min(p.ranges, total);
-#pragma unroll
-        for (int s = 0; s < S::kStreams; ++s) {
-          const int i = static_cast<int>(blockIdx.x + s * gridDim.x);
-          begin[s] = i < N ? range_start(i, N, total) : total;
-          count[s] = i < N ? range_start(i + 1, N, total) - begin[s] : 0;
-          if (w > 0 && begin[s] >= excl && begin[s] < excl + w) {
-            rc[s].b0 = b;
-            sh_rem[s] = begin[s] - excl;
-          }
-        }
-        if (blockIdx.x == 0 && b < B) p.pre[b] = excl;
-      }
-    }
-    if (pass == 0) total = base;
-  }
-  if (blockIdx.x == 0 && tid == 0) p.head[0] = total;
-  __syncthreads();
-#pragma unroll
-  for (int s = 0; s < S::kStreams; ++s) {
-    const int i = tid - s * kReqCache;
-    if (count[s] > 0 && i >= 0 && i < kReqCache && rc[s].b0 + i < B) {
-      uint32_t st = 0;
-      int L, n;
-      lengths(a.bt, rc[s].b0 + i, L, n, st);
-      rc[s].len[i] = make_int2(L, n);
-    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  sv::pdl_wait();
+  sv::pdl_launch_dependents();
+
+  // Every warp finds its stream's range for itself.
+  const int upt = p.TT * S::kTilesPerUnit;
   uint32_t *const err = p.err;
   bool ok = true;
-  Walk walk[S::kStreams];
-#pragma unroll
-  for (int s = 0; s < S::kStreams; ++s) walk[s].left = count[s];
-  // Steps to the next tile of a stream's range, or (begin) to its first.
-  const auto advance = [&](Cursor &c, int s, bool begin = false) {
-    step_to(a, upt, rc[s], walk[s], c, begin, sh_rem[s]);
-  };
-
+  int total = 0;
+  {
+    uint32_t st = 0;
+#pragma unroll 4
+    for (int b = lane; b < a.bt.B; b += 32) total += weight_of(a, upt, b, st);
+    total = __reduce_add_sync(kFull, total);
+    if (blockIdx.x == 0 && warp == 0) report(a.bt.status, st);
+  }
+  // A range's loads, in order: K of its first tile, then for each tile its V
+  // and the next tile's K; a tile's stages from its last keys (V: their P is
+  // ready first) or its first ones (K).
   if (warp < 8) {
     // ------------------------------------------------ softmax warpgroups ----
     const int s = warp >> 2;                 // stream
@@ -543,24 +491,24 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t col_s = lanes + kColS + 128u * s, col_o = lanes + kColO + 128u * s;
     const int my = wq * 32 + lane;           // row of the 128-row tile
-    constexpr int kR = S::kStreams - 1;
-    const int rs = s & kR;                   // range of the block
+    const int rs = kPair ? 0 : s;            // range of the block
     uint32_t ph_s = 0, ph_o = 0;
-    int seg = 0;
-    for (; ok; ++seg) {
-      Seg next_seg;
-      if (!walk_next(a, upt, rc[rs], walk[rs], next_seg, seg == 0 ? sh_rem[rs] : -1)) break;
-      const Seg sg = next_seg;
-      const Req r = sg.r;
-      const int nt = sg.t1 - sg.t0;
+    Walk walk;
+    begin_walk(a, upt, static_cast<int>(blockIdx.x + rs * gridDim.x), p.ranges, total, walk);
+#pragma unroll 1
+    while (ok && walk.on) {
+      const Walk sg = walk;
+      const Req &r = sg.r;
+      const int nt = sg.t1 - sg.t0, seg = sg.seg;
       // Tokens and rows of this stream's tile.
       const int tok0 = sg.mp * upt + (kPair ? s * p.TT : 0);
       const int tile_rows = min(max(r.n - tok0, 0), p.TT) * a.G;
       const bool active = wq * 32 < tile_rows;               // warp-uniform
       const int t_row = tok0 + min(my, max(tile_rows - 1, 0)) / a.G;
-      const int full_end = min(r.L, r.kv_end);               // every row sees these
+      const int full_end = sg.new0();                        // every row sees these
       const uint8_t *mrow = a.mask ? a.mask + sg.b * a.msb + static_cast<int64_t>(t_row) * a.bt.T : nullptr;
       float m_ref = -INFINITY, mc = 0.f, l = 0.f;            // mc = m_ref * c, 0 before a key is seen
+#pragma unroll 1
       for (int j = 0; j < nt; ++j) {
         // Which of the tile's keys the row sees, while S is being computed.
         const int k0 = (sg.t0 + j) * kTile;
@@ -598,7 +546,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
                 put(bits, o + r.L - k0);
               }
             } else {
-#pragma unroll 4
+#pragma unroll 1
               for (int o = o0; o < o1; ++o) put(ld8(mrow + o) != 0, o + r.L - k0);
             }
             vis[0] |= static_cast<uint32_t>(lo);
@@ -752,452 +700,392 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           uint32_t o[32];
           tc_ld32(col_o + c, o);
           tc_wait_ld(o);
-          float v[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]);
           if (mine) {
             if (whole) {
 #pragma unroll
               for (int k = 0; k < 32; k += 8) {
                 uint32_t u[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) u[e] = pack2<Q>(v[k + 2 * e] * inv, v[k + 2 * e + 1] * inv);
+                for (int e = 0; e < 4; ++e)
+                  u[e] = pack2<Q>(__uint_as_float(o[k + 2 * e]) * inv, __uint_as_float(o[k + 2 * e + 1]) * inv);
                 *reinterpret_cast<uint4 *>(orow + (c + k) * 2) = make_uint4(u[0], u[1], u[2], u[3]);
               }
             } else {
 #pragma unroll
               for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<float4 *>(slot + (static_cast<size_t>((c + k) >> 2) * p.slot_rows + base_row +
-                                                    my) * 4) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                *reinterpret_cast<uint4 *>(slot + (static_cast<size_t>((c + k) >> 2) * p.slot_rows + base_row +
+                                                   my) * 4) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
             }
           }
           __syncwarp();  // the warp's loads from TMEM are executed together
         }
       }
       tc_fence_before();   // O is read before the next P is announced
+      walk.t = walk.t1 - 1;
+      next_tile(a, upt, walk);
     }
-  } else if (warp == 8) {
-    // --------------------------------------------------------- producer ----
-    // Lane i looks up box i of a tile, an elected lane issues all copies.
-    const int nb = kTile / p.box;                       // boxes per tile, at most 16
+  } else if (warp < 10) {
+    // -------------------------------------------------------- producers ----
+    // One warp per stream, or (kPair) one for K and one for V.  Lane i looks
+    // up box i of a tile, an elected lane issues the copies (~90 cycles each).
+    const int s = warp - 8, rs = kPair ? 0 : s;
+    const int box = p.box, nb = kTile / box;                  // boxes of a tile, at most 16
+    const int nbp = nb / S::kParts;                           // and of a stage
     constexpr int kRing = S::kRaw ? S::kRawStages : S::kStages;
-    uint64_t *const fullb = S::kRaw ? bars.rfull : bars.full;
-    uint64_t *const emptyb = S::kRaw ? bars.rempty : bars.empty;
-    int it = 0, q_issued[2] = {0, 0};
-    // A step whose block numbers are on their way: fetched a turn before they
-    // are used, for the tables' latency would otherwise bound the loads.
-    struct Step {
-      Cursor c;
-      int id, row;                           // this lane's box; id -2: none
+    uint64_t *const fullb = S::kRaw ? rings[rs].rfull : rings[rs].full;
+    uint64_t *const emptyb = S::kRaw ? rings[rs].rempty : rings[rs].empty;
+    const uint32_t stage0 = S::kRaw ? sv::smem_addr(raw0) + rs * (S::kRawStages * S::kRawBytes)
+                                    : sv::smem_addr(ring0) + rs * (S::kStages * S::kStageBytes);
+    constexpr int kRingBytes = S::kRaw ? S::kRawBytes : S::kStageBytes;
+    int issued = -1, q_issued = 0;                      // last position, Q loads
+    // This lane's box of a tile: its block (-2: none) and the row in it.
+    struct Box {
+      int id, row;
     };
-    const auto fetch = [&](const Cursor &c) {
-      Step k;
-      k.c = c;
-      k.id = -2;
-      k.row = 0;
-      const int pos = c.t * kTile + lane * p.box;
-      if (c.on && lane < nb && pos < c.kv_end) {
+    const auto fetch = [&](const Walk &w) {
+      Box x = {-2, 0};
+      const int pos = w.t * kTile + lane * box;
+      if (w.on && lane < nb && pos < w.r.kv_end) {
         const int j = pos / a.c.bs;
-        k.row = pos - j * a.c.bs;
-        k.id = ld32(a.c.tables + static_cast<size_t>(c.b) * a.c.max_blocks + j);
+        x.row = pos - j * a.c.bs;
+        x.id = ld32(a.c.tables + static_cast<size_t>(w.b) * a.c.max_blocks + j);
       }
-      return k;
+      return x;
     };
     // A block that is not there marks the segment, whose unit is recomputed;
     // any block is loaded in its place.
-    const auto settle = [&](Step &k, int rs) {
-      const bool box = lane < nb && k.c.t * kTile + lane * p.box < k.c.kv_end;
-      if (box && (k.id < 0 || k.id >= a.c.num_blocks)) {
-        report(a.bt.status, k.id == -1 ? SV_KV_MISSING_BLOCK : SV_KV_BAD_BLOCK);
-        seg_bad[rs][k.c.seg % kSegRing] = k.c.seg + 1;
-        k.id = 0;
+    const auto settle = [&](Box &x, const Walk &w) {
+      const bool in = lane < nb && w.t * kTile + lane * box < w.r.kv_end;
+      if (in && (x.id < 0 || x.id >= a.c.num_blocks)) {
+        report(a.bt.status, x.id == -1 ? SV_KV_MISSING_BLOCK : SV_KV_BAD_BLOCK);
+        seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
+        x.id = 0;
       }
-      if (!box) k.id = -2;
+      if (!in) x.id = -2;
+    };
+    // A tile's K or V into the stages from position `pos` on.
+    const auto load = [&](const Box &x, int h, bool is_v, int pos) {
+      const CUtensorMap *map = is_v ? &p.vmap : &p.kmap;
+      constexpr int srow = D / SV_KV_GROUP;
+      const uint32_t box_bytes = S::kRaw ? box * (D + srow) : S::kHalves * box * 128;
+      const int boxes = __popc(__ballot_sync(kFull, x.id >= 0));   // the first ones
+#pragma unroll 1
+      for (int q = 0; q < S::kParts; ++q, ++pos) {
+        const int part = is_v ? S::kParts - 1 - q : q, st = pos % kRing;
+        if (pos >= kRing && !wait_warp(&emptyb[st], pos / kRing - 1, err)) return false;
+        const uint32_t bar = sv::smem_addr(&fullb[st]), dst = stage0 + st * kRingBytes;
+        const int i0 = part * nbp, i1 = min(i0 + nbp, boxes);
+        if (elect_one()) sv::mbar_arrive_expect_tx(bar, max(i1 - i0, 0) * box_bytes);
+        __syncwarp();
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i) {
+          const int id = __shfl_sync(kFull, x.id, i), row = __shfl_sync(kFull, x.row, i);
+          const int at = (i - i0) * box;     // row in the stage
+          if (elect_one()) {
+            if constexpr (S::kRaw) {
+              tma_4d(dst + at * D, map, 0, row, h, id, bar);
+              bulk_1d(dst + S::kRawData + at * srow,
+                      (is_v ? a.c.vs : a.c.ks) + id * a.c.sblock_bytes +
+                          (static_cast<int64_t>(h) * a.c.bs + row) * srow,
+                      box * srow, bar);
+            } else {
+#pragma unroll
+              for (int hf = 0; hf < S::kHalves; ++hf)
+                tma_4d(dst + hf * S::kHalf + at * 128, map, hf * 64, row, h, id, bar);
+            }
+          }
+          __syncwarp();
+        }
+        issued = pos;
+      }
+      return true;
     };
     // A segment's queries: whole tokens, G heads each, in the swizzled layout.
-    const auto load_q = [&](const Cursor &c, int rs) {
-      if (lane == 0 && c.cut) report(a.bt.status, SV_KV_TABLE_SHORT);
-      if (c.seg > 0 && !wait_warp(&bars.q_empty[rs], (c.seg - 1) & 1, err)) return false;
+    const auto load_q = [&](const Walk &w) {
+      if (lane == 0 && w.r.kv_end < w.r.L + w.r.n) report(a.bt.status, SV_KV_TABLE_SHORT);
+      if (w.seg > 0 && !wait_warp(&bars.q_empty[rs], w.seg - 1, err)) return false;
+      if (kPair && w.seg > 0 && !wait_warp(&bars.q_empty[1], w.seg - 1, err)) return false;
       const uint32_t bar = sv::smem_addr(&bars.q_full[rs]);
-      const uint32_t bytes = S::kTilesPerUnit * S::kHalves * p.qbox * a.G * 128;
       if (elect_one()) {
-        sv::mbar_arrive_expect_tx(bar, bytes);
+        sv::mbar_arrive_expect_tx(bar, S::kTilesPerUnit * S::kHalves * p.qbox * a.G * 128);
 #pragma unroll
         for (int i = 0; i < S::kTilesPerUnit; ++i)
 #pragma unroll
           for (int hf = 0; hf < S::kHalves; ++hf)
-            tma_4d(sv::smem_addr(sq) + (kPair ? i : rs) * S::kStageBytes + hf * (kTile * 128), &p.qmap,
-                   hf * 64, c.h * a.G, c.mp * upt + i * p.TT, c.b, bar);
+            tma_4d(sv::smem_addr(sq) + (kPair ? i : rs) * S::kQTile + hf * (kTile * 128), &p.qmap,
+                   hf * 64, w.h * a.G, w.mp * upt + i * p.TT, w.b, bar);
       }
       __syncwarp();
-      ++q_issued[rs];
+      ++q_issued;
       return true;
     };
-    const auto load = [&](const Step &k, bool is_v) {
-      const int st = it % kRing;
-      if (it >= kRing && !wait_warp(&emptyb[st], (it / kRing) & 1 ? 0u : 1u, err)) return false;
-      const uint32_t bar = sv::smem_addr(&fullb[st]);
-      const int boxes = __popc(__ballot_sync(kFull, k.id >= 0));   // the first ones
-      constexpr int srow = D / SV_KV_GROUP;
-      const uint32_t box_bytes = S::kRaw ? p.box * (D + srow) : S::kHalves * p.box * 128;
-      const CUtensorMap *map = is_v ? &p.vmap : &p.kmap;
-      const uint32_t dst =
-          S::kRaw ? sv::smem_addr(raw + st * S::kRawBytes) : sv::smem_addr(ring + st * S::kStageBytes);
-      if (elect_one()) sv::mbar_arrive_expect_tx(bar, boxes * box_bytes);
-      __syncwarp();
-      for (int i = 0; i < boxes; ++i) {
-        const int id = __shfl_sync(kFull, k.id, i), row = __shfl_sync(kFull, k.row, i);
-        if (elect_one()) {
-          if constexpr (S::kRaw) {
-            tma_4d(dst + i * p.box * D, map, 0, row, k.c.h, id, bar);
-            bulk_1d(dst + S::kRawData + i * p.box * srow,
-                    (is_v ? a.c.vs : a.c.ks) + id * a.c.sblock_bytes +
-                        (static_cast<int64_t>(k.c.h) * a.c.bs + row) * srow,
-                    p.box * srow, bar);
-          } else {
-#pragma unroll
-            for (int hf = 0; hf < S::kHalves; ++hf)
-              tma_4d(dst + hf * (kTile * 128) + i * p.box * 128, map, hf * 64, row, k.c.h, id, bar);
-          }
-        }
-        __syncwarp();
-      }
-      ++it;
-      return true;
-    };
+    Walk w;
+    begin_walk(a, upt, static_cast<int>(blockIdx.x + rs * gridDim.x), p.ranges, total, w);
+    Box x = fetch(w);
     if constexpr (kPair) {
-      // K0 V0 K1 V1 ...; a segment's queries behind its first tiles.
-      Cursor c;
-      advance(c, 0, true);
-      Step next = fetch(c);
 #pragma unroll 1
-      while (ok && next.c.on) {
-        Step k = next;
-        advance(c, 0);
-        next = fetch(c);
-        settle(k, 0);
-#pragma unroll 1
-        for (int v = 0; ok && v < 2; ++v) ok = load(k, v);
-        if (ok && k.c.first()) ok = load_q(k.c, 0);
+      for (int i = 0; ok && w.on; ++i) {
+        Box now = x;
+        settle(now, w);
+        const bool first = w.first() && s == 0;
+        const Walk at = w;
+        next_tile(a, upt, w);
+        x = fetch(w);                        // on its way while the stage is waited for
+        ok = load(now, at.h, s == 1, 2 * i + s);
+        if (ok && first) ok = load_q(at);
       }
-    } else {
-      // K of both streams, then by turns V and the next K of each.  A new
-      // segment's queries follow the other stream's turn: by then the products
-      // that read the buffer have most likely ended.  One turn's code serves
-      // both streams, whose states change places after it.
-      struct State {
-        Cursor c;
-        Step now, next;
-        bool q_due;
-      } me, other;
-      int s = 0;
-      me.q_due = other.q_due = false;
-      me.now.c.on = other.now.c.on = false;
+    } else if (w.on) {
+      int pos = 0;
+      Walk at = w;
+      Box now = x;
+      settle(now, at);
+      next_tile(a, upt, w);
+      x = fetch(w);                          // on its way while stages are waited for
+      ok = load(now, at.h, false, pos) && load_q(at);
+      pos += S::kParts;
 #pragma unroll 1
-      for (int turn = 0; ok && (turn < 2 || me.now.c.on || other.now.c.on); ++turn) {
-        if (turn < 2) {
-          advance(me.c, s, true);
-          me.next = fetch(me.c);
-          me.now.c.on = me.next.c.on;
-        } else if (me.now.c.on) {
-          ok = load(me.now, true);
-        }
-        if (ok && me.now.c.on) {
-          me.now = me.next;
-          if (me.now.c.on) {
-            advance(me.c, s);
-            me.next = fetch(me.c);
-            settle(me.now, s);
-            me.q_due = me.now.c.first();
-            ok = load(me.now, false);
-          }
-        }
-        if (ok && other.q_due) {
-          ok = load_q(other.now.c, 1 - s);
-          other.q_due = false;
-        }
-        if (ok && me.q_due && (turn < 2 || !other.now.c.on)) {
-          ok = load_q(me.now.c, s);
-          me.q_due = false;
-        }
-        swap2(me, other);
-        s = 1 - s;
+      while (ok) {
+        ok = load(now, at.h, true, pos);
+        pos += S::kParts;
+        if (!ok || !w.on) break;
+        at = w;
+        now = x;
+        settle(now, at);
+        next_tile(a, upt, w);
+        x = fetch(w);
+        ok = load(now, at.h, false, pos);
+        pos += S::kParts;
+        if (ok && at.first()) ok = load_q(at);
       }
     }
-    if (!ok) {  // every copy in flight lands before the block ends
-      for (int k = max(0, it - kRing); k < it; ++k) wait_warp(&fullb[k % kRing], (k / kRing) & 1, err);
-#pragma unroll
-      for (int s = 0; s < S::kStreams; ++s)
-        if (q_issued[s] > 0) wait_warp(&bars.q_full[s], (q_issued[s] - 1) & 1, err);
+    if (!ok) {  // copies in flight land before the block ends (a position not issued: the wait gives up)
+#pragma unroll 1
+      for (int k = max(0, issued - kRing + 1); k <= issued; ++k) wait_warp(&fullb[k % kRing], k / kRing, err);
+      if (q_issued > 0) wait_warp(&bars.q_full[rs], q_issued - 1, err);
     }
-  } else if (warp == 9) {
-    // --------------------------------------------------------------- MMA ----
-    const uint32_t kQK = mma_desc<Q>(kTile, false) | (p.negate ? kNegateA : 0u);
+  } else if (warp < 12) {
+    // -------------------------------------------------------- products ----
+    // One warp per stream issues its Q K^T and P V, in order.
+    const int s = warp - 10, rs = kPair ? 0 : s;
+    const uint32_t kQK = mma_desc<Q>(S::kKeys, false) | (p.negate ? kNegateA : 0u);
     constexpr uint32_t kPV = mma_desc<Q>(D, true);
-    const uint64_t q_desc = smem_desc(sv::smem_addr(sq), 16), k_desc = smem_desc(sv::smem_addr(ring), 16);
-    const uint64_t v_desc = smem_desc(sv::smem_addr(ring), kTile * 128);
-    int it = 0;                    // stages taken, in load order
-    uint32_t ph_p = 0, fix = 0;    // parities: of P per stream, of its repairs per stage
-    const auto take = [&](const Cursor &c, bool is_v) {
-      const int st = it % S::kStages;
-      bool good = wait_warp(&bars.full[st], (it / S::kStages) & 1, err);
-      if (!S::kRaw && good && is_v && (c.t + 1) * kTile > c.new0) {
-        good = wait_warp(&bars.fixed[st], (fix >> st) & 1u, err);
-        fix ^= 1u << st;
-      }
+    uint8_t *const ring = ring0 + rs * (S::kStages * S::kStageBytes);
+    RingBars &rb = rings[rs];
+    const uint64_t q_desc = smem_desc(sv::smem_addr(sq) + s * S::kQTile, 16);
+    const uint64_t k_desc = smem_desc(sv::smem_addr(ring), 16);
+    const uint64_t v_desc = smem_desc(sv::smem_addr(ring), S::kHalf);
+    const uint32_t ts = tmem + kColS + 128u * s, to = tmem + kColO + 128u * s;
+    uint32_t ph_p = 0, fix = 0;    // parities: of P, of the repairs per stage
+    const auto take = [&](int pos) {
+      const bool good = wait_warp(&rb.full[pos % S::kStages], pos / S::kStages, err);
       tc_fence_after();
       return good;
     };
-    auto release = [&]() {
-      if (elect_one()) tc_commit(sv::smem_addr(&bars.empty[it % S::kStages]));
-      ++it;
-    };
-    auto qk = [&](int s) {
-      const uint64_t qd = q_desc + s * (S::kStageBytes >> 4);
-      const uint64_t kd = k_desc + (it % S::kStages) * (S::kStageBytes >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
-          tc_mma_ss(tmem + kColS + 128u * s, qd + off, kd + off, kQK, k > 0);
+    // Not kRaw: rows of V behind the committed tokens, keys k0 .. of a stage.
+    // What lies behind the last token becomes 0, a value that is not finite
+    // marks the segment.
+    const auto repair = [&](const Walk &w, int k0, int st) {
+      uint8_t *base = ring + st * S::kStageBytes;
+      const int r0 = max(w.new0() - k0, 0), r1 = w.r.kv_end - k0;   // new rows [r0, r1)
+      constexpr int kCh = S::kHalves * 8;
+      bool found = false;
+#pragma unroll 2
+      for (int i = lane + r0 * kCh; i < S::kKeys * kCh; i += 32) {
+        const int row = i / kCh, ch = i % kCh;
+        uint4 *v = reinterpret_cast<uint4 *>(base + (ch >> 3) * S::kHalf + row * 128 + (ch & 7) * 16);
+        if (row >= r1) {
+          *v = make_uint4(0, 0, 0, 0);
+        } else {
+          const uint4 y = *v;
+          found = found || odd16<Q>(y.x) || odd16<Q>(y.y) || odd16<Q>(y.z) || odd16<Q>(y.w);
         }
       }
+      if (found) seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
+      fence_async_smem();
       __syncwarp();
     };
-    // Keys 64 .. 127 of the tile first: their P is ready first.
-    auto pv = [&](int s, bool first) {
-      const uint64_t vd = v_desc + (it % S::kStages) * (S::kStageBytes >> 4);
-#pragma unroll
-      for (int half = 1; half >= 0; --half) {
-        if (half == 0) {
-          if (!wait_warp(&bars.p_ready[s], ph_p >> s, err)) return false;
-          ph_p ^= 1u << s;
-        }
-        tc_fence_after();
+    // S of the tile whose K is at `pos`.
+    const auto qk = [&](const Walk &w, int pos) {
+      if (w.first() && !wait_warp(&bars.q_full[rs], w.seg, err)) return false;
+#pragma unroll 1
+      for (int part = 0; part < S::kParts; ++part, ++pos) {
+        if (!take(pos)) return false;
+        const uint64_t kd = k_desc + (pos % S::kStages) * (S::kStageBytes >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 4 * half; k < 4 * half + 4; ++k)
-            tc_mma_ts(tmem + kColO + 128u * s, tmem + kColS + 128u * s + kPOff + 8u * k,
-                      vd + k * (2048 >> 4), kPV, !(first && k == 4));
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma_ss(ts + part * S::kKeys, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
+                      kd + (((k >> 2) * S::kHalf + (k & 3) * 32) >> 4), kQK, k > 0);
+          tc_commit(sv::smem_addr(&rb.empty[pos % S::kStages]));
+          if (part == S::kParts - 1) {
+            tc_commit(sv::smem_addr(&bars.s_full[s]));
+            if (w.last()) tc_commit(sv::smem_addr(&bars.q_empty[s]));
+          }
         }
         __syncwarp();
       }
       return true;
     };
-    auto commit = [&](uint64_t *bar) {
-      if (elect_one()) tc_commit(sv::smem_addr(bar));
-    };
-    if constexpr (kPair) {
-      // S of both streams for step c, whose K is stage `it`.
-      const auto products = [&](const Cursor &c, int s) {
-        if (s == 0) {
-          if (c.first() && !wait_warp(&bars.q_full[0], c.seg, err)) return false;
-          if (!take(c, false)) return false;
-        }
-        qk(s);
-        commit(&bars.s_full[s]);
-        if (s == 1) {
-          release();
-          if (c.last()) commit(&bars.q_empty[0]);
-        }
-        return true;
-      };
-      // One turn is one stream's P V and its next Q K^T; the first two turns
-      // have only the latter.  V's stage is `it`, the next K's the one after.
-      Cursor c, n;
-      advance(n, 0, true);
-      c.on = false;
+    // O += P V, keys 64 .. 127 of the tile first: their P is ready first.
+    const auto pv = [&](const Walk &w, int pos) {
 #pragma unroll 1
-      for (int turn = 0; ok && (n.on || c.on); ++turn) {
-        const int s = turn & 1;
-        if (turn >= 2) {
-          ok = wait_warp(&bars.p_half[s], ph_p >> s, err) && (s == 1 || take(c, true)) && pv(s, c.first());
-          if (!ok) break;
-          if (s == 1) release();                     // V
-          if (c.last()) commit(&bars.o_done[s]);
-          if (n.on) {
-            if (s == 0) ++it;
-            ok = products(n, s);
-            if (s == 0) --it;
+      for (int half = 1; half >= 0; --half) {
+        const int st = pos % S::kStages;
+        if (half == 1 || S::kParts == 2) {            // a stage begins
+          if (!take(pos)) return false;
+          const int k0 = w.t * kTile + (S::kParts == 2 ? half * S::kKeys : 0);
+          if (!S::kRaw && k0 + S::kKeys > w.new0()) {
+            if (!kPair || s == 0) {
+              repair(w, k0, st);
+              if (kPair && lane == 0) sv::mbar_arrive(sv::smem_addr(&rb.fixed[st]));
+            } else {
+              if (!wait_warp(&rb.fixed[st], fix >> st, err)) return false;
+              fix ^= 1u << st;
+            }
           }
-        } else {
-          ok = products(n, s);
         }
-        if (s == 1) {                                // both streams have taken the step
-          c = n;
-          if (n.on) advance(n, 0);
+        if (!wait_warp(half ? &bars.p_half[s] : &bars.p_ready[s], ph_p, err)) return false;
+        tc_fence_after();
+        // Its 64 keys: rows 64 * half .. of a whole tile, or all of a half one.
+        const uint64_t vd = v_desc + st * (S::kStageBytes >> 4) + (S::kParts == 1 ? half * (64 * 128 >> 4) : 0);
+        const uint32_t first = w.first() && half == 1;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_ts(to, ts + kPOff + 32u * half + 8u * k, vd + k * (2048 >> 4), kPV, !(first && k == 0));
+          if (half == 0 || S::kParts == 2) tc_commit(sv::smem_addr(&rb.empty[st]));
+          if (half == 0 && w.last()) tc_commit(sv::smem_addr(&bars.o_done[s]));
         }
+        __syncwarp();
+        if (S::kParts == 2) ++pos;
       }
-    } else {
-      Cursor me, other;
-      int s = 0;
-      me.on = other.on = false;
+      ph_p ^= 1u;
+      return true;
+    };
+    Walk w;
+    begin_walk(a, upt, static_cast<int>(blockIdx.x + rs * gridDim.x), p.ranges, total, w);
+    if (w.on) {
+      int pos = 0;
+      ok = qk(w, pos);
+      pos += S::kParts;
 #pragma unroll 1
-      for (int turn = 0; ok && (turn < 2 || me.on || other.on); ++turn) {
-        if (turn < 2) {
-          advance(me, s, true);
-        } else if (me.on) {
-          ok = wait_warp(&bars.p_half[s], ph_p >> s, err) && take(me, true) && pv(s, me.first());
-          release();
-          if (me.last()) commit(&bars.o_done[s]);
-          advance(me, s);
-        }
-        if (ok && me.on) {
-          ok = (!me.first() || wait_warp(&bars.q_full[s], me.seg, err)) && take(me, false);
-          if (ok) {
-            qk(s);
-            commit(&bars.s_full[s]);
-            release();
-            if (me.last()) commit(&bars.q_empty[s]);
-          }
-        }
-        swap2(me, other);
-        s = 1 - s;
+      while (ok) {
+        ok = pv(w, pos);
+        pos += S::kParts;
+        if (!ok) break;
+        next_tile(a, upt, w);
+        if (!w.on) break;
+        ok = qk(w, pos);
+        pos += S::kParts;
       }
     }
     if (!ok) {  // issued products end before TMEM is freed
-      if (elect_one()) tc_commit(sv::smem_addr(&bars.drain));
+      if (elect_one()) tc_commit(sv::smem_addr(&bars.drain[s]));
       __syncwarp();
-      wait_warp(&bars.drain, 0, err);
+      wait_warp(&bars.drain[s], 0, err);
     }
   } else {
-    // ------------------------------------------------------------ helpers ----
-    const int ht = tid - 320;                           // helper thread
-    constexpr int kHT = S::kHelpers * 32;
-    int it = 0, rit = 0;
-    uint32_t found = 0;
-    // Not kRaw: V tiles that reach past the committed tokens, in place.
-    const auto repair = [&](const Cursor &c) {
-      const int st = it % S::kStages;
-      uint8_t *base = ring + st * S::kStageBytes;
-      const int k0 = c.t * kTile, r0 = max(c.new0 - k0, 0), r1 = c.kv_end - k0;  // new rows [r0, r1)
-      constexpr int kCh = S::kHalves * 8;
-      for (int i = ht + r0 * kCh; i < kTile * kCh; i += kHT) {
-        const int row = i / kCh, ch = i % kCh;
-        uint4 *w = reinterpret_cast<uint4 *>(base + (ch >> 3) * (kTile * 128) + row * 128 + (ch & 7) * 16);
-        if (row >= r1) {
-          *w = make_uint4(0, 0, 0, 0);
-        } else {
-          const uint4 v = *w;
-          if (odd16<Q>(v.x) || odd16<Q>(v.y) || odd16<Q>(v.z) || odd16<Q>(v.w)) found = 1;
-        }
-      }
-    };
-    // kRaw: 16 codes at a time, widened into the swizzled layout.
-    const auto widen = [&](const Cursor &c, bool is_v) {
-      const int st = it % S::kStages, rs = rit % (S::kRaw ? S::kRawStages : 1);
-      if (!wait_warp(&bars.rfull[rs], (rit / (S::kRaw ? S::kRawStages : 1)) & 1, err)) return false;
-      if (it >= S::kStages && !wait_warp(&bars.empty[st], (it / S::kStages) & 1 ? 0u : 1u, err)) return false;
-      const uint8_t *src = raw + rs * S::kRawBytes;
-      const uint8_t *sc = src + S::kRawData;
-      uint8_t *dst = ring + st * S::kStageBytes;
-      constexpr int kCh = D / 16;                       // 16-code chunks per row
-      const int k0 = c.t * kTile, r0 = max(c.new0 - k0, 0), r1 = is_v ? c.kv_end - k0 : kTile;
-      const bool look = is_v && k0 + kTile > c.new0;
+    // ------------------------------------------------------------ wideners ----
+    // e4m3 stages, 16 codes at a time, into the swizzled 16-bit layout; rows of
+    // V behind the committed tokens are repaired on the way.
+    constexpr int kRW = S::kRaw ? S::kRingWideners : 1, kRS = S::kRaw ? S::kRawStages : 1;
+    const int rs = kPair ? 0 : (warp - 12) / kRW, ht = (warp - 12 - rs * kRW) * 32 + lane;
+    RingBars &rb = rings[rs];
+    uint8_t *const ring = ring0 + rs * (S::kStages * S::kStageBytes);
+    uint8_t *const raw = raw0 + rs * (S::kRawStages * S::kRawBytes);
+    // A tile's K or V from position `pos` on.
+    const auto widen = [&](const Walk &w, bool is_v, int pos) {
+#pragma unroll 1
+      for (int q = 0; q < S::kParts; ++q, ++pos) {
+        const int st = pos % S::kStages, rst = pos % kRS;
+        const int k0 = w.t * kTile + (is_v ? S::kParts - 1 - q : q) * S::kKeys;
+        if (!wait_warp(&rb.rfull[rst], pos / kRS, err)) return false;
+        if (pos >= S::kStages && !wait_warp(&rb.empty[st], pos / S::kStages - 1, err)) return false;
+        const uint8_t *src = raw + rst * S::kRawBytes;
+        const uint8_t *sc = src + S::kRawData;
+        uint8_t *dst = ring + st * S::kStageBytes;
+        constexpr int kCh = D / 16;                     // 16-code chunks per row
+        const int r0 = max(w.new0() - k0, 0), r1 = is_v ? w.r.kv_end - k0 : S::kKeys;
+        const bool look = is_v && k0 + S::kKeys > w.new0();
+        bool found = false;
 #pragma unroll 4
-      for (int i = ht; i < kTile * kCh; i += kHT) {
-        const int row = i / kCh, ch = i % kCh;
-        const uint4 w = *reinterpret_cast<const uint4 *>(src + i * 16);
-        const float m = scale_value(sc[row * (D / SV_KV_GROUP) + (ch >> 1)]);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        uint32_t o[8];
+        for (int i = ht; i < S::kKeys * kCh; i += kRW * 32) {
+          const int row = i / kCh, ch = i % kCh;
+          const uint4 c = *reinterpret_cast<const uint4 *>(src + i * 16);
+          const float m = scale_value(sc[row * (D / SV_KV_GROUP) + (ch >> 1)]);
+          const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+          uint32_t o[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-              static_cast<__nv_fp8x2_storage_t>(u[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-          o[k] = pack2<Q>(f.x * m, f.y * m);
-        }
-        if (look && row >= r0) {
-          if (row >= r1) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = 0;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (odd16<Q>(o[k])) found = 1;
+          for (int k = 0; k < 8; ++k) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                static_cast<__nv_fp8x2_storage_t>(u[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            o[k] = pack2<Q>(f.x * m, f.y * m);
           }
+          if (look && row >= r0) {
+            if (row >= r1) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] = 0;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) found = found || odd16<Q>(o[k]);
+            }
+          }
+          // Odd chunk pairs are written in the other order: the two 64-column
+          // halves of a row lie in the same banks.
+          uint8_t *d = dst + (ch >> 2) * S::kHalf + row * 128;
+          const int c0 = (ch & 3) * 2, sw = row & 7;
+          const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+          const bool swap = ch >> 2;
+          *reinterpret_cast<uint4 *>(d + (((c0 + (swap ? 1 : 0)) ^ sw) << 4)) = swap ? hi : lo;
+          *reinterpret_cast<uint4 *>(d + (((c0 + (swap ? 0 : 1)) ^ sw) << 4)) = swap ? lo : hi;
         }
-        // Odd chunk pairs are written in the other order: the two 64-column
-        // halves of a row lie in the same banks.
-        uint8_t *d = dst + (ch >> 2) * (kTile * 128) + row * 128;
-        const int c0 = (ch & 3) * 2, sw = row & 7;
-        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-        const bool swap = ch >> 2;
-        *reinterpret_cast<uint4 *>(d + (((c0 + (swap ? 1 : 0)) ^ sw) << 4)) = swap ? hi : lo;
-        *reinterpret_cast<uint4 *>(d + (((c0 + (swap ? 0 : 1)) ^ sw) << 4)) = swap ? lo : hi;
-      }
-      return true;
-    };
-    // One stage of the load order.
-    const auto stage = [&](const Cursor &c, bool is_v, int rs) {
-      if constexpr (S::kRaw) {
-        if (!widen(c, is_v)) return false;
-        if (found) seg_bad[rs][c.seg % kSegRing] = c.seg + 1;
-        found = 0;
+        if (found) seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          sv::mbar_arrive(sv::smem_addr(&bars.full[it % S::kStages]));
-          sv::mbar_arrive(sv::smem_addr(&bars.rempty[rit % (S::kRaw ? S::kRawStages : 1)]));
-        }
-        ++rit;
-      } else {
-        // Every stage is looked at, also those that need nothing: a warp that
-        // ran ahead would take an older phase of the barrier for its own, and
-        // one that fell behind would miss a phase.
-        const int st = it % S::kStages;
-        if (!wait_warp(&bars.full[st], (it / S::kStages) & 1, err)) return false;
-        const bool fix = is_v && (c.t + 1) * kTile > c.new0;
-        if (fix) {
-          repair(c);
-          if (found) seg_bad[rs][c.seg % kSegRing] = c.seg + 1;
-          found = 0;
-          fence_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) {
-          if (fix) sv::mbar_arrive(sv::smem_addr(&bars.fixed[st]));
-          sv::mbar_arrive(sv::smem_addr(&bars.empty[st]));
+          sv::mbar_arrive(sv::smem_addr(&rb.full[st]));
+          sv::mbar_arrive(sv::smem_addr(&rb.rempty[rst]));
         }
       }
-      ++it;
       return true;
     };
-    if constexpr (kPair) {
-      Cursor c;
-      advance(c, 0, true);
+    Walk k, v;                             // the next K and the next V
+    begin_walk(a, upt, static_cast<int>(blockIdx.x + rs * gridDim.x), p.ranges, total, k);
+    v = k;
+    int pos = 0;
 #pragma unroll 1
-      for (int v = 0; ok && c.on; v ^= 1) {
-        ok = stage(c, v, 0);
-        if (v) advance(c, 0);
-      }
-    } else {
-      // K of both streams, then by turns V and the next K of each.
-      Cursor me, other;
-      int s = 0;
-      me.on = other.on = false;
-#pragma unroll 1
-      for (int turn = 0; ok && (turn < 4 || me.on || other.on); ++turn) {
-        const bool v = !(turn & 1);                  // turns 0 and 2 begin a stream instead
-        if (turn < 4 && v) {
-          advance(me, s, true);
-        } else if (me.on) {
-          ok = stage(me, v, s);
-          if (v) advance(me, s);
-        }
-        if (!v) {
-          swap2(me, other);
-          s = 1 - s;
-        }
-      }
+    for (bool is_v = false; ok && v.on; is_v = !is_v) {
+      Walk &w = is_v ? v : k;
+      if (!w.on) continue;                 // no next K
+      ok = widen(w, is_v, pos);
+      pos += S::kParts;
+      next_tile(a, upt, w);
     }
   }
 
+  // For the second kernel: where each request's tiles begin.
+  if (blockIdx.x == 0 && warp == 8) {
+    uint32_t st = 0;
+    int base = 0;
+#pragma unroll 1
+    for (int c = 0; c < a.bt.B; c += 32) {
+      const int x = weight_of(a, upt, c + lane, st);
+      int incl = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (c + lane < a.bt.B) p.pre[c + lane] = base + incl - x;
+      base += __shfl_sync(kFull, incl, 31);
+    }
+    if (lane == 0) p.head[0] = total;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tc_dealloc(tmem, 512);
+  if (warp == 11) tc_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------- second kernel ----
@@ -1221,7 +1109,14 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
   const int tok0 = mp * upt, rows = min(upt, r.n - tok0) * a.G;
   const int total = ld32(p.head), start = ld32(p.pre + b) + (h * r.mp + mp) * r.kt;
   const int N = min(p.ranges, total);
-  const int c0 = range_of(start, N, total), c1 = range_of(start + r.kt - 1, N, total);
+  // The range a tile is in: an estimate, put right.
+  const auto range_of = [&](int tile) {
+    int i = min(N - 1, static_cast<int>(static_cast<float>(tile) / static_cast<float>(total) * N));
+    while (range_start(i, N, total) > tile) --i;
+    while (i + 1 < N && range_start(i + 1, N, total) <= tile) ++i;
+    return i;
+  };
+  const int c0 = range_of(start), c1 = range_of(start + r.kt - 1);
   const int late = range_start(c0, N, total) == start ? 0 : 1;  // not the first segment of range c0
   auto slot_of = [&](int c) {
     return p.slots + (static_cast<size_t>(c) * 2 + (c == c0 ? late : 0)) * p.slot_floats;

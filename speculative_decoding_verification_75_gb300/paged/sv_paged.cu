@@ -354,8 +354,9 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
   p.slot_rows = w.slot_rows;
   p.slot_floats = w.slot_floats;
   p.MP = w.MP;
-  p.box = 8;
-  while (p.box < kTile && ap.c.bs % (2 * p.box) == 0) p.box *= 2;
+  const bool pair = ap.bt.T > w.TT;
+  p.box = 8;  // a power of two that divides the block size, at most a stage
+  while (p.box < (pair ? kTile : kTile / 2) && ap.c.bs % (2 * p.box) == 0) p.box *= 2;
   p.c = std::max(std::fabs(ap.scale_log2), 1e-30f);
   p.negate = ap.scale_log2 < 0.f;
   p.TT = w.TT;
@@ -364,7 +365,6 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
            make_map(p.vmap, ap.c, ap.c.v, a->cache.dtype, p.box) &&
            make_query_map(p.qmap, ap, a->dtype, p.qbox);
   if (!*taken) return SV_OK;  // strides that no tensor map describes
-  const bool pair = ap.bt.T > w.TT;
   p.ranges = std::min(nsm, kMaxGrid) * (pair ? 1 : 2);
   p.mvec = ap.mask && ap.bt.T % 4 == 0 && aligned(ap.mask, 4) && ap.msb % 4 == 0;
   if (a->cache.dtype == SV_E4M3) return tc_pick<BF16, E4M3>(p, pair, nsm, dev, stream);

@@ -123,6 +123,25 @@ def test_long_contexts_are_split_and_joined(B, T, L, cdt):
     check(build(rng, B, T, 8, 1, 128, 16, L, None, "tree", "bf16", cdt))
 
 
+MANY = [
+    # Ranges of many tiles: the rings of stages go round several times, units
+    # begin and end within a range, and short ones lie between.
+    (6, 2, 8, 8, 128, 16, [3000, 2500, 40, 3100, 0, 2222], None, "chain", "bf16", "bf16"),
+    (6, 3, 16, 16, 128, 64, [1500, 2500, 40, 1100, 129, 2222], [3, 1, 0, 2, 3, 3], "tree", "bf16", "e4m3"),
+    (5, 1, 32, 32, 64, 32, [2000, 1000, 1, 127, 1800], None, "chain", "fp16", "fp16"),
+    (5, 2, 32, 32, 64, 8, [2000, 1000, 1, 127, 1500], None, "any", "bf16", "e4m3"),
+    (4, 40, 16, 4, 128, 16, [9000, 20, 5000, 7000], [40, 40, 31, 33], "tree", "bf16", "bf16"),
+    (4, 40, 16, 4, 128, 128, [9000, 20, 5000, 7000], [40, 7, 40, 36], "chain", "bf16", "e4m3"),
+    (4, 70, 8, 4, 64, 32, [6000, 120, 4000, 5000], None, "any", "fp16", "fp16"),
+    (4, 70, 8, 4, 64, 64, [6000, 120, 4000, 5000], None, "tree", "bf16", "e4m3"),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=str)
+def test_ranges_of_many_tiles(case):
+    check(build(np.random.default_rng(len(case[6]) + case[4]), *case))
+
+
 @pytest.mark.parametrize("cdt", ["bf16", "e4m3"])
 def test_many_short_and_one_long(cdt):
     rng = np.random.default_rng(0)
