@@ -33,10 +33,10 @@ struct RowState {
 };
 
 // Positions j0 + lane, j0 + step + lane, ... below `total` of row (b, i) and
-// KV head h, by one warp.  qs: the row as fp32 in shared memory, scaled.
-template <typename C, int kMaxD>
+// KV head h, by one warp.  load_q(d, f): elements d .. d + 7 of the row.
+template <typename C, int kMaxD, typename LoadQ>
 __device__ __forceinline__ void attend(const AttnParams &p, int b, int i, int h, int L, int n,
-                                       int total, const float *qs, int j0, int step, int lane,
+                                       int total, const LoadQ &load_q, int j0, int step, int lane,
                                        RowState<kMaxD> &r, uint32_t &st) {
   const int D = p.c.D, row_bytes = D * C::kBytes, srow = D / SV_KV_GROUP;
   const int64_t head_bytes = static_cast<int64_t>(h) * p.c.bs * row_bytes;
@@ -66,15 +66,18 @@ __device__ __forceinline__ void attend(const AttnParams &p, int b, int i, int h,
         } else {
           raw = ld128(p.c.k + at + d * C::kBytes);
         }
-        float f[8];
+        float f[8], q[8];
         unpack8<C>(&raw, f);
+        load_q(d, q);
         float s8 = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s8 = fmaf(qs[d + e], f[e], s8);
+        for (int e = 0; e < 8; ++e) s8 = fmaf(q[e], f[e], s8);
         if constexpr (C::kBytes == 1) s8 *= scale_value(ld8(p.c.ks + sat + d / SV_KV_GROUP));
         x += s8;
       }
     }
+    x *= p.scale_log2;
+    if (!see) x = -INFINITY;
     // fmaxf drops a NaN: it comes back through 2^(x - m) below.
     const float mt = fmaxf(r.m, sv::warp_max(x));
     const float base = mt == -INFINITY ? 0.f : mt;
@@ -124,6 +127,28 @@ __device__ __forceinline__ void store_row(const AttnParams &p, int64_t row, int 
     p.lse[row] = r.l == 0.f ? -INFINITY : r.m * kLn2 + logf(r.l);
 }
 
+// A whole row by one warp, for query rows on 16-byte boundaries.  Not inlined:
+// the rare way out of the tensor-core kernels.
+template <typename Q, typename C, int D>
+__device__ __noinline__ void recompute_row(const AttnParams &p, int b, int i, int hq) {
+  const int lane = threadIdx.x & 31;
+  uint32_t st = 0;
+  int L, n;
+  lengths(p.bt, b, L, n, st);
+  const uint8_t *q = p.q + b * p.qsb + i * p.qst + hq * p.qsh;
+  const auto load_q = [&](int d, float (&f)[8]) {
+    const uint4 w = ld128(q + d * 2);
+    unpack8<Q>(&w, f);
+  };
+  RowState<D> r;
+  r.m = -INFINITY;
+  r.l = 0.f;
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) r.o[e] = 0.f;
+  attend<C, D>(p, b, i, hq / p.G, L, n, L + n, load_q, 0, 32, lane, r, st);
+  store_row<Q, D>(p, (static_cast<int64_t>(b) * p.bt.T + i) * p.Hq + hq, lane, r);
+}
+
 constexpr int kGenWarps = 4;
 
 // One thread block per (request, new token, head); its warps take every
@@ -150,7 +175,7 @@ __global__ void __launch_bounds__(32 * kGenWarps) sv_attn_general_kernel(const A
   const uint8_t *q = p.q + b * p.qsb + i * p.qst + h * p.qsh;
   for (int d = threadIdx.x; d < p.c.D; d += 32 * kGenWarps) {
     const uint16_t w = static_cast<uint16_t>(ld16(q + 2 * d));
-    qs[d] = load1<Q>(&w) * p.scale_log2;
+    qs[d] = load1<Q>(&w);
   }
   __syncthreads();
   RowState<kMaxD> r;
@@ -158,7 +183,11 @@ __global__ void __launch_bounds__(32 * kGenWarps) sv_attn_general_kernel(const A
   r.l = 0.f;
 #pragma unroll
   for (int e = 0; e < kMaxD / 32; ++e) r.o[e] = 0.f;
-  attend<C, kMaxD>(p, b, i, h / p.G, L, n, L + n, qs, warp * 32, 32 * kGenWarps, lane, r, st);
+  const auto load_q = [&](int d, float (&f)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = qs[d + e];
+  };
+  attend<C, kMaxD>(p, b, i, h / p.G, L, n, L + n, load_q, warp * 32, 32 * kGenWarps, lane, r, st);
 #pragma unroll
   for (int e = 0; e < kMaxD / 32; ++e) part[warp][lane + 32 * e] = r.o[e];
   if (lane == 0) {

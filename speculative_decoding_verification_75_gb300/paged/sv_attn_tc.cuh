@@ -27,13 +27,13 @@
 // and fp16 hold 2^8 as exactly as 1, fp32 sums lose nothing), which after
 // the first tiles is rare.
 //
-// Data.  TMA boxes of one page's rows (or of gcd(block size, 128) rows) fill
-// 128-byte swizzled tiles through an mbarrier ring; e4m3 tiles arrive raw with
-// their scale bytes and are widened to 16-bit tiles by four warps (exactly:
-// code * 2^e is a bf16 number).  Rows of V behind the last token are zeroed
-// in shared memory, because 0 * garbage may be NaN; a value that is not
-// finite among the new tokens, or a missing block, marks the unit, and the
-// second kernel recomputes it row by row (sv_attn_general.cuh).
+// Data.  TMA boxes of one page's rows (a power of two of them that divides the
+// block size) fill 128-byte swizzled tiles through an mbarrier ring; e4m3 tiles
+// arrive raw with their scale bytes and are widened to 16-bit tiles by four
+// warps (exactly: code * 2^e is a bf16 number).  Rows of V behind the last
+// token are zeroed in shared memory, because 0 * garbage may be NaN; a value
+// that is not finite among the new tokens, or a missing block, marks the unit,
+// which is recomputed row by row (sv_attn_general.cuh).
 #pragma once
 
 #include <cuda.h>
@@ -46,18 +46,21 @@ constexpr int kMaxGrid = 152;   // thread blocks, one per SM
 constexpr int kTile = 128;      // keys per step, rows per tile
 constexpr int kSegRing = 8;
 
+// The first segment of a range: its unit, the tile of the unit it begins at,
+// and the unit's tiles; `total` tiles of all ranges.
+struct alignas(16) Cut {
+  int b, h, mp, n, t0, kt, total, pad;
+};
+
 struct TcParams {
   CUtensorMap kmap, vmap, qmap;
   AttnParams a;
   uint32_t *err;       // SV_FAULT_TIMEOUT goes here
-  int32_t *head;       // [0] tiles of all ranges
-  int32_t *pre;        // [B + 1] tiles before each request
-  uint8_t *dirty;      // [B * heads * MP] units to recompute (whole ranges)
+  Cut *cuts;           // [ranges] where each range begins
   float *slots;        // [ranges * 2] partial results
   int ranges;
   int slot_rows;       // rows of a slot
   int slot_floats;
-  int MP;              // row-tile groups per (request, head), at most
   int box;             // rows of a TMA box of the cache
   int TT;              // tokens of a row tile: its rows are TT * G <= 128
   int qbox;            // tokens of a TMA box of the queries
@@ -325,17 +328,16 @@ __device__ __noinline__ void next_segment(const AttnParams &p, int upt, Walk &w)
   Walk v = w;
   v.on = v.left > 0;
   if (v.on) {
-    if (v.seg >= 0 && ++v.unit == p.c.heads * v.r.mp) {
+    if (++v.unit == p.c.heads * v.r.mp) {
       v.unit = 0;
       uint32_t st = 0;
       do {
         v.r = request(p, upt, ++v.b, st);
       } while (v.r.weight == 0);
     }
-    if (v.seg >= 0) v.t0 = 0;                // a later segment begins a unit
-    v.t1 = min(v.r.kt, v.t0 + v.left);
-    v.left -= v.t1 - v.t0;
-    v.t = v.t0;
+    v.t = v.t0 = 0;                          // a later segment begins a unit
+    v.t1 = min(v.r.kt, v.left);
+    v.left -= v.t1;
     v.h = v.unit / v.r.mp;
     v.mp = v.unit - v.h * v.r.mp;
   }
@@ -347,43 +349,50 @@ __device__ __forceinline__ void next_tile(const AttnParams &p, int upt, Walk &w)
   if (++w.t == w.t1) next_segment(p, upt, w);
 }
 
-// Range i's first tile.  Called by whole warps: the requests are spread over
-// the lanes, 32 at a time, and `total` is all their tiles.
-__device__ __noinline__ void begin_walk(const AttnParams &p, int upt, int i, int ranges, int total, Walk &w) {
+// Range i's first tile, by a whole warp: the requests are spread over the
+// lanes, 32 at a time.
+__device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, int ranges, Walk &w, int &total) {
+  const int lane = threadIdx.x & 31, B = p.bt.B;
+  uint32_t st = 0;
+  const int mine = weight_of(p, upt, lane, st);  // requests 0 .. 31
+  total = mine;
+#pragma unroll 1
+  for (int b = lane + 32; b < B; b += 32) total += weight_of(p, upt, b, st);
+  total = __reduce_add_sync(kFull, total);
+  if (i == 0) report(p.bt.status, st);
   const int N = min(ranges, total);
-  w.on = false;
-  w.left = 0;
+  w = Walk{};
   if (i >= N) return;
   const int begin = range_start(i, N, total);
   w.left = range_start(i + 1, N, total) - begin;
-  const int lane = threadIdx.x & 31;
-  uint32_t st = 0;
-  int base = 0;
+  int base = 0, x = mine, c = 0;
 #pragma unroll 1
-  for (int c = 0; c < p.bt.B; c += 32) {
-    const int x = weight_of(p, upt, c + lane, st);
+  for (;;) {
     const int sum = __reduce_add_sync(kFull, x);
-    if (begin < base + sum) {
-      int incl = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const int excl = base + incl - x;
-      const int src = __ffs(__ballot_sync(kFull, begin >= excl && begin < excl + x)) - 1;
-      const int rem = begin - __shfl_sync(kFull, excl, src);
-      w.b = c + src;
-      w.r = request(p, upt, w.b, st);
-      w.unit = rem / w.r.kt;
-      w.t0 = rem - w.unit * w.r.kt;
-      w.seg = -1;
-      w.t1 = 0;
-      next_segment(p, upt, w);
-      return;
-    }
+    if (begin < base + sum) break;               // begin < total: it ends
     base += sum;
+    c += 32;
+    x = weight_of(p, upt, c + lane, st);
   }
+  int incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const int excl = base + incl - x;
+  const int src = __ffs(__ballot_sync(kFull, begin >= excl && begin < excl + x)) - 1;
+  const int rem = begin - __shfl_sync(kFull, excl, src);
+  w.b = c + src;
+  w.r = request(p, upt, w.b, st);
+  w.unit = rem / w.r.kt;
+  w.t0 = w.t = rem - w.unit * w.r.kt;
+  w.t1 = min(w.r.kt, w.t0 + w.left);
+  w.left -= w.t1 - w.t0;
+  w.h = w.unit / w.r.mp;
+  w.mp = w.unit - w.h * w.r.mp;
+  w.seg = 0;
+  w.on = true;
 }
 
 // A converged warp's wait for an mbarrier phase; false when it gives up.  It
@@ -413,6 +422,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   __shared__ Bars bars;
   __shared__ RingBars rings[S::kStreams];
   __shared__ uint32_t tmem_slot;
+  __shared__ Walk sh_walk[S::kStreams];
   __shared__ int seg_bad[S::kStreams][kSegRing];  // holds 1 + a marked segment's number
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -469,18 +479,23 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   sv::pdl_wait();
   sv::pdl_launch_dependents();
 
-  // Every warp finds its stream's range for itself.
+  // Where this block's ranges begin: one warp each finds out, all start there.
   const int upt = p.TT * S::kTilesPerUnit;
   uint32_t *const err = p.err;
   bool ok = true;
-  int total = 0;
-  {
-    uint32_t st = 0;
-#pragma unroll 4
-    for (int b = lane; b < a.bt.B; b += 32) total += weight_of(a, upt, b, st);
-    total = __reduce_add_sync(kFull, total);
-    if (blockIdx.x == 0 && warp == 0) report(a.bt.status, st);
+  if (warp >= 8 && warp - 8 < S::kStreams) {
+    const int i = static_cast<int>(blockIdx.x + (warp - 8) * gridDim.x);
+    Walk w;
+    int total;
+    begin_walk(a, upt, i, p.ranges, w, total);
+    if (lane == 0) {
+      sh_walk[warp - 8] = w;
+      // Range 0 is written even if there are no tiles: its total says so.
+      if (w.on || i == 0) p.cuts[i] = Cut{w.b, w.h, w.mp, w.r.n, w.t0, w.r.kt, total, 0};
+    }
   }
+  __syncthreads();
+
   // A range's loads, in order: K of its first tile, then for each tile its V
   // and the next tile's K; a tile's stages from its last keys (V: their P is
   // ready first) or its first ones (K).
@@ -493,8 +508,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const int my = wq * 32 + lane;           // row of the 128-row tile
     const int rs = kPair ? 0 : s;            // range of the block
     uint32_t ph_s = 0, ph_o = 0;
-    Walk walk;
-    begin_walk(a, upt, static_cast<int>(blockIdx.x + rs * gridDim.x), p.ranges, total, walk);
+    Walk walk = sh_walk[rs];
 #pragma unroll 1
     while (ok && walk.on) {
       const Walk sg = walk;
@@ -681,8 +695,6 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         orow = a.out + row * (D * 2);
         inv = l == 0.f ? 0.f : 1.f / l;
         if (mine && a.lse && !bad) a.lse[row] = l == 0.f ? -INFINITY : mx * kLn2 + logf(l);
-        if (boss)
-          p.dirty[(static_cast<int64_t>(sg.b) * a.c.heads + sg.h) * p.MP + sg.mp] = bad ? 1 : 0;
       } else {
         // Slot 0 of the range where the segment starts it, else slot 1.
         slot = p.slots + (static_cast<size_t>(blockIdx.x + rs * gridDim.x) * 2 + (seg == 0 ? 0 : 1)) *
@@ -694,6 +706,10 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         if (boss) reinterpret_cast<int *>(slot)[(D + 2) * p.slot_rows] = bad ? 1 : 0;
       }
       __syncwarp();
+      if (bad && whole) {
+        for (int row = wq; row < tile_rows; row += 4)
+          recompute_row<Q, C, D>(a, sg.b, tok0 + row / a.G, sg.h * a.G + row % a.G);
+      }
       if (active && !bad) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -819,8 +835,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       ++q_issued;
       return true;
     };
-    Walk w;
-    begin_walk(a, upt, static_cast<int>(blockIdx.x + rs * gridDim.x), p.ranges, total, w);
+    Walk w = sh_walk[rs];
     Box x = fetch(w);
     if constexpr (kPair) {
 #pragma unroll 1
@@ -962,8 +977,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       ph_p ^= 1u;
       return true;
     };
-    Walk w;
-    begin_walk(a, upt, static_cast<int>(blockIdx.x + rs * gridDim.x), p.ranges, total, w);
+    Walk w = sh_walk[rs];
     if (w.on) {
       int pos = 0;
       ok = qk(w, pos);
@@ -1050,9 +1064,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       }
       return true;
     };
-    Walk k, v;                             // the next K and the next V
-    begin_walk(a, upt, static_cast<int>(blockIdx.x + rs * gridDim.x), p.ranges, total, k);
-    v = k;
+    Walk k = sh_walk[rs], v = k;           // the next K and the next V
     int pos = 0;
 #pragma unroll 1
     for (bool is_v = false; ok && v.on; is_v = !is_v) {
@@ -1064,24 +1076,6 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     }
   }
 
-  // For the second kernel: where each request's tiles begin.
-  if (blockIdx.x == 0 && warp == 8) {
-    uint32_t st = 0;
-    int base = 0;
-#pragma unroll 1
-    for (int c = 0; c < a.bt.B; c += 32) {
-      const int x = weight_of(a, upt, c + lane, st);
-      int incl = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (c + lane < a.bt.B) p.pre[c + lane] = base + incl - x;
-      base += __shfl_sync(kFull, incl, 31);
-    }
-    if (lane == 0) p.head[0] = total;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1092,95 +1086,77 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
 
 constexpr int kJoinThreads = 256;
 
-// Joins the partial results of units that ranges cut, and recomputes marked
-// ones.  Grid: (units, parts of a unit's rows x D / 4 columns).
+// Joins the partial results of a unit that range ends cut: block (x, y) looks
+// at the cut where range x + 1 begins and, if it is the unit's first, joins
+// part y of the unit's rows x D / 4 columns.  K threads share an output, each
+// with every K-th range.
 template <typename Q, typename C, int D, bool kPair>
-__global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid_constant__ TcParams p) {
-  __shared__ float qs[kJoinThreads / 32][D];
+__global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid_constant__ TcParams p, const int K) {
+  __shared__ float4 so[kJoinThreads];
+  __shared__ float sm[kJoinThreads], sl[kJoinThreads];
   const AttnParams &a = p.a;
-  const int per_b = a.c.heads * p.MP;
-  const int b = blockIdx.x / per_b, rem = blockIdx.x - b * per_b, h = rem / p.MP, mp = rem - h * p.MP;
+  const int i = static_cast<int>(blockIdx.x) + 1, tid = threadIdx.x;
   sv::pdl_wait();
   sv::pdl_launch_dependents();
-  uint32_t st = 0;
-  const int upt = p.TT * (kPair ? 2 : 1);
-  const Req r = request(a, upt, b, st);
-  if (mp >= r.mp) return;
-  const int tok0 = mp * upt, rows = min(upt, r.n - tok0) * a.G;
-  const int total = ld32(p.head), start = ld32(p.pre + b) + (h * r.mp + mp) * r.kt;
-  const int N = min(p.ranges, total);
-  // The range a tile is in: an estimate, put right.
-  const auto range_of = [&](int tile) {
-    int i = min(N - 1, static_cast<int>(static_cast<float>(tile) / static_cast<float>(total) * N));
-    while (range_start(i, N, total) > tile) --i;
-    while (i + 1 < N && range_start(i + 1, N, total) <= tile) ++i;
-    return i;
-  };
-  const int c0 = range_of(start), c1 = range_of(start + r.kt - 1);
-  const int late = range_start(c0, N, total) == start ? 0 : 1;  // not the first segment of range c0
-  auto slot_of = [&](int c) {
+  const int4 *cp = reinterpret_cast<const int4 *>(p.cuts);
+  const int4 z = __ldcg(cp + 1), u0 = __ldcg(cp + 2 * i), u1 = __ldcg(cp + 2 * i + 1);
+  const int total = z.z, N = min(p.ranges, total);
+  if (i >= N || u1.x == 0) return;                    // no such range, or a unit begins with it
+  const int b = u0.x, h = u0.y, mp = u0.z, n = u0.w, kt = u1.y;
+  const int start = range_start(i, N, total) - u1.x;
+  if (range_start(i - 1, N, total) > start) return;   // cut before as well: another block's
+  const int c0 = i - 1, late = range_start(c0, N, total) == start ? 0 : 1;
+  int c1 = i;
+  while (c1 + 1 < N && range_start(c1 + 1, N, total) < start + kt) ++c1;
+  const int upt = p.TT * (kPair ? 2 : 1), tok0 = mp * upt, rows = min(upt, n - tok0) * a.G;
+  const auto slot_of = [&](int c) {
     return p.slots + (static_cast<size_t>(c) * 2 + (c == c0 ? late : 0)) * p.slot_floats;
   };
   int bad = 0;
-  if (c0 == c1) {
-    if (!ld8(p.dirty + (static_cast<int64_t>(b) * a.c.heads + h) * p.MP + mp)) return;
-    bad = 1;
-  } else {
-    for (int c = c0; c <= c1; ++c)
-      bad |= ld32(reinterpret_cast<const int32_t *>(slot_of(c)) + (D + 2) * p.slot_rows);
-  }
-  const auto out_row = [&](int row) {
-    const int t = tok0 + row / a.G, g = row % a.G;
-    return (static_cast<int64_t>(b) * a.bt.T + t) * a.Hq + h * a.G + g;
-  };
-  if (bad) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < rows;
-         row += gridDim.y * (kJoinThreads / 32)) {
-      const int t = tok0 + row / a.G, g = row % a.G;
-      const uint8_t *q = a.q + b * a.qsb + t * a.qst + static_cast<int64_t>(h * a.G + g) * a.qsh;
-      __syncwarp();
-      for (int d = lane; d < D; d += 32) {
-        const uint16_t w = static_cast<uint16_t>(ld16(q + 2 * d));
-        qs[warp][d] = load1<Q>(&w) * a.scale_log2;
-      }
-      __syncwarp();
-      RowState<D> rs;
-      rs.m = -INFINITY;
-      rs.l = 0.f;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) rs.o[e] = 0.f;
-      uint32_t none = 0;
-      attend<C, D>(a, b, t, h, r.L, r.n, r.L + r.n, qs[warp], 0, 32, lane, rs, none);
-      store_row<Q, D>(a, out_row(row), lane, rs);
-    }
+  for (int c = c0 + tid % 32; c <= c1; c += 32)
+    bad |= __ldcg(reinterpret_cast<const int32_t *>(slot_of(c)) + (D + 2) * p.slot_rows);
+  if (__any_sync(kFull, bad)) {                       // the same for every warp
+    constexpr int warps = kJoinThreads / 32;
+    for (int row = blockIdx.y * warps + tid / 32; row < rows; row += gridDim.y * warps)
+      recompute_row<Q, C, D>(a, b, tok0 + row / a.G, h * a.G + row % a.G);
     return;
   }
-  const int i = blockIdx.y * kJoinThreads + threadIdx.x;
-  if (i >= rows * (D / 4)) return;
-  const int row = i % rows, d4 = i / rows;
+  const int per = kJoinThreads / K, k = tid / per, o = blockIdx.y * per + tid % per;
+  const bool in = o < rows * (D / 4);
+  const int row = in ? o % rows : 0, d4 = in ? o / rows : 0;
   // Rows of the second tile start at row 128 of a slot.
   const int tile_rows = p.TT * a.G, srow = row < tile_rows ? row : kTile + row - tile_rows;
-  float m = -INFINITY;
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(slot_of(c) + D * p.slot_rows + srow));
-  const float mb = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  const auto add = [&](float m2, float l2, float4 w) {
+    const float nm = fmaxf(m, m2), nb = nm == -INFINITY ? 0.f : nm;
+    const float f = sv::ex2(m - nb), g = sv::ex2(m2 - nb);
+    m = nm;
+    l = l * f + l2 * g;
+    v = make_float4(v.x * f + w.x * g, v.y * f + w.y * g, v.z * f + w.z * g, v.w * f + w.w * g);
+  };
+  if (in) {
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float *s = slot_of(c);
-    const float f = sv::ex2(__ldcg(s + D * p.slot_rows + srow) - mb);
-    l += __ldcg(s + (D + 1) * p.slot_rows + srow) * f;
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(s) + static_cast<size_t>(d4) * p.slot_rows + srow);
-    o.x += v.x * f;
-    o.y += v.y * f;
-    o.z += v.z * f;
-    o.w += v.w * f;
+    for (int c = c0 + k; c <= c1; c += K) {
+      const float *s = slot_of(c);
+      add(__ldcg(s + D * p.slot_rows + srow), __ldcg(s + (D + 1) * p.slot_rows + srow),
+          __ldcg(reinterpret_cast<const float4 *>(s) + static_cast<size_t>(d4) * p.slot_rows + srow));
+    }
   }
+  if (K > 1) {
+    so[tid] = v;
+    sm[tid] = m;
+    sl[tid] = l;
+    __syncthreads();
+    if (k > 0) return;
+    for (int q = 1; q < K; ++q) add(sm[q * per + tid], sl[q * per + tid], so[q * per + tid]);
+  }
+  if (!in) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t orow = out_row(row);
+  const int t = tok0 + row / a.G, g = row % a.G;
+  const int64_t orow = (static_cast<int64_t>(b) * a.bt.T + t) * a.Hq + h * a.G + g;
   *reinterpret_cast<uint2 *>(a.out + orow * (D * 2) + d4 * 8) =
-      make_uint2(pack2<Q>(o.x * inv, o.y * inv), pack2<Q>(o.z * inv, o.w * inv));
+      make_uint2(pack2<Q>(v.x * inv, v.y * inv), pack2<Q>(v.z * inv, v.w * inv));
   if (a.lse && d4 == 0) a.lse[orow] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 

@@ -91,8 +91,8 @@ bool batch_ok(int64_t B, int64_t T) {
   return B >= 0 && T >= 0 && B <= INT_MAX && T <= INT_MAX && (B == 0 || T <= INT_MAX / B);
 }
 
-template <typename K, typename P>
-sv_status launch(K kernel, dim3 grid, int threads, size_t smem, sv_stream_t stream, const P &p) {
+template <typename K, typename... P>
+sv_status launch(K kernel, dim3 grid, int threads, size_t smem, sv_stream_t stream, const P &...p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -103,7 +103,7 @@ sv_status launch(K kernel, dim3 grid, int threads, size_t smem, sv_stream_t stre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, p...) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 // The dense side of kv_write and kv_read and their grid.
@@ -272,11 +272,11 @@ bool make_query_map(CUtensorMap &m, const AttnParams &p, int64_t dtype, int toke
 
 // Workspace of the tensor-core path.
 struct TcLayout {
-  size_t head, pre, dirty, slots, total;
+  size_t cuts, err, slots, total;
   int TT, MP, slot_rows, slot_floats;
 };
 
-TcLayout tc_layout(int64_t B, int64_t T, int64_t G, int64_t heads, int64_t D) {
+TcLayout tc_layout(int64_t T, int64_t G, int64_t D) {
   const auto up = [](size_t x, size_t a) { return (x + a - 1) / a * a; };
   TcLayout w;
   w.TT = static_cast<int>(std::max<int64_t>(kTile / G, 1));  // tokens of a row tile
@@ -286,10 +286,9 @@ TcLayout tc_layout(int64_t B, int64_t T, int64_t G, int64_t heads, int64_t D) {
   w.slot_rows = pair ? 2 * kTile
                      : static_cast<int>(up(std::min<int64_t>(std::max<int64_t>(T * G, 1), kTile), 32));
   w.slot_floats = static_cast<int>(up((D + 2) * w.slot_rows + 1, 32));
-  w.head = 0;
-  w.pre = 256;
-  w.dirty = w.pre + up(4 * (B + 1), 256);
-  w.slots = w.dirty + up(B * heads * w.MP, 256);
+  w.cuts = 0;
+  w.err = up(2 * kMaxGrid * sizeof(Cut), 256);
+  w.slots = w.err + 256;
   w.total = w.slots + up(static_cast<size_t>(kMaxGrid) * (pair ? 1 : 2) * 2 * w.slot_floats * 4, 256);
   return w;
 }
@@ -309,7 +308,7 @@ bool tc_takes(const sv_tree_attention_args *a, const AttnParams &p, const TcLayo
 }
 
 template <typename Q, typename C, int D, bool kPair>
-sv_status tc_launch(const TcParams &p, int nsm, int dev, sv_stream_t stream) {
+sv_status tc_launch(const TcParams &p, int64_t units, int dev, sv_stream_t stream) {
   using S = Shape<Q, C, D, kPair>;
   static std::atomic<uint64_t> done{0};
   auto *k = sv_attn_tc_kernel<Q, C, D, kPair>;
@@ -322,19 +321,21 @@ sv_status tc_launch(const TcParams &p, int nsm, int dev, sv_stream_t stream) {
   const int grid = p.ranges / S::kStreams;
   if (const sv_status s = launch(k, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, stream, p))
     return s;
-  const int rows = std::min(p.a.bt.T, p.TT * S::kTilesPerUnit) * p.a.G;
-  const int64_t units = static_cast<int64_t>(p.a.bt.B) * p.a.c.heads * p.MP;
+  if (p.ranges < 2) return SV_OK;  // nothing is cut
+  // Few units are cut into many parts: then more threads share an output.
+  int K = 1;
+  while (K < 8 && K * 4 * units <= p.ranges) K *= 2;
+  const int per = kJoinThreads / K, rows = std::min(p.a.bt.T, p.TT * S::kTilesPerUnit) * p.a.G;
   return launch(sv_attn_join_kernel<Q, C, D, kPair>,
-                dim3(static_cast<unsigned>(units),
-                     static_cast<unsigned>((rows * (D / 4) + kJoinThreads - 1) / kJoinThreads)),
-                kJoinThreads, 0, stream, p);
+                dim3(static_cast<unsigned>(p.ranges - 1), static_cast<unsigned>((rows * (D / 4) + per - 1) / per)),
+                kJoinThreads, 0, stream, p, K);
 }
 
 template <typename Q, typename C>
-sv_status tc_pick(const TcParams &p, bool pair, int nsm, int dev, sv_stream_t stream) {
+sv_status tc_pick(const TcParams &p, bool pair, int64_t units, int dev, sv_stream_t stream) {
   if (p.a.c.D == 64)
-    return pair ? tc_launch<Q, C, 64, true>(p, nsm, dev, stream) : tc_launch<Q, C, 64, false>(p, nsm, dev, stream);
-  return pair ? tc_launch<Q, C, 128, true>(p, nsm, dev, stream) : tc_launch<Q, C, 128, false>(p, nsm, dev, stream);
+    return pair ? tc_launch<Q, C, 64, true>(p, units, dev, stream) : tc_launch<Q, C, 64, false>(p, units, dev, stream);
+  return pair ? tc_launch<Q, C, 128, true>(p, units, dev, stream) : tc_launch<Q, C, 128, false>(p, units, dev, stream);
 }
 
 sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const TcLayout &w,
@@ -346,14 +347,11 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
   TcParams p = {};
   p.a = ap;
   uint8_t *ws = static_cast<uint8_t *>(a->workspace);
-  p.head = reinterpret_cast<int32_t *>(ws + w.head);
-  p.err = a->status ? a->status : reinterpret_cast<uint32_t *>(ws + w.head) + 1;
-  p.pre = reinterpret_cast<int32_t *>(ws + w.pre);
-  p.dirty = ws + w.dirty;
+  p.cuts = reinterpret_cast<Cut *>(ws + w.cuts);
+  p.err = a->status ? a->status : reinterpret_cast<uint32_t *>(ws + w.err);
   p.slots = reinterpret_cast<float *>(ws + w.slots);
   p.slot_rows = w.slot_rows;
   p.slot_floats = w.slot_floats;
-  p.MP = w.MP;
   const bool pair = ap.bt.T > w.TT;
   p.box = 8;  // a power of two that divides the block size, at most a stage
   while (p.box < (pair ? kTile : kTile / 2) && ap.c.bs % (2 * p.box) == 0) p.box *= 2;
@@ -367,9 +365,10 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
   if (!*taken) return SV_OK;  // strides that no tensor map describes
   p.ranges = std::min(nsm, kMaxGrid) * (pair ? 1 : 2);
   p.mvec = ap.mask && ap.bt.T % 4 == 0 && aligned(ap.mask, 4) && ap.msb % 4 == 0;
-  if (a->cache.dtype == SV_E4M3) return tc_pick<BF16, E4M3>(p, pair, nsm, dev, stream);
-  return a->dtype == SV_BF16 ? tc_pick<BF16, BF16>(p, pair, nsm, dev, stream)
-                             : tc_pick<F16, F16>(p, pair, nsm, dev, stream);
+  const int64_t units = static_cast<int64_t>(ap.bt.B) * ap.c.heads * w.MP;
+  if (a->cache.dtype == SV_E4M3) return tc_pick<BF16, E4M3>(p, pair, units, dev, stream);
+  return a->dtype == SV_BF16 ? tc_pick<BF16, BF16>(p, pair, units, dev, stream)
+                             : tc_pick<F16, F16>(p, pair, units, dev, stream);
 }
 
 bool attn_sizes_ok(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
@@ -406,7 +405,7 @@ sv_status tree_attention(const sv_tree_attention_args *a, sv_stream_t stream) {
   p.scale_log2 = static_cast<float>(sl2);
   p.Hq = static_cast<int>(a->num_heads);
   p.G = p.Hq / p.c.heads;
-  const TcLayout w = tc_layout(a->B, a->T, p.G, p.c.heads, p.c.D);
+  const TcLayout w = tc_layout(a->T, p.G, p.c.D);
   if (tc_takes(a, p, w)) {
     bool taken = false;
     const sv_status s = attn_tc(a, p, w, stream, &taken);
@@ -440,7 +439,7 @@ sv_status sv_tree_attention(const sv_tree_attention_args *args, sv_stream_t stre
 size_t sv_tree_attention_workspace_bytes(int64_t B, int64_t T, int64_t num_heads,
                                          int64_t num_kv_heads, int64_t head_dim) {
   if (!svp::attn_sizes_ok(B, T, num_heads, num_kv_heads, head_dim)) return 0;
-  return svp::tc_layout(B, T, num_heads / num_kv_heads, num_kv_heads, head_dim).total;
+  return svp::tc_layout(T, num_heads / num_kv_heads, head_dim).total;
 }
 
 }  // extern "C"
