@@ -1106,8 +1106,11 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
   const int start = range_start(i, N, total) - u1.x;
   if (range_start(i - 1, N, total) > start) return;   // cut before as well: another block's
   const int c0 = i - 1, late = range_start(c0, N, total) == start ? 0 : 1;
-  int c1 = i;
-  while (c1 + 1 < N && range_start(c1 + 1, N, total) < start + kt) ++c1;
+  // The range of the unit's last tile: an estimate, put right.
+  const int end = start + kt - 1;
+  int c1 = min(N - 1, static_cast<int>(static_cast<float>(end) * N / static_cast<float>(total)));
+  while (range_start(c1, N, total) > end) --c1;
+  while (c1 + 1 < N && range_start(c1 + 1, N, total) <= end) ++c1;
   const int upt = p.TT * (kPair ? 2 : 1), tok0 = mp * upt, rows = min(upt, n - tok0) * a.G;
   const auto slot_of = [&](int c) {
     return p.slots + (static_cast<size_t>(c) * 2 + (c == c0 ? late : 0)) * p.slot_floats;

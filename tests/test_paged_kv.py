@@ -2,6 +2,8 @@
 what the operators refuse (the attention's own tests: test_tree_attention.py).
 """
 
+import struct
+
 import numpy as np
 import pytest
 import torch
@@ -40,6 +42,10 @@ def _pkg():
     return sv, api, kv
 
 
+# The argument structs of include/sv_paged.h: struct_bytes, the cache, the rest.
+WRITE = READ = struct.Struct("@31q")
+COMPACT = struct.Struct("@23q")
+ATTN = struct.Struct("@27qd7q")
 PTR = 0x10000  # never dereferenced: the call returns before any launch
 
 
@@ -54,27 +60,27 @@ def _write(lib, kv, cache=None, **over):
     f = dict(seq=PTR, new=0, key=PTR, value=PTR, kb=512, kt=128, kh=64, vb=512, vt=128, vh=64,
              B=2, T=4, dtype=1, status=0)
     f.update(over)
-    return lib.sv_kv_write(kv._WRITE.pack(kv._WRITE.size, *(cache or _cache_words()), *f.values()), None)
+    return lib.sv_kv_write(WRITE.pack(WRITE.size, *(cache or _cache_words()), *f.values()), None)
 
 
 def _read(lib, kv, cache=None, **over):
     f = dict(starts=0, lens=PTR, key=PTR, value=PTR, kb=512, kt=128, kh=64, vb=512, vt=128, vh=64,
              B=2, T=4, dtype=1, status=0)
     f.update(over)
-    return lib.sv_kv_read(kv._READ.pack(kv._READ.size, *(cache or _cache_words()), *f.values()), None)
+    return lib.sv_kv_read(READ.pack(READ.size, *(cache or _cache_words()), *f.values()), None)
 
 
 def _compact(lib, kv, cache=None, **over):
     f = dict(path=PTR, nacc=PTR, seq=PTR, B=2, P=4, status=0)
     f.update(over)
-    return lib.sv_kv_compact(kv._COMPACT.pack(kv._COMPACT.size, *(cache or _cache_words()), *f.values()), None)
+    return lib.sv_kv_compact(COMPACT.pack(COMPACT.size, *(cache or _cache_words()), *f.values()), None)
 
 
 def _attn(lib, kv, cache=None, **over):
     f = dict(seq=PTR, new=0, q=PTR, qb=1024, qt=256, qh=64, mask=0, msb=0, out=PTR, lse=0,
              scale=0.125, B=2, T=4, H=4, dtype=1, ws=PTR, wsb=1 << 30, status=0)
     f.update(over)
-    return lib.sv_tree_attention(kv._ATTN.pack(kv._ATTN.size, *(cache or _cache_words()), *f.values()), None)
+    return lib.sv_tree_attention(ATTN.pack(ATTN.size, *(cache or _cache_words()), *f.values()), None)
 
 
 CALLS = {"write": _write, "read": _read, "compact": _compact, "attn": _attn}
