@@ -29,14 +29,16 @@
 //
 // Data.  TMA boxes of one page's rows (a power of two of them that divides the
 // block size) fill 128-byte swizzled tiles through an mbarrier ring; e4m3 tiles
-// arrive raw with their scale bytes and are widened to 16-bit tiles by four
-// warps (exactly: code * 2^e is a bf16 number).  Rows of V behind the last
-// token are zeroed in shared memory, because 0 * garbage may be NaN; a value
-// that is not finite among the new tokens, or a missing block, marks the unit,
-// which is recomputed row by row (sv_attn_general.cuh).
+// arrive raw with their scale bytes and are widened to fp16 by four warps.
+// Rows of V behind the last token are zeroed in shared memory, because
+// 0 * garbage may be NaN; a value that is not finite among the new tokens, or a
+// missing block, marks the unit, which is recomputed row by row
+// (sv_attn_general.cuh).
 #pragma once
 
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "sv_attn_general.cuh"
 
@@ -65,7 +67,7 @@ struct TcParams {
   int TT;              // tokens of a row tile: its rows are TT * G <= 128
   int qbox;            // tokens of a TMA box of the queries
   int mvec;            // mask rows are whole 4-byte words
-  float c;             // |scale| * log2(e), at least 1e-30
+  float c;             // |scale| * log2(e), not 0
   int negate;          // scale < 0: S is computed with Q's signs flipped
 };
 
@@ -240,6 +242,7 @@ __device__ __forceinline__ bool odd16(uint32_t u) {
 template <typename Q, typename C, int D, bool kPair>
 struct Shape {
   static constexpr bool kRaw = C::kBytes == 1;      // e4m3: widened on chip
+  using M = typename std::conditional<kRaw, F16, Q>::type;   // what the tensor cores multiply
   static constexpr int kHalves = D / 64;
   static constexpr int kStreams = kPair ? 1 : 2;    // ranges of a block
   static constexpr int kQTile = kTile * D * 2;
@@ -276,7 +279,7 @@ struct RingBars {
   uint64_t full[11], empty[11], fixed[11], rfull[10], rempty[10];
 };
 struct Bars {
-  uint64_t s_full[2], p_half[2], p_ready[2], o_done[2], q_full[2], q_empty[2], drain[2];
+  uint64_t s_full[2], p_half[2], p_ready[2], o_done[2], q_full[2], q_ready[2], q_empty[2], drain[2];
 };
 
 // ----------------------------------------------------------------- work ----
@@ -424,6 +427,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ Walk sh_walk[S::kStreams];
   __shared__ int seg_bad[S::kStreams][kSegRing];  // holds 1 + a marked segment's number
+  // kRaw: scale bytes that the stages of a K tile, and a segment's V, refer to.
+  __shared__ int k_scale[S::kStreams][4][2], v_scale[S::kStreams][kSegRing];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t *const sq = smem;
@@ -453,6 +458,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       sv::mbar_init(sv::smem_addr(&bars.p_ready[s]), 4);
       sv::mbar_init(sv::smem_addr(&bars.o_done[s]), 1);
       sv::mbar_init(sv::smem_addr(&bars.q_full[s]), 1);
+      sv::mbar_init(sv::smem_addr(&bars.q_ready[s]), 4);
       sv::mbar_init(sv::smem_addr(&bars.q_empty[s]), 1);
       sv::mbar_init(sv::smem_addr(&bars.drain[s]), 1);
     }
@@ -508,10 +514,48 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const int my = wq * 32 + lane;           // row of the 128-row tile
     const int rs = kPair ? 0 : s;            // range of the block
     uint32_t ph_s = 0, ph_o = 0;
+    // kRaw: Q as fp16, each row times a power of two that brings its largest
+    // magnitude to 2^14 .. 2^15 (exact for elements down to 2^-31 of it, and
+    // what is lost below is 2^-39 of it); c_next takes the power back.
+    float c_next = p.c;
+    const auto prepare_q = [&](const Walk &w) {
+      const int rows = min(max(w.r.n - (w.mp * upt + (kPair ? s * p.TT : 0)), 0), p.TT) * a.G;
+      if (!wait_warp(&bars.q_full[rs], w.seg, err)) return false;
+      if (my < rows) {
+        uint8_t *q = sq + s * S::kQTile + my * 128;
+        uint32_t big = 0;
+#pragma unroll 4
+        for (int ch = 0; ch < D / 8; ++ch) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(q + (ch >> 3) * (kTile * 128) + (((ch & 7) ^ (my & 7)) << 4));
+          big = __vmaxu2(big, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        }
+        const int e = max(static_cast<int>(max(big & 0xffffu, big >> 16) >> 7), 14);   // 127 + exponent
+        const float m = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);         // 2^(141 - e)
+        c_next = fmaxf(p.c * __uint_as_float(static_cast<uint32_t>(max(e - 14, 1)) << 23), 1.2e-38f);
+#pragma unroll 4
+        for (int ch = 0; ch < D / 8; ++ch) {
+          uint4 *at = reinterpret_cast<uint4 *>(q + (ch >> 3) * (kTile * 128) + (((ch & 7) ^ (my & 7)) << 4));
+          const uint4 v = *at;
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) h[k] = pack2<F16>(sv::bf16_lo(u[k]) * m, sv::bf16_hi(u[k]) * m);
+          *at = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) sv::mbar_arrive(sv::smem_addr(&bars.q_ready[s]));
+      return true;
+    };
     Walk walk = sh_walk[rs];
+    if (S::kRaw && walk.on) ok = prepare_q(walk);
+    uint32_t tiles = 0;                      // of the range
 #pragma unroll 1
     while (ok && walk.on) {
       const Walk sg = walk;
+      const float c_row = c_next;
       const Req &r = sg.r;
       const int nt = sg.t1 - sg.t0, seg = sg.seg;
       // Tokens and rows of this stream's tile.
@@ -521,9 +565,9 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       const int t_row = tok0 + min(my, max(tile_rows - 1, 0)) / a.G;
       const int full_end = sg.new0();                        // every row sees these
       const uint8_t *mrow = a.mask ? a.mask + sg.b * a.msb + static_cast<int64_t>(t_row) * a.bt.T : nullptr;
-      float m_ref = -INFINITY, mc = 0.f, l = 0.f;            // mc = m_ref * c, 0 before a key is seen
+      float m_ref = -INFINITY, mc = 0.f, l = 0.f;            // log2 units; mc: 0 before a key is seen
 #pragma unroll 1
-      for (int j = 0; j < nt; ++j) {
+      for (int j = 0; j < nt; ++j, ++tiles) {
         // Which of the tile's keys the row sees, while S is being computed.
         const int k0 = (sg.t0 + j) * kTile;
         const bool masked = k0 + kTile > full_end;
@@ -597,7 +641,12 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             for (int k = 0; k < W; k += 32) tc_ld32(col_s + ch * W + k, x + k);
             tc_wait_ld(x);
           };
-          float mt = -INFINITY;
+          float mt = -INFINITY, cf[2] = {c_row, c_row};      // of the tile's halves
+          if constexpr (S::kRaw) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              cf[k] = fmaxf(c_row * scale_value(k_scale[rs][tiles & 3][S::kParts == 2 ? k : 0]), 1.2e-38f);
+          }
 #pragma unroll
           for (int ch = 0; ch < kTile / W; ++ch) {
             load_s(ch);
@@ -609,18 +658,16 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
               q2 = fmaxf(q2, __uint_as_float(x[k + 2]));
               q3 = fmaxf(q3, __uint_as_float(x[k + 3]));
             }
-            mt = fmaxf(mt, fmaxf(fmaxf(q0, q1), fmaxf(q2, q3)));
+            mt = fmaxf(mt, fmaxf(fmaxf(q0, q1), fmaxf(q2, q3)) * cf[ch * W / 64]);
           }
           // Raise the reference where the tile's maximum is more than 2^8
           // above it (or nothing was seen before).
-          const bool up = mt > m_ref && !((mt - m_ref) * p.c <= 8.f);
+          const bool up = mt > m_ref && !(mt - m_ref <= 8.f);
           if (__any_sync(kFull, up)) {
             float f = 1.f;
             if (up) {
-              const float nmc = mt * p.c;
-              f = sv::ex2(m_ref == -INFINITY ? -INFINITY : mc - nmc);
-              m_ref = mt;
-              mc = nmc;
+              f = sv::ex2(m_ref - mt);
+              m_ref = mc = mt;
               l *= f;
             }
             __syncwarp();
@@ -636,13 +683,14 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
               }
             }
           }
-          const uint64_t c2 = f2_pack(p.c, p.c), nm2 = f2_pack(-mc, -mc);
+          const uint64_t nm2 = f2_pack(-mc, -mc);
           uint64_t l2a = 0, l2b = 0;
           // The last chunk first: it is in registers, and P's columns are the
           // upper half of S, where a chunk's P covers only S already taken.
 #pragma unroll
           for (int ch = kTile / W - 1; ch >= 0; --ch) {
             if (ch < kTile / W - 1) load_s(ch);
+            const uint64_t c2 = f2_pack(cf[ch * W / 64], cf[ch * W / 64]);
             uint32_t pk[W / 2];
 #pragma unroll
             for (int k = 0; k < W; k += 2) {
@@ -654,7 +702,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
               y1 = sv::ex2(y1);
               if (k & 2) l2a = f2_add(l2a, f2_pack(y0, y1));
               else l2b = f2_add(l2b, f2_pack(y0, y1));
-              pk[k >> 1] = pack2<Q>(y0, y1);
+              pk[k >> 1] = pack2<typename S::M>(y0, y1);
             }
             if constexpr (W == 64) tc_st32(col_s + kPOff + ch * (W / 2), pk);
             else tc_st16(col_s + kPOff + ch * (W / 2), pk);
@@ -678,8 +726,13 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         __syncwarp();
         if (lane == 0) sv::mbar_arrive(sv::smem_addr(&bars.p_ready[s]));
       }
-      if (!ok || !(ok = wait_warp(&bars.o_done[s], ph_o++, err))) break;
+      if (!ok) break;
+      walk.t = walk.t1 - 1;
+      next_tile(a, upt, walk);
+      if (S::kRaw && walk.on && !(ok = prepare_q(walk))) break;   // while the last products run
+      if (!(ok = wait_warp(&bars.o_done[s], ph_o++, err))) break;
       tc_fence_after();
+      const float vs = S::kRaw ? scale_value(v_scale[rs][seg % kSegRing]) : 1.f;
       const bool bad = seg_bad[rs][seg % kSegRing] == seg + 1;
       const bool whole = sg.t0 == 0 && sg.t1 == r.kt;
       const int base_row = kPair ? s * kTile : 0;            // of the slot
@@ -693,7 +746,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         const int t = tok0 + my / a.G, g = my % a.G;
         const int64_t row = (static_cast<int64_t>(sg.b) * a.bt.T + t) * a.Hq + sg.h * a.G + g;
         orow = a.out + row * (D * 2);
-        inv = l == 0.f ? 0.f : 1.f / l;
+        inv = l == 0.f ? 0.f : vs / l;
         if (mine && a.lse && !bad) a.lse[row] = l == 0.f ? -INFINITY : mx * kLn2 + logf(l);
       } else {
         // Slot 0 of the range where the segment starts it, else slot 1.
@@ -729,16 +782,16 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             } else {
 #pragma unroll
               for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<uint4 *>(slot + (static_cast<size_t>((c + k) >> 2) * p.slot_rows + base_row +
-                                                   my) * 4) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                *reinterpret_cast<float4 *>(slot + (static_cast<size_t>((c + k) >> 2) * p.slot_rows + base_row +
+                                                    my) * 4) =
+                    make_float4(__uint_as_float(o[k]) * vs, __uint_as_float(o[k + 1]) * vs,
+                                __uint_as_float(o[k + 2]) * vs, __uint_as_float(o[k + 3]) * vs);
             }
           }
           __syncwarp();  // the warp's loads from TMEM are executed together
         }
       }
       tc_fence_before();   // O is read before the next P is announced
-      walk.t = walk.t1 - 1;
-      next_tile(a, upt, walk);
     }
   } else if (warp < 10) {
     // -------------------------------------------------------- producers ----
@@ -882,8 +935,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // -------------------------------------------------------- products ----
     // One warp per stream issues its Q K^T and P V, in order.
     const int s = warp - 10, rs = kPair ? 0 : s;
-    const uint32_t kQK = mma_desc<Q>(S::kKeys, false) | (p.negate ? kNegateA : 0u);
-    constexpr uint32_t kPV = mma_desc<Q>(D, true);
+    const uint32_t kQK = mma_desc<typename S::M>(S::kKeys, false) | (p.negate ? kNegateA : 0u);
+    constexpr uint32_t kPV = mma_desc<typename S::M>(D, true);
     uint8_t *const ring = ring0 + rs * (S::kStages * S::kStageBytes);
     RingBars &rb = rings[rs];
     const uint64_t q_desc = smem_desc(sv::smem_addr(sq) + s * S::kQTile, 16);
@@ -921,7 +974,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     };
     // S of the tile whose K is at `pos`.
     const auto qk = [&](const Walk &w, int pos) {
-      if (w.first() && !wait_warp(&bars.q_full[rs], w.seg, err)) return false;
+      if (w.first() && !wait_warp(S::kRaw ? &bars.q_ready[s] : &bars.q_full[rs], w.seg, err)) return false;
 #pragma unroll 1
       for (int part = 0; part < S::kParts; ++part, ++pos) {
         if (!take(pos)) return false;
@@ -1000,13 +1053,25 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ wideners ----
-    // e4m3 stages, 16 codes at a time, into the swizzled 16-bit layout; rows of
-    // V behind the committed tokens are repaired on the way.
+    // e4m3 stages as fp16, 16 codes at a time, into the swizzled layout: a code
+    // becomes code * 2^(e - E), one conversion and one product for two codes
+    // (as bf16 numbers they took six, and the widening bound the kernel).  E is
+    // the largest e of the stage for K, that of a segment's first stage for V;
+    // S and O are scaled back in fp32.  The product is exact where it is at least
+    // 2^-14 (a code has 4 significant bits: down to 2^-21 it still is), and off
+    // by 2^-25 at most below.  A group's largest code is at least 224, so for
+    // e >= E - 16 that is 2^-16 of its largest value; V is held to this, for its
+    // elements are results.  For K, where only the sum counts, 2^-25 is 2^-33 of
+    // the stage's largest value; it is held to e >= E - 24, so that a row that
+    // is not seen cannot wipe out those that are.  A unit whose scales differ by
+    // more is recomputed.  Groups at the smallest scale (2^-120, which the cache
+    // writes for zeros) do not count and become 0 in V and beside larger ones.
     constexpr int kRW = S::kRaw ? S::kRingWideners : 1, kRS = S::kRaw ? S::kRawStages : 1;
     const int rs = kPair ? 0 : (warp - 12) / kRW, ht = (warp - 12 - rs * kRW) * 32 + lane;
     RingBars &rb = rings[rs];
     uint8_t *const ring = ring0 + rs * (S::kStages * S::kStageBytes);
     uint8_t *const raw = raw0 + rs * (S::kRawStages * S::kRawBytes);
+    int v_ref = 0, k_tile = 0;
     // A tile's K or V from position `pos` on.
     const auto widen = [&](const Walk &w, bool is_v, int pos) {
 #pragma unroll 1
@@ -1018,23 +1083,58 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         const uint8_t *src = raw + rst * S::kRawBytes;
         const uint8_t *sc = src + S::kRawData;
         uint8_t *dst = ring + st * S::kStageBytes;
+        // The range of the stage's scales, over the rows that hold tokens: each
+        // warp reads them all.
+        constexpr int kSc = D / SV_KV_GROUP;            // scale bytes of a row
+        const int live = min(w.r.kv_end - k0, S::kKeys) * kSc;
+        int hi = 0, lo = 255;
+#pragma unroll
+        for (int k = 0; k < S::kKeys * kSc / 128; ++k) {
+          const uint32_t u = *reinterpret_cast<const uint32_t *>(sc + (k * 32 + lane) * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = (u >> (8 * e)) & 255;
+            if ((k * 32 + lane) * 4 + e < live && x < 255) {
+              hi = max(hi, x);
+              if (x > 7) lo = min(lo, x);
+            }
+          }
+        }
+        hi = __reduce_max_sync(kFull, hi);
+        lo = __reduce_min_sync(kFull, lo);
+        bool found;
+        int ref = hi;
+        if (is_v) {
+          if (w.first() && q == 0) v_ref = 0;
+          if (v_ref == 0 && hi > 7) v_ref = hi;         // the first stage with more than zeros
+          ref = v_ref ? v_ref : 254;
+          found = v_ref && (hi > ref + 7 || lo < ref - 16);   // 448 * 2^7 is below fp16's largest
+          v_scale[rs][w.seg % kSegRing] = ref;
+        } else {
+          found = lo < ref - 24;
+          k_scale[rs][k_tile & 3][q] = ref;
+        }
         constexpr int kCh = D / 16;                     // 16-code chunks per row
         const int r0 = max(w.new0() - k0, 0), r1 = is_v ? w.r.kv_end - k0 : S::kKeys;
         const bool look = is_v && k0 + S::kKeys > w.new0();
-        bool found = false;
 #pragma unroll 4
         for (int i = ht; i < S::kKeys * kCh; i += kRW * 32) {
           const int row = i / kCh, ch = i % kCh;
           const uint4 c = *reinterpret_cast<const uint4 *>(src + i * 16);
-          const float m = scale_value(sc[row * (D / SV_KV_GROUP) + (ch >> 1)]);
+          // 2^(e - E) as fp16: a normal number, a subnormal one or 0; NaN for NaN.
+          const int x = sc[row * kSc + (ch >> 1)], d = min(x - ref, 15);
+          uint32_t mb = d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
+          if (x == 255) mb = 0x7e00u;
+          mb |= mb << 16;
+          const __half2 m = *reinterpret_cast<const __half2 *>(&mb);
           const uint32_t u[4] = {c.x, c.y, c.z, c.w};
           uint32_t o[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
                 static_cast<__nv_fp8x2_storage_t>(u[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            o[k] = pack2<Q>(f.x * m, f.y * m);
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), m);
+            o[k] = *reinterpret_cast<const uint32_t *>(&y);
           }
           if (look && row >= r0) {
             if (row >= r1) {
@@ -1042,17 +1142,17 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
               for (int k = 0; k < 8; ++k) o[k] = 0;
             } else {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) found = found || odd16<Q>(o[k]);
+              for (int k = 0; k < 8; ++k) found = found || odd16<F16>(o[k]);
             }
           }
           // Odd chunk pairs are written in the other order: the two 64-column
           // halves of a row lie in the same banks.
-          uint8_t *d = dst + (ch >> 2) * S::kHalf + row * 128;
+          uint8_t *to = dst + (ch >> 2) * S::kHalf + row * 128;
           const int c0 = (ch & 3) * 2, sw = row & 7;
-          const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+          const uint4 c_lo = make_uint4(o[0], o[1], o[2], o[3]), c_hi = make_uint4(o[4], o[5], o[6], o[7]);
           const bool swap = ch >> 2;
-          *reinterpret_cast<uint4 *>(d + (((c0 + (swap ? 1 : 0)) ^ sw) << 4)) = swap ? hi : lo;
-          *reinterpret_cast<uint4 *>(d + (((c0 + (swap ? 0 : 1)) ^ sw) << 4)) = swap ? lo : hi;
+          *reinterpret_cast<uint4 *>(to + (((c0 + (swap ? 1 : 0)) ^ sw) << 4)) = swap ? c_hi : c_lo;
+          *reinterpret_cast<uint4 *>(to + (((c0 + (swap ? 0 : 1)) ^ sw) << 4)) = swap ? c_lo : c_hi;
         }
         if (found) seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
         fence_async_smem();
@@ -1072,6 +1172,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       if (!w.on) continue;                 // no next K
       ok = widen(w, is_v, pos);
       pos += S::kParts;
+      k_tile += !is_v;
       next_tile(a, upt, w);
     }
   }

@@ -116,6 +116,52 @@ def test_attention(case):
     check(build(rng, *case))
 
 
+def test_scales_of_an_e4m3_cache_that_differ_widely():
+    """Groups whose scales lie far apart, within a tile and from tile to tile,
+    a row that nobody sees with an enormous one, zeros at the smallest scale."""
+    rng = np.random.default_rng(31)
+    for D, T, kind in ((128, 6, "chain"), (64, 40, "tree"), (128, 3, "tree")):
+        for spread in ((100, 140), (60, 130), (120, 122)):
+            s = build(rng, 2, T, 8, 2, D, 16, [700, 300], None, kind, "bf16", "e4m3")
+            for x in (s["ks"], s["vs"]):
+                x[:] = torch.from_numpy(rng.integers(*spread, tuple(x.shape)).astype(np.uint8)).to(DEV)
+                # Whole pages at one scale, others at random ones.
+                x[::2] = torch.from_numpy(rng.integers(*spread, (x.shape[0] + 1) // 2).astype(np.uint8)).to(DEV)[:, None, None, None]
+            s["q"] *= 2.0 ** (118 - spread[1])       # scores of a few units
+            for c in (s["k"], s["v"]):               # a page of zeros
+                c.view(torch.uint8)[int(s["tables"][0, 2])] = 0
+            s["ks"][int(s["tables"][0, 2])] = 7
+            s["vs"][int(s["tables"][0, 2])] = 7
+            check(s)
+            for i in range(8):                       # a first tile of zeros
+                for c, x in ((s["k"], s["ks"]), (s["v"], s["vs"])):
+                    c.view(torch.uint8)[int(s["tables"][1, i])] = 0
+                    x[int(s["tables"][1, i])] = 7
+            check(s)
+            if s["mask"] is not None:
+                s["mask"][0, :, T - 1] = False       # hidden from all
+                blk, row = int(s["tables"][0, (700 + T - 1) // 16]), (700 + T - 1) % 16
+                s["ks"][blk, :, row] = 250
+                s["vs"][blk, :, row] = 250
+                check(s)
+
+
+@pytest.mark.parametrize("big", [-130, -40, 0, 100])
+def test_queries_of_any_magnitude(big):
+    """Query rows that are huge, tiny, zero or of one element, against keys
+    that bring the scores back to a few units."""
+    rng = np.random.default_rng(32)
+    for cdt in ("bf16", "e4m3"):
+        s = build(rng, 1, 5, 8, 2, 64, 16, [200], None, "chain", "bf16", cdt)
+        q = s["q"].double()
+        q *= 2.0 ** big
+        q[0, 1, :, 1:] = 0
+        q[0, 2] = 0
+        q[0, 3] *= torch.from_numpy(2.0 ** rng.integers(-30, 1, (8, 64))).to(DEV)
+        s["q"] = q.to(torch.bfloat16)
+        check(s, scale=2.0 ** -3 * 2.0 ** -big if abs(big) < 120 else 1.0)
+
+
 @pytest.mark.parametrize("cdt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("B,T,L", [(1, 1, [20011]), (2, 7, [4999, 9001]), (1, 40, [6007])])
 def test_long_contexts_are_split_and_joined(B, T, L, cdt):
