@@ -398,21 +398,23 @@ __device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, 
   w.on = true;
 }
 
-// A converged warp's wait for an mbarrier phase; false when it gives up.  It
-// polls: a warp suspended in try_wait was seen to wake a microsecond late when
-// its scheduler is busy, and these waits are links of one chain.  2^25 polls
-// of some 40 cycles end after about a second.
+// A converged warp's wait for an mbarrier phase; false when it gives up, after
+// about two seconds.  The warp is suspended meanwhile: polling warps took the
+// issue slots of those that widen and of the softmax.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t *err) {
+  const uint64_t t0 = sv::global_timer_ns();
 #pragma unroll 1
-  for (uint32_t i = 0; i < (1u << 25); ++i)
-    if (__any_sync(kFull, sv::mbar_test_wait(bar, parity))) return true;
+  for (uint32_t i = 0; i < (1u << 30); ++i) {
+    if (__any_sync(kFull, sv::mbar_try_wait_sleep(bar, parity, 20000u))) return true;
+    if (__any_sync(kFull, sv::global_timer_ns() - t0 > sv::kWaitLimitNs)) break;
+  }
   report(err, SV_FAULT_TIMEOUT);
   return false;
 }
 __device__ __forceinline__ bool wait_warp(const uint64_t *bar, uint32_t parity, uint32_t *err) {
   const uint32_t at = sv::smem_addr(bar);
   parity &= 1u;
-  return __any_sync(kFull, sv::mbar_test_wait(at, parity)) || wait_long(at, parity, err);
+  return __any_sync(kFull, sv::mbar_try_wait(at, parity)) || wait_long(at, parity, err);
 }
 
 // ------------------------------------------------------------ main kernel ----
@@ -1117,42 +1119,56 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         constexpr int kCh = D / 16;                     // 16-code chunks per row
         const int r0 = max(w.new0() - k0, 0), r1 = is_v ? w.r.kv_end - k0 : S::kKeys;
         const bool look = is_v && k0 + S::kKeys > w.new0();
-#pragma unroll 4
-        for (int i = ht; i < S::kKeys * kCh; i += kRW * 32) {
-          const int row = i / kCh, ch = i % kCh;
-          const uint4 c = *reinterpret_cast<const uint4 *>(src + i * 16);
-          // 2^(e - E) as fp16: a normal number, a subnormal one or 0; NaN for NaN.
-          const int x = sc[row * kSc + (ch >> 1)], d = min(x - ref, 15);
-          uint32_t mb = d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
-          if (x == 255) mb = 0x7e00u;
-          mb |= mb << 16;
-          const __half2 m = *reinterpret_cast<const __half2 *>(&mb);
-          const uint32_t u[4] = {c.x, c.y, c.z, c.w};
-          uint32_t o[8];
+        // Four chunks a turn: their loads first, for a chunk alone is a chain of
+        // latencies.
+        constexpr int kStep = kRW * 32, kTurn = 4;
+        static_assert(S::kKeys * kCh % (kStep * kTurn) == 0 || !S::kRaw, "whole turns");
+#pragma unroll 1
+        for (int i0 = ht; i0 < S::kKeys * kCh; i0 += kStep * kTurn) {
+          uint4 c[kTurn];
+          int x[kTurn];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                static_cast<__nv_fp8x2_storage_t>(u[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
-            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), m);
-            o[k] = *reinterpret_cast<const uint32_t *>(&y);
+          for (int t = 0; t < kTurn; ++t) {
+            const int i = i0 + t * kStep;
+            c[t] = *reinterpret_cast<const uint4 *>(src + i * 16);
+            x[t] = sc[(i / kCh) * kSc + ((i % kCh) >> 1)];
           }
-          if (look && row >= r0) {
-            if (row >= r1) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = 0;
-            } else {
+          for (int t = 0; t < kTurn; ++t) {
+            const int i = i0 + t * kStep, row = i / kCh, ch = i % kCh;
+            // 2^(e - E) as fp16: a normal number, a subnormal one or 0; NaN for NaN.
+            const int d = min(x[t] - ref, 15);
+            uint32_t mb = d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
+            if (x[t] == 255) mb = 0x7e00u;
+            mb |= mb << 16;
+            const __half2 m = *reinterpret_cast<const __half2 *>(&mb);
+            const uint32_t u[4] = {c[t].x, c[t].y, c[t].z, c[t].w};
+            uint32_t o[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) found = found || odd16<F16>(o[k]);
+            for (int k = 0; k < 8; ++k) {
+              const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                  static_cast<__nv_fp8x2_storage_t>(u[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), m);
+              o[k] = *reinterpret_cast<const uint32_t *>(&y);
             }
+            if (look && row >= r0) {                    // rare: the last tiles of a unit
+              if (row >= r1) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = 0;
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) found = found || odd16<F16>(o[k]);
+              }
+            }
+            // Odd chunk pairs are written in the other order: the two 64-column
+            // halves of a row lie in the same banks.
+            uint8_t *to = dst + (ch >> 2) * S::kHalf + row * 128;
+            const int c0 = (ch & 3) * 2, sw = row & 7;
+            const uint4 c_lo = make_uint4(o[0], o[1], o[2], o[3]), c_hi = make_uint4(o[4], o[5], o[6], o[7]);
+            const bool swap = ch >> 2;
+            *reinterpret_cast<uint4 *>(to + (((c0 + (swap ? 1 : 0)) ^ sw) << 4)) = swap ? c_hi : c_lo;
+            *reinterpret_cast<uint4 *>(to + (((c0 + (swap ? 0 : 1)) ^ sw) << 4)) = swap ? c_lo : c_hi;
           }
-          // Odd chunk pairs are written in the other order: the two 64-column
-          // halves of a row lie in the same banks.
-          uint8_t *to = dst + (ch >> 2) * S::kHalf + row * 128;
-          const int c0 = (ch & 3) * 2, sw = row & 7;
-          const uint4 c_lo = make_uint4(o[0], o[1], o[2], o[3]), c_hi = make_uint4(o[4], o[5], o[6], o[7]);
-          const bool swap = ch >> 2;
-          *reinterpret_cast<uint4 *>(to + (((c0 + (swap ? 1 : 0)) ^ sw) << 4)) = swap ? c_hi : c_lo;
-          *reinterpret_cast<uint4 *>(to + (((c0 + (swap ? 0 : 1)) ^ sw) << 4)) = swap ? c_lo : c_hi;
         }
         if (found) seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
         fence_async_smem();
