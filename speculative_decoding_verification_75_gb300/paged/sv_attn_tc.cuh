@@ -262,9 +262,9 @@ struct Shape {
   static constexpr int kRawStages = kRaw ? (D == 128 ? 3 : 10) : 0;
   static constexpr int kChunk = kRaw ? 32 : 64;     // S columns in registers at once
   static constexpr int kTilesPerUnit = kPair ? 2 : 1;
-  // Warps: 8 softmax, 2 producers, 2 for the products, and 4 that widen: 3 or
-  // 4 on each scheduler.
-  static constexpr int kWideners = kRaw ? 4 : 0;
+  // Warps: 8 softmax, 2 producers, 2 for the products, and 8 that widen: 3 or
+  // 5 on each scheduler (4 wideners were bound by their latencies).
+  static constexpr int kWideners = kRaw ? 8 : 0;
   static constexpr int kWarps = 12 + kWideners;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRingWideners = kWideners / kStreams;
@@ -1090,13 +1090,23 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         constexpr int kSc = D / SV_KV_GROUP;            // scale bytes of a row
         const int live = min(w.r.kv_end - k0, S::kKeys) * kSc;
         int hi = 0, lo = 255;
+        uint32_t top = 0, low = ~0u;
 #pragma unroll
         for (int k = 0; k < S::kKeys * kSc / 128; ++k) {
           const uint32_t u = *reinterpret_cast<const uint32_t *>(sc + (k * 32 + lane) * 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int x = (u >> (8 * e)) & 255;
-            if ((k * 32 + lane) * 4 + e < live && x < 255) {
+          top = __vmaxu4(top, u);
+          low = __vminu4(low, u);
+        }
+        // Whole stages of ordinary scales, by bytes; else one by one.
+        const uint32_t odd = __vcmpgtu4(0x08080808u, low) | __vcmpeq4(top, ~0u);
+        if (live == S::kKeys * kSc && !__any_sync(kFull, odd)) {
+          hi = max(max(top & 255, (top >> 8) & 255), max((top >> 16) & 255, top >> 24));
+          lo = min(min(low & 255, (low >> 8) & 255), min((low >> 16) & 255, low >> 24));
+        } else {
+#pragma unroll 1
+          for (int i = lane; i < live; i += 32) {
+            const int x = sc[i];
+            if (x < 255) {
               hi = max(hi, x);
               if (x > 7) lo = min(lo, x);
             }
@@ -1121,7 +1131,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         const bool look = is_v && k0 + S::kKeys > w.new0();
         // Four chunks a turn: their loads first, for a chunk alone is a chain of
         // latencies.
-        constexpr int kStep = kRW * 32, kTurn = 4;
+        constexpr int kStep = kRW * 32, kTurn = S::kKeys * kCh / kStep < 4 ? S::kKeys * kCh / kStep : 4;
         static_assert(S::kKeys * kCh % (kStep * kTurn) == 0 || !S::kRaw, "whole turns");
 #pragma unroll 1
         for (int i0 = ht; i0 < S::kKeys * kCh; i0 += kStep * kTurn) {
