@@ -24,7 +24,7 @@
  * block block_tables[b][p / block_size]; -1 is no block.  Element types:
  * SV_BF16, SV_F16, or SV_E4M3 with one scale byte s per 32 elements of
  * head_dim (k_scale, v_scale: [num_layers][num_blocks][num_kv_heads]
- * [block_size][head_dim / 32], E8M0: value = code * 2^(s - 127)).
+ * [block_size][head_dim / 32], E8M0: value = code * 2^(s - 127), 255 is NaN).
  * k, v and the scales start on 16-byte boundaries; block_stride and
  * layer_stride in bytes, scale_block_stride and scale_layer_stride are
  * multiples of 16 where they are used.

@@ -1074,6 +1074,16 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     uint8_t *const ring = ring0 + rs * (S::kStages * S::kStageBytes);
     uint8_t *const raw = raw0 + rs * (S::kRawStages * S::kRawBytes);
     int v_ref = 0, k_tile = 0;
+    // This thread's chunks: 16 codes (column group ch) of every kRowStep-th row.
+    // Eight lanes write 4 chunks of one row and 4 of the next, whose swizzles
+    // differ in the lowest bit: eight different 16-byte columns of the banks.
+    constexpr int kCh = D / 16, kRowStep = kRW * 32 / kCh, kTurn = S::kKeys / kRowStep;
+    static_assert(kRowStep % 8 == 0 || !S::kRaw, "one swizzle per thread");
+    const int ch = (ht & 3) + (kCh == 8 ? (ht >> 3 & 1) * 4 : 0);
+    const int row0 = (kCh == 8 ? ht >> 4 : ht >> 3) * 2 + (ht >> 2 & 1);
+    const int from = row0 * D + ch * 16;
+    const int to_row = (ch >> 2) * S::kHalf + row0 * 128, c0 = (ch & 3) * 2;
+    const int to_lo = to_row + ((c0 ^ (row0 & 7)) << 4), to_hi = to_row + (((c0 + 1) ^ (row0 & 7)) << 4);
     // A tile's K or V from position `pos` on.
     const auto widen = [&](const Walk &w, bool is_v, int pos) {
 #pragma unroll 1
@@ -1106,10 +1116,9 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
 #pragma unroll 1
           for (int i = lane; i < live; i += 32) {
             const int x = sc[i];
-            if (x < 255) {
-              hi = max(hi, x);
-              if (x > 7) lo = min(lo, x);
-            }
+            if (x == 255) lo = -255;                  // NaN: the unit is recomputed
+            else hi = max(hi, x);
+            if (x > 7) lo = min(lo, x);
           }
         }
         hi = __reduce_max_sync(kFull, hi);
@@ -1120,65 +1129,51 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           if (w.first() && q == 0) v_ref = 0;
           if (v_ref == 0 && hi > 7) v_ref = hi;         // the first stage with more than zeros
           ref = v_ref ? v_ref : 254;
-          found = v_ref && (hi > ref + 7 || lo < ref - 16);   // 448 * 2^7 is below fp16's largest
+          found = lo < 0 || (v_ref && (hi > ref + 7 || lo < ref - 16));   // 448 * 2^7 is below fp16's largest
           v_scale[rs][w.seg % kSegRing] = ref;
         } else {
           found = lo < ref - 24;
           k_scale[rs][k_tile & 3][q] = ref;
         }
-        constexpr int kCh = D / 16;                     // 16-code chunks per row
         const int r0 = max(w.new0() - k0, 0), r1 = is_v ? w.r.kv_end - k0 : S::kKeys;
         const bool look = is_v && k0 + S::kKeys > w.new0();
-        // Four chunks a turn: their loads first, for a chunk alone is a chain of
-        // latencies.
-        constexpr int kStep = kRW * 32, kTurn = S::kKeys * kCh / kStep < 4 ? S::kKeys * kCh / kStep : 4;
-        static_assert(S::kKeys * kCh % (kStep * kTurn) == 0 || !S::kRaw, "whole turns");
-#pragma unroll 1
-        for (int i0 = ht; i0 < S::kKeys * kCh; i0 += kStep * kTurn) {
-          uint4 c[kTurn];
-          int x[kTurn];
+        // All of the thread's chunks at once, loads first: a chunk alone is a
+        // chain of latencies.
+        uint4 c[kTurn];
+        int x[kTurn];
 #pragma unroll
-          for (int t = 0; t < kTurn; ++t) {
-            const int i = i0 + t * kStep;
-            c[t] = *reinterpret_cast<const uint4 *>(src + i * 16);
-            x[t] = sc[(i / kCh) * kSc + ((i % kCh) >> 1)];
+        for (int t = 0; t < kTurn; ++t) {
+          c[t] = *reinterpret_cast<const uint4 *>(src + from + t * kRowStep * D);
+          x[t] = sc[row0 * kSc + (ch >> 1) + t * kRowStep * kSc];
+        }
+#pragma unroll
+        for (int t = 0; t < kTurn; ++t) {
+          // 2^(e - E), rounded to fp16 as fp32 is: a subnormal number or 0 where
+          // it is that small.
+          const float mf = __uint_as_float(static_cast<uint32_t>(min(max(x[t] - ref + 127, 0), 254)) << 23);
+          const __half2 m = __float2half2_rn(mf);
+          const uint32_t u[4] = {c[t].x, c[t].y, c[t].z, c[t].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                static_cast<__nv_fp8x2_storage_t>(u[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), m);
+            o[k] = *reinterpret_cast<const uint32_t *>(&y);
           }
+          if (look) {                                   // rare: the last tiles of a unit
+            const int row = row0 + t * kRowStep;
+            if (row >= r1) {
 #pragma unroll
-          for (int t = 0; t < kTurn; ++t) {
-            const int i = i0 + t * kStep, row = i / kCh, ch = i % kCh;
-            // 2^(e - E) as fp16: a normal number, a subnormal one or 0; NaN for NaN.
-            const int d = min(x[t] - ref, 15);
-            uint32_t mb = d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
-            if (x[t] == 255) mb = 0x7e00u;
-            mb |= mb << 16;
-            const __half2 m = *reinterpret_cast<const __half2 *>(&mb);
-            const uint32_t u[4] = {c[t].x, c[t].y, c[t].z, c[t].w};
-            uint32_t o[8];
+              for (int k = 0; k < 8; ++k) o[k] = 0;
+            } else if (row >= r0) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                  static_cast<__nv_fp8x2_storage_t>(u[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
-              const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), m);
-              o[k] = *reinterpret_cast<const uint32_t *>(&y);
+              for (int k = 0; k < 8; ++k) found = found || odd16<F16>(o[k]);
             }
-            if (look && row >= r0) {                    // rare: the last tiles of a unit
-              if (row >= r1) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] = 0;
-              } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) found = found || odd16<F16>(o[k]);
-              }
-            }
-            // Odd chunk pairs are written in the other order: the two 64-column
-            // halves of a row lie in the same banks.
-            uint8_t *to = dst + (ch >> 2) * S::kHalf + row * 128;
-            const int c0 = (ch & 3) * 2, sw = row & 7;
-            const uint4 c_lo = make_uint4(o[0], o[1], o[2], o[3]), c_hi = make_uint4(o[4], o[5], o[6], o[7]);
-            const bool swap = ch >> 2;
-            *reinterpret_cast<uint4 *>(to + (((c0 + (swap ? 1 : 0)) ^ sw) << 4)) = swap ? c_hi : c_lo;
-            *reinterpret_cast<uint4 *>(to + (((c0 + (swap ? 0 : 1)) ^ sw) << 4)) = swap ? c_lo : c_hi;
           }
+          uint8_t *to = dst + t * kRowStep * 128;
+          *reinterpret_cast<uint4 *>(to + to_lo) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(to + to_hi) = make_uint4(o[4], o[5], o[6], o[7]);
         }
         if (found) seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
         fence_async_smem();

@@ -47,8 +47,10 @@ def quantise(x):
 
 
 def values(codes, scale):
+    """code * 2^(byte - 127); a scale byte of 255 is E8M0's NaN."""
     v = E4M3[codes].reshape(*codes.shape[:-1], -1, GROUP)
-    return (v * 2.0 ** (scale.astype(np.float64)[..., None] - 127)).reshape(codes.shape)
+    w = np.where(scale == 255, np.nan, 2.0 ** (scale.astype(np.float64) - 127))
+    return (v * w[..., None]).reshape(codes.shape)
 
 
 def to64(t):

@@ -146,6 +146,16 @@ def test_scales_of_an_e4m3_cache_that_differ_widely():
                 check(s)
 
 
+@pytest.mark.parametrize("where", ["ks", "vs", "k", "v"])
+def test_not_a_number_among_the_committed_tokens_of_an_e4m3_cache(where):
+    for T, D in ((3, 128), (70, 64)):
+        s = build(np.random.default_rng(33), 2, T, 4, 2, D, 16, [300, 40], None, "tree", "bf16", "e4m3")
+        x = s[where].view(torch.uint8)
+        x[int(s["tables"][0, 9]), 1, 5, 1] = 0xFF      # one group, or one code, of request 0's head 1
+        out = check(s)
+        assert np.isnan(out).any() and np.isfinite(out).any()
+
+
 @pytest.mark.parametrize("big", [-130, -40, 0, 100])
 def test_queries_of_any_magnitude(big):
     """Query rows that are huge, tiny, zero or of one element, against keys
