@@ -317,11 +317,9 @@ __device__ __forceinline__ int range_start(int i, int N, int total) {
 struct Walk {
   int b, unit, left;      // left: tiles of the range behind this segment
   Req r;
-  int h, mp, t, t0, t1, seg;
+  int h, mp, t0, t1, seg;
   bool on;
 
-  __device__ __forceinline__ bool first() const { return t == t0; }
-  __device__ __forceinline__ bool last() const { return t + 1 == t1; }
   __device__ __forceinline__ int new0() const { return min(r.L, r.kv_end); }  // keys every row sees
 };
 
@@ -338,7 +336,7 @@ __device__ __noinline__ void next_segment(const AttnParams &p, int upt, Walk &w)
         v.r = request(p, upt, ++v.b, st);
       } while (v.r.weight == 0);
     }
-    v.t = v.t0 = 0;                          // a later segment begins a unit
+    v.t0 = 0;                                // a later segment begins a unit
     v.t1 = min(v.r.kt, v.left);
     v.left -= v.t1;
     v.h = v.unit / v.r.mp;
@@ -348,8 +346,24 @@ __device__ __noinline__ void next_segment(const AttnParams &p, int upt, Walk &w)
   w = v;
 }
 
-__device__ __forceinline__ void next_tile(const AttnParams &p, int upt, Walk &w) {
-  if (++w.t == w.t1) next_segment(p, upt, w);
+// What the roles ask about the tile they are at, in registers (a Walk lives in
+// local memory, for next_segment takes its address).
+struct Tile {
+  int t, t0, t1, b, h, mp, seg, kv_end, new0;
+  bool on, cut;  // cut: the table is too short
+
+  __device__ __forceinline__ bool first() const { return t == t0; }
+  __device__ __forceinline__ bool last() const { return t + 1 == t1; }
+};
+
+__device__ __forceinline__ Tile tile_of(const Walk &w) {
+  return Tile{w.t0, w.t0, w.t1, w.b, w.h, w.mp, w.seg, w.r.kv_end, w.new0(), w.on, w.r.kv_end < w.r.L + w.r.n};
+}
+
+__device__ __forceinline__ void next_tile(const AttnParams &p, int upt, Walk &w, Tile &x) {
+  if (++x.t < x.t1) return;
+  next_segment(p, upt, w);
+  x = tile_of(w);
 }
 
 // Range i's first tile, by a whole warp: the requests are spread over the
@@ -389,7 +403,7 @@ __device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, 
   w.b = c + src;
   w.r = request(p, upt, w.b, st);
   w.unit = rem / w.r.kt;
-  w.t0 = w.t = rem - w.unit * w.r.kt;
+  w.t0 = rem - w.unit * w.r.kt;
   w.t1 = min(w.r.kt, w.t0 + w.left);
   w.left -= w.t1 - w.t0;
   w.h = w.unit / w.r.mp;
@@ -643,13 +657,15 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             for (int k = 0; k < W; k += 32) tc_ld32(col_s + ch * W + k, x + k);
             tc_wait_ld(x);
           };
+          // (kRaw: loops over chunks, for the instruction cache's sake.)
+          constexpr int kUnroll = S::kRaw ? 1 : kTile / W;
           float mt = -INFINITY, cf[2] = {c_row, c_row};      // of the tile's halves
           if constexpr (S::kRaw) {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               cf[k] = fmaxf(c_row * scale_value(k_scale[rs][tiles & 3][S::kParts == 2 ? k : 0]), 1.2e-38f);
           }
-#pragma unroll
+#pragma unroll kUnroll
           for (int ch = 0; ch < kTile / W; ++ch) {
             load_s(ch);
             float q0 = -INFINITY, q1 = -INFINITY, q2 = -INFINITY, q3 = -INFINITY;
@@ -660,7 +676,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
               q2 = fmaxf(q2, __uint_as_float(x[k + 2]));
               q3 = fmaxf(q3, __uint_as_float(x[k + 3]));
             }
-            mt = fmaxf(mt, fmaxf(fmaxf(q0, q1), fmaxf(q2, q3)) * cf[ch * W / 64]);
+            mt = fmaxf(mt, fmaxf(fmaxf(q0, q1), fmaxf(q2, q3)) * (ch * W < 64 ? cf[0] : cf[1]));
           }
           // Raise the reference where the tile's maximum is more than 2^8
           // above it (or nothing was seen before).
@@ -689,10 +705,11 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           uint64_t l2a = 0, l2b = 0;
           // The last chunk first: it is in registers, and P's columns are the
           // upper half of S, where a chunk's P covers only S already taken.
-#pragma unroll
+#pragma unroll kUnroll
           for (int ch = kTile / W - 1; ch >= 0; --ch) {
-            if (ch < kTile / W - 1) load_s(ch);
-            const uint64_t c2 = f2_pack(cf[ch * W / 64], cf[ch * W / 64]);
+            if (S::kRaw || ch < kTile / W - 1) load_s(ch);
+            const float cc = ch * W < 64 ? cf[0] : cf[1];
+            const uint64_t c2 = f2_pack(cc, cc);
             uint32_t pk[W / 2];
 #pragma unroll
             for (int k = 0; k < W; k += 2) {
@@ -729,8 +746,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         if (lane == 0) sv::mbar_arrive(sv::smem_addr(&bars.p_ready[s]));
       }
       if (!ok) break;
-      walk.t = walk.t1 - 1;
-      next_tile(a, upt, walk);
+      next_segment(a, upt, walk);
       if (S::kRaw && walk.on && !(ok = prepare_q(walk))) break;   // while the last products run
       if (!(ok = wait_warp(&bars.o_done[s], ph_o++, err))) break;
       tc_fence_after();
@@ -813,10 +829,10 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     struct Box {
       int id, row;
     };
-    const auto fetch = [&](const Walk &w) {
+    const auto fetch = [&](const Tile &w) {
       Box x = {-2, 0};
       const int pos = w.t * kTile + lane * box;
-      if (w.on && lane < nb && pos < w.r.kv_end) {
+      if (w.on && lane < nb && pos < w.kv_end) {
         const int j = pos / a.c.bs;
         x.row = pos - j * a.c.bs;
         x.id = ld32(a.c.tables + static_cast<size_t>(w.b) * a.c.max_blocks + j);
@@ -825,8 +841,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     };
     // A block that is not there marks the segment, whose unit is recomputed;
     // any block is loaded in its place.
-    const auto settle = [&](Box &x, const Walk &w) {
-      const bool in = lane < nb && w.t * kTile + lane * box < w.r.kv_end;
+    const auto settle = [&](Box &x, const Tile &w) {
+      const bool in = lane < nb && w.t * kTile + lane * box < w.kv_end;
       if (in && (x.id < 0 || x.id >= a.c.num_blocks)) {
         report(a.bt.status, x.id == -1 ? SV_KV_MISSING_BLOCK : SV_KV_BAD_BLOCK);
         seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
@@ -872,8 +888,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       return true;
     };
     // A segment's queries: whole tokens, G heads each, in the swizzled layout.
-    const auto load_q = [&](const Walk &w) {
-      if (lane == 0 && w.r.kv_end < w.r.L + w.r.n) report(a.bt.status, SV_KV_TABLE_SHORT);
+    const auto load_q = [&](const Tile &w) {
+      if (lane == 0 && w.cut) report(a.bt.status, SV_KV_TABLE_SHORT);
       if (w.seg > 0 && !wait_warp(&bars.q_empty[rs], w.seg - 1, err)) return false;
       if (kPair && w.seg > 0 && !wait_warp(&bars.q_empty[1], w.seg - 1, err)) return false;
       const uint32_t bar = sv::smem_addr(&bars.q_full[rs]);
@@ -890,39 +906,37 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       ++q_issued;
       return true;
     };
-    Walk w = sh_walk[rs];
+    Walk walk = sh_walk[rs];
+    Tile w = tile_of(walk);
     Box x = fetch(w);
     if constexpr (kPair) {
 #pragma unroll 1
       for (int i = 0; ok && w.on; ++i) {
         Box now = x;
         settle(now, w);
-        const bool first = w.first() && s == 0;
-        const Walk at = w;
-        next_tile(a, upt, w);
+        const Tile at = w;
+        next_tile(a, upt, walk, w);
         x = fetch(w);                        // on its way while the stage is waited for
         ok = load(now, at.h, s == 1, 2 * i + s);
-        if (ok && first) ok = load_q(at);
+        if (ok && at.first() && s == 0) ok = load_q(at);
       }
-    } else if (w.on) {
+    } else {
+      // Turn -1: K of the first tile; then a tile's V and the next tile's K.
       int pos = 0;
-      Walk at = w;
+      Tile at = w;
       Box now = x;
-      settle(now, at);
-      next_tile(a, upt, w);
-      x = fetch(w);                          // on its way while stages are waited for
-      ok = load(now, at.h, false, pos) && load_q(at);
-      pos += S::kParts;
 #pragma unroll 1
-      while (ok) {
-        ok = load(now, at.h, true, pos);
-        pos += S::kParts;
+      for (bool begun = false; ok; begun = true) {
+        if (begun) {
+          ok = load(now, at.h, true, pos);
+          pos += S::kParts;
+        }
         if (!ok || !w.on) break;
         at = w;
         now = x;
         settle(now, at);
-        next_tile(a, upt, w);
-        x = fetch(w);
+        next_tile(a, upt, walk, w);
+        x = fetch(w);                        // on its way while stages are waited for
         ok = load(now, at.h, false, pos);
         pos += S::kParts;
         if (ok && at.first()) ok = load_q(at);
@@ -954,9 +968,9 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // Not kRaw: rows of V behind the committed tokens, keys k0 .. of a stage.
     // What lies behind the last token becomes 0, a value that is not finite
     // marks the segment.
-    const auto repair = [&](const Walk &w, int k0, int st) {
+    const auto repair = [&](const Tile &w, int k0, int st) {
       uint8_t *base = ring + st * S::kStageBytes;
-      const int r0 = max(w.new0() - k0, 0), r1 = w.r.kv_end - k0;   // new rows [r0, r1)
+      const int r0 = max(w.new0 - k0, 0), r1 = w.kv_end - k0;   // new rows [r0, r1)
       constexpr int kCh = S::kHalves * 8;
       bool found = false;
 #pragma unroll 2
@@ -975,7 +989,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       __syncwarp();
     };
     // S of the tile whose K is at `pos`.
-    const auto qk = [&](const Walk &w, int pos) {
+    const auto qk = [&](const Tile &w, int pos) {
       if (w.first() && !wait_warp(S::kRaw ? &bars.q_ready[s] : &bars.q_full[rs], w.seg, err)) return false;
 #pragma unroll 1
       for (int part = 0; part < S::kParts; ++part, ++pos) {
@@ -997,14 +1011,14 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       return true;
     };
     // O += P V, keys 64 .. 127 of the tile first: their P is ready first.
-    const auto pv = [&](const Walk &w, int pos) {
+    const auto pv = [&](const Tile &w, int pos) {
 #pragma unroll 1
       for (int half = 1; half >= 0; --half) {
         const int st = pos % S::kStages;
         if (half == 1 || S::kParts == 2) {            // a stage begins
           if (!take(pos)) return false;
           const int k0 = w.t * kTile + (S::kParts == 2 ? half * S::kKeys : 0);
-          if (!S::kRaw && k0 + S::kKeys > w.new0()) {
+          if (!S::kRaw && k0 + S::kKeys > w.new0) {
             if (!kPair || s == 0) {
               repair(w, k0, st);
               if (kPair && lane == 0) sv::mbar_arrive(sv::smem_addr(&rb.fixed[st]));
@@ -1032,21 +1046,20 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       ph_p ^= 1u;
       return true;
     };
-    Walk w = sh_walk[rs];
-    if (w.on) {
-      int pos = 0;
-      ok = qk(w, pos);
-      pos += S::kParts;
+    Walk walk = sh_walk[rs];
+    Tile w = tile_of(walk);
+    int pos = 0;
 #pragma unroll 1
-      while (ok) {
+    for (bool begun = false; ok; begun = true) {
+      if (begun) {
         ok = pv(w, pos);
         pos += S::kParts;
         if (!ok) break;
-        next_tile(a, upt, w);
-        if (!w.on) break;
-        ok = qk(w, pos);
-        pos += S::kParts;
+        next_tile(a, upt, walk, w);
       }
+      if (!w.on) break;
+      ok = qk(w, pos);
+      pos += S::kParts;
     }
     if (!ok) {  // issued products end before TMEM is freed
       if (elect_one()) tc_commit(sv::smem_addr(&bars.drain[s]));
@@ -1085,7 +1098,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const int to_row = (ch >> 2) * S::kHalf + row0 * 128, c0 = (ch & 3) * 2;
     const int to_lo = to_row + ((c0 ^ (row0 & 7)) << 4), to_hi = to_row + (((c0 + 1) ^ (row0 & 7)) << 4);
     // A tile's K or V from position `pos` on.
-    const auto widen = [&](const Walk &w, bool is_v, int pos) {
+    const auto widen = [&](const Tile &w, bool is_v, int pos) {
 #pragma unroll 1
       for (int q = 0; q < S::kParts; ++q, ++pos) {
         const int st = pos % S::kStages, rst = pos % kRS;
@@ -1098,7 +1111,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         // The range of the stage's scales, over the rows that hold tokens: each
         // warp reads them all.
         constexpr int kSc = D / SV_KV_GROUP;            // scale bytes of a row
-        const int live = min(w.r.kv_end - k0, S::kKeys) * kSc;
+        const int live = min(w.kv_end - k0, S::kKeys) * kSc;
         int hi = 0, lo = 255;
         uint32_t top = 0, low = ~0u;
 #pragma unroll
@@ -1135,8 +1148,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           found = lo < ref - 24;
           k_scale[rs][k_tile & 3][q] = ref;
         }
-        const int r0 = max(w.new0() - k0, 0), r1 = is_v ? w.r.kv_end - k0 : S::kKeys;
-        const bool look = is_v && k0 + S::kKeys > w.new0();
+        const int r0 = max(w.new0 - k0, 0), r1 = is_v ? w.kv_end - k0 : S::kKeys;
+        const bool look = is_v && k0 + S::kKeys > w.new0;
         // All of the thread's chunks at once, loads first: a chunk alone is a
         // chain of latencies.
         uint4 c[kTurn];
@@ -1161,19 +1174,22 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), m);
             o[k] = *reinterpret_cast<const uint32_t *>(&y);
           }
-          if (look) {                                   // rare: the last tiles of a unit
-            const int row = row0 + t * kRowStep;
-            if (row >= r1) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = 0;
-            } else if (row >= r0) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) found = found || odd16<F16>(o[k]);
-            }
-          }
           uint8_t *to = dst + t * kRowStep * 128;
           *reinterpret_cast<uint4 *>(to + to_lo) = make_uint4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<uint4 *>(to + to_hi) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        if (look) {  // the last tiles of a unit: the thread's own rows once more
+#pragma unroll 1
+          for (int t = 0; t < 2 * kTurn; ++t) {
+            const int row = row0 + (t >> 1) * kRowStep;
+            uint4 *at = reinterpret_cast<uint4 *>(dst + (t >> 1) * kRowStep * 128 + (t & 1 ? to_hi : to_lo));
+            if (row >= r1) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else if (row >= r0) {
+              const uint4 y = *at;
+              found = found || odd16<F16>(y.x) || odd16<F16>(y.y) || odd16<F16>(y.z) || odd16<F16>(y.w);
+            }
+          }
         }
         if (found) seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
         fence_async_smem();
@@ -1185,16 +1201,19 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       }
       return true;
     };
-    Walk k = sh_walk[rs], v = k;           // the next K and the next V
+    Walk walk = sh_walk[rs];
+    Tile k = tile_of(walk), v = k;         // the next K; the V of the one before
     int pos = 0;
 #pragma unroll 1
-    for (bool is_v = false; ok && v.on; is_v = !is_v) {
-      Walk &w = is_v ? v : k;
-      if (!w.on) continue;                 // no next K
-      ok = widen(w, is_v, pos);
+    for (bool is_v = false; ok; is_v = !is_v) {
+      if (!is_v && !k.on) break;
+      ok = widen(is_v ? v : k, is_v, pos);
       pos += S::kParts;
-      k_tile += !is_v;
-      next_tile(a, upt, w);
+      if (!is_v) {
+        ++k_tile;
+        v = k;
+        next_tile(a, upt, walk, k);
+      }
     }
   }
 
