@@ -459,13 +459,13 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   if (tid == 0) {
     for (int r = 0; r < S::kStreams; ++r) {
       for (int i = 0; i < S::kStages; ++i) {
-        sv::mbar_init(sv::smem_addr(&rings[r].full[i]), S::kRaw ? S::kRingWideners : 1);
+        sv::mbar_init(sv::smem_addr(&rings[r].full[i]), S::kRaw ? S::kRingWideners / 2 : 1);
         sv::mbar_init(sv::smem_addr(&rings[r].empty[i]), kPair ? 2 : 1);
         sv::mbar_init(sv::smem_addr(&rings[r].fixed[i]), 1);
       }
       for (int i = 0; i < S::kRawStages; ++i) {
         sv::mbar_init(sv::smem_addr(&rings[r].rfull[i]), 1);
-        sv::mbar_init(sv::smem_addr(&rings[r].rempty[i]), S::kRingWideners);
+        sv::mbar_init(sv::smem_addr(&rings[r].rempty[i]), S::kRingWideners / 2);
       }
     }
     for (int s = 0; s < 2; ++s) {
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       if (S::kRaw && walk.on && !(ok = prepare_q(walk))) break;   // while the last products run
       if (!(ok = wait_warp(&bars.o_done[s], ph_o++, err))) break;
       tc_fence_after();
-      const float vs = S::kRaw ? scale_value(v_scale[rs][seg % kSegRing]) : 1.f;
+      const float vs = S::kRaw ? scale_value(v_scale[rs][seg % kSegRing] & 255) : 1.f;
       const bool bad = seg_bad[rs][seg % kSegRing] == seg + 1;
       const bool whole = sg.t0 == 0 && sg.t1 == r.kt;
       const int base_row = kPair ? s * kTile : 0;            // of the slot
@@ -1081,8 +1081,18 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // is not seen cannot wipe out those that are.  A unit whose scales differ by
     // more is recomputed.  Groups at the smallest scale (2^-120, which the cache
     // writes for zeros) do not count and become 0 in V and beside larger ones.
-    constexpr int kRW = S::kRaw ? S::kRingWideners : 1, kRS = S::kRaw ? S::kRawStages : 1;
-    const int rs = kPair ? 0 : (warp - 12) / kRW, ht = (warp - 12 - rs * kRW) * 32 + lane;
+    //
+    // The wideners of a ring are two groups, for its even and its odd positions:
+    // what a stage costs besides its conversions (two waits, the scales, a
+    // fence) is latency, and two stages at a time hide each other's.  A group
+    // waits for a stage to be empty before it waits for the raw one: by then the
+    // stage's last user is done, so that no parity is a round ahead (rings of
+    // different sizes: kRawStages is even, and the raw stage's last user is the
+    // group itself).
+    static_assert(S::kRawStages == S::kStages || S::kRawStages % 2 == 0, "parities");
+    constexpr int kGW = S::kRaw ? S::kRingWideners / 2 : 1, kRS = S::kRaw ? S::kRawStages : 1;
+    const int rs = kPair ? 0 : (warp - 12) / (2 * kGW), grp = warp & 1;
+    const int ht = ((warp - 12 - rs * 2 * kGW) >> 1) * 32 + lane;
     RingBars &rb = rings[rs];
     uint8_t *const ring = ring0 + rs * (S::kStages * S::kStageBytes);
     uint8_t *const raw = raw0 + rs * (S::kRawStages * S::kRawBytes);
@@ -1090,77 +1100,79 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // This thread's chunks: 16 codes (column group ch) of every kRowStep-th row.
     // Eight lanes write 4 chunks of one row and 4 of the next, whose swizzles
     // differ in the lowest bit: eight different 16-byte columns of the banks.
-    constexpr int kCh = D / 16, kRowStep = kRW * 32 / kCh, kTurn = S::kKeys / kRowStep;
-    static_assert(kRowStep % 8 == 0 || !S::kRaw, "one swizzle per thread");
+    constexpr int kCh = D / 16, kRowStep = kGW * 32 / kCh, kRows = S::kKeys / kRowStep, kTurn = 4;
+    static_assert((kRowStep % 8 == 0 && kRows % kTurn == 0) || !S::kRaw, "one swizzle per thread, whole turns");
     const int ch = (ht & 3) + (kCh == 8 ? (ht >> 3 & 1) * 4 : 0);
     const int row0 = (kCh == 8 ? ht >> 4 : ht >> 3) * 2 + (ht >> 2 & 1);
     const int from = row0 * D + ch * 16;
     const int to_row = (ch >> 2) * S::kHalf + row0 * 128, c0 = (ch & 3) * 2;
     const int to_lo = to_row + ((c0 ^ (row0 & 7)) << 4), to_hi = to_row + (((c0 + 1) ^ (row0 & 7)) << 4);
-    // A tile's K or V from position `pos` on.
-    const auto widen = [&](const Tile &w, bool is_v, int pos) {
-#pragma unroll 1
-      for (int q = 0; q < S::kParts; ++q, ++pos) {
-        const int st = pos % S::kStages, rst = pos % kRS;
-        const int k0 = w.t * kTile + (is_v ? S::kParts - 1 - q : q) * S::kKeys;
-        if (!wait_warp(&rb.rfull[rst], pos / kRS, err)) return false;
-        if (pos >= S::kStages && !wait_warp(&rb.empty[st], pos / S::kStages - 1, err)) return false;
-        const uint8_t *src = raw + rst * S::kRawBytes;
-        const uint8_t *sc = src + S::kRawData;
-        uint8_t *dst = ring + st * S::kStageBytes;
-        // The range of the stage's scales, over the rows that hold tokens: each
-        // warp reads them all.
-        constexpr int kSc = D / SV_KV_GROUP;            // scale bytes of a row
-        const int live = min(w.kv_end - k0, S::kKeys) * kSc;
-        int hi = 0, lo = 255;
-        uint32_t top = 0, low = ~0u;
+    // Stage q of a tile's K or V, at position `pos`.
+    const auto widen = [&](const Tile &w, bool is_v, int q, int pos) {
+      const int st = pos % S::kStages, rst = pos % kRS;
+      const int k0 = w.t * kTile + (is_v ? S::kParts - 1 - q : q) * S::kKeys;
+      if (pos >= S::kStages && !wait_warp(&rb.empty[st], pos / S::kStages - 1, err)) return false;
+      if (!wait_warp(&rb.rfull[rst], pos / kRS, err)) return false;
+      const uint8_t *src = raw + rst * S::kRawBytes;
+      const uint8_t *sc = src + S::kRawData;
+      uint8_t *dst = ring + st * S::kStageBytes;
+      constexpr int kSc = D / SV_KV_GROUP;            // scale bytes of a row
+      const int live = min(w.kv_end - k0, S::kKeys);  // rows that hold tokens
+      int *const vs = &v_scale[rs][w.seg % kSegRing];
+      if (is_v) {
+        if (w.first()) v_ref = 0;
+        if (v_ref == 0 && !(w.first() && q == 0) && S::kParts == 2) {  // the other group may have set it, in V's last stage
+          const int last = q == 0 ? pos - 3 : pos - 1;
+          if (!wait_warp(&rb.full[last % S::kStages], last / S::kStages, err)) return false;
+          const int x = *vs;
+          v_ref = x & 256 ? x & 255 : 0;
+        }
+      }
+      int ref = v_ref;
+      if (!is_v || v_ref == 0) {
+        // The stage's largest scale, over the rows that hold tokens: each warp
+        // reads them all.
+        int hi = 0;
+        if (live == S::kKeys) {
+          uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < S::kKeys * kSc / 128; ++k) {
-          const uint32_t u = *reinterpret_cast<const uint32_t *>(sc + (k * 32 + lane) * 4);
-          top = __vmaxu4(top, u);
-          low = __vminu4(low, u);
-        }
-        // Whole stages of ordinary scales, by bytes; else one by one.
-        const uint32_t odd = __vcmpgtu4(0x08080808u, low) | __vcmpeq4(top, ~0u);
-        if (live == S::kKeys * kSc && !__any_sync(kFull, odd)) {
-          hi = max(max(top & 255, (top >> 8) & 255), max((top >> 16) & 255, top >> 24));
-          lo = min(min(low & 255, (low >> 8) & 255), min((low >> 16) & 255, low >> 24));
+          for (int k = 0; k < S::kKeys * kSc / 128; ++k) {
+            const uint32_t u = *reinterpret_cast<const uint32_t *>(sc + (k * 32 + lane) * 4);
+            m = __vmaxu2(m, __vmaxu2(u & 0x00ff00ffu, (u >> 8) & 0x00ff00ffu));
+          }
+          hi = max(m & 0xffff, m >> 16);
         } else {
 #pragma unroll 1
-          for (int i = lane; i < live; i += 32) {
-            const int x = sc[i];
-            if (x == 255) lo = -255;                  // NaN: the unit is recomputed
-            else hi = max(hi, x);
-            if (x > 7) lo = min(lo, x);
-          }
+          for (int i = lane; i < live * kSc; i += 32) hi = max(hi, static_cast<int>(sc[i]));
         }
-        hi = __reduce_max_sync(kFull, hi);
-        lo = __reduce_min_sync(kFull, lo);
-        bool found;
-        int ref = hi;
+        ref = min(__reduce_max_sync(kFull, hi), 254);
         if (is_v) {
-          if (w.first() && q == 0) v_ref = 0;
-          if (v_ref == 0 && hi > 7) v_ref = hi;         // the first stage with more than zeros
-          ref = v_ref ? v_ref : 254;
-          found = lo < 0 || (v_ref && (hi > ref + 7 || lo < ref - 16));   // 448 * 2^7 is below fp16's largest
-          v_scale[rs][w.seg % kSegRing] = ref;
-        } else {
-          found = lo < ref - 24;
+          if (ref > 7) v_ref = ref;                   // the first stage with more than zeros
+          else ref = 254;
+          __syncwarp();
+          if (ht == 0) *vs = v_ref ? 256 + ref : ref;
+        } else if (ht == 0) {
           k_scale[rs][k_tile & 3][q] = ref;
         }
-        const int r0 = max(w.new0 - k0, 0), r1 = is_v ? w.kv_end - k0 : S::kKeys;
-        const bool look = is_v && k0 + S::kKeys > w.new0;
-        // All of the thread's chunks at once, loads first: a chunk alone is a
-        // chain of latencies.
+      }
+      // Scales that the products cannot hold (448 * 2^7 is below fp16's
+      // largest), and NaN: the unit is recomputed.
+      const int below = ref - (is_v ? 16 : 24), above = min(is_v ? ref + 7 : ref, 254);
+      bool found = false;
+      // A turn's chunks together, loads first: a chunk alone is a chain of
+      // latencies.
+#pragma unroll 1
+      for (int t0 = 0; t0 < kRows; t0 += kTurn) {
         uint4 c[kTurn];
         int x[kTurn];
 #pragma unroll
         for (int t = 0; t < kTurn; ++t) {
-          c[t] = *reinterpret_cast<const uint4 *>(src + from + t * kRowStep * D);
-          x[t] = sc[row0 * kSc + (ch >> 1) + t * kRowStep * kSc];
+          c[t] = *reinterpret_cast<const uint4 *>(src + from + (t0 + t) * kRowStep * D);
+          x[t] = sc[row0 * kSc + (ch >> 1) + (t0 + t) * kRowStep * kSc];
         }
 #pragma unroll
         for (int t = 0; t < kTurn; ++t) {
+          found = found || (row0 + (t0 + t) * kRowStep < live && x[t] > 7 && (x[t] < below || x[t] > above));
           // 2^(e - E), rounded to fp16 as fp32 is: a subnormal number or 0 where
           // it is that small.
           const float mf = __uint_as_float(static_cast<uint32_t>(min(max(x[t] - ref + 127, 0), 254)) << 23);
@@ -1174,45 +1186,44 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), m);
             o[k] = *reinterpret_cast<const uint32_t *>(&y);
           }
-          uint8_t *to = dst + t * kRowStep * 128;
+          uint8_t *to = dst + (t0 + t) * kRowStep * 128;
           *reinterpret_cast<uint4 *>(to + to_lo) = make_uint4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<uint4 *>(to + to_hi) = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        if (look) {  // the last tiles of a unit: the thread's own rows once more
+      }
+      if (is_v && k0 + S::kKeys > w.new0) {  // the last tiles of a unit: the thread's own rows once more
+        const int r0 = max(w.new0 - k0, 0), r1 = w.kv_end - k0;
 #pragma unroll 1
-          for (int t = 0; t < 2 * kTurn; ++t) {
-            const int row = row0 + (t >> 1) * kRowStep;
-            uint4 *at = reinterpret_cast<uint4 *>(dst + (t >> 1) * kRowStep * 128 + (t & 1 ? to_hi : to_lo));
-            if (row >= r1) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else if (row >= r0) {
-              const uint4 y = *at;
-              found = found || odd16<F16>(y.x) || odd16<F16>(y.y) || odd16<F16>(y.z) || odd16<F16>(y.w);
-            }
+        for (int t = 0; t < 2 * kRows; ++t) {
+          const int row = row0 + (t >> 1) * kRowStep;
+          uint4 *at = reinterpret_cast<uint4 *>(dst + (t >> 1) * kRowStep * 128 + (t & 1 ? to_hi : to_lo));
+          if (row >= r1) {
+            *at = make_uint4(0, 0, 0, 0);
+          } else if (row >= r0) {
+            const uint4 y = *at;
+            found = found || odd16<F16>(y.x) || odd16<F16>(y.y) || odd16<F16>(y.z) || odd16<F16>(y.w);
           }
         }
-        if (found) seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          sv::mbar_arrive(sv::smem_addr(&rb.full[st]));
-          sv::mbar_arrive(sv::smem_addr(&rb.rempty[rst]));
-        }
+      }
+      if (found) seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        sv::mbar_arrive(sv::smem_addr(&rb.full[st]));
+        sv::mbar_arrive(sv::smem_addr(&rb.rempty[rst]));
       }
       return true;
     };
     Walk walk = sh_walk[rs];
-    Tile k = tile_of(walk), v = k;         // the next K; the V of the one before
-    int pos = 0;
+    Tile w = tile_of(walk);
+    // Whole tiles: group 0 has their K, group 1 their V; half ones: a half of both each.
 #pragma unroll 1
-    for (bool is_v = false; ok; is_v = !is_v) {
-      if (!is_v && !k.on) break;
-      ok = widen(is_v ? v : k, is_v, pos);
-      pos += S::kParts;
-      if (!is_v) {
+    for (int i = 0; ok && w.on; ++i) {
+      const bool is_v = kPair ? grp == 1 : i & 1;
+      ok = widen(w, is_v, kPair ? 0 : grp, 2 * i + grp);
+      if (kPair || is_v) {
         ++k_tile;
-        v = k;
-        next_tile(a, upt, walk, k);
+        next_tile(a, upt, walk, w);
       }
     }
   }
