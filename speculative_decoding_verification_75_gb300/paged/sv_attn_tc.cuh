@@ -45,8 +45,9 @@
 namespace svp {
 
 constexpr int kMaxGrid = 152;   // thread blocks, one per SM
-constexpr int kTile = 128;      // keys per step, rows per tile
-constexpr int kSegRing = 8;
+constexpr int kTile = 128;      // rows of a tile
+constexpr int kScaleRing = 16;  // K tiles that are widened and not yet used, at most 7
+constexpr int kSegRing = 16;    // more segments than any role is ahead of another
 
 // The first segment of a range: its unit, the tile of the unit it begins at,
 // and the unit's tiles; `total` tiles of all ranges.
@@ -247,11 +248,15 @@ struct Shape {
   static constexpr int kStreams = kPair ? 1 : 2;    // ranges of a block
   static constexpr int kQTile = kTile * D * 2;
   static constexpr int kQBytes = 2 * kQTile;        // a Q tile per stream
+  // Keys of a step, and of a stage.  A pair shares 128 and has one S each; two
+  // streams have 64 and two S each, so that Q K^T is a step ahead of the softmax
+  // (with one S of 128 the chain Q K^T, softmax, P V set the pace: 413 us for
+  // 128 e4m3 requests).
+  static constexpr int kKeys = kPair ? 128 : 64;
+  static constexpr int kBufs = kPair ? 1 : 2;
   // Each range has a ring of its own, with one order of loads: a parity tells
-  // two phases of a barrier apart only if no one is a whole round ahead.  Two
-  // rings get half tiles, so that each is deep enough.
-  static constexpr int kKeys = kPair ? kTile : kTile / 2;   // keys of a stage
-  static constexpr int kParts = kTile / kKeys;              // stages of a tile
+  // two phases of a barrier apart only if no one is a whole round ahead.
+  static constexpr uint32_t kPOff = kKeys / 2;      // P in the upper half of its S
   static constexpr int kStageBytes = kKeys * D * 2;
   static constexpr int kHalf = kKeys * 128;                 // bytes of a stage's 64 columns
   static constexpr int kRawData = kKeys * D, kRawScale = kKeys * (D / SV_KV_GROUP);
@@ -272,14 +277,15 @@ struct Shape {
 };
 
 // TMEM columns.
-constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream
-constexpr uint32_t kPOff = 64;              // P in the upper half of its S
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream (S: + 64 * buffer)
 
 struct RingBars {
   uint64_t full[11], empty[11], fixed[11], rfull[10], rempty[10];
 };
+// One barrier of s_full, p_ready and o_done per S buffer: of the tile two before,
+// all three are done when a tile's S is, and none of the tile two behind can be.
 struct Bars {
-  uint64_t s_full[2], p_half[2], p_ready[2], o_done[2], q_full[2], q_ready[2], q_empty[2], drain[2];
+  uint64_t s_full[2][2], p_half[2], p_ready[2][2], o_done[2][2], q_full[2], q_ready[2], q_empty[2], drain[2];
 };
 
 // ----------------------------------------------------------------- work ----
@@ -290,18 +296,20 @@ struct Req {
 
 // Tiles of a request: its units (KV head, group of row tiles) times its key
 // tiles.  upt: new tokens of a unit.
+template <int kKeys>
 __device__ __forceinline__ Req request(const AttnParams &p, int upt, int b, uint32_t &st) {
   Req r;
   lengths(p.bt, b, r.L, r.n, st);
   r.mp = (r.n + upt - 1) / upt;
   r.kv_end = min(r.L + r.n, p.c.max_blocks * p.c.bs);
-  r.kt = max(1, (r.kv_end + kTile - 1) / kTile);
+  r.kt = max(1, (r.kv_end + kKeys - 1) / kKeys);
   r.weight = p.c.heads * r.mp * r.kt;
   return r;
 }
 
+template <int kKeys>
 __device__ __forceinline__ int weight_of(const AttnParams &p, int upt, int b, uint32_t &st) {
-  return b < p.bt.B ? request(p, upt, b, st).weight : 0;
+  return b < p.bt.B ? request<kKeys>(p, upt, b, st).weight : 0;
 }
 
 // Range i of N <= total over `total` tiles is [start(i), start(i + 1)): none is
@@ -325,6 +333,7 @@ struct Walk {
 
 // To the next segment.  Not inlined: every role of the kernel walks, and the
 // copies together would crowd the instruction cache.
+template <int kKeys>
 __device__ __noinline__ void next_segment(const AttnParams &p, int upt, Walk &w) {
   Walk v = w;
   v.on = v.left > 0;
@@ -333,7 +342,7 @@ __device__ __noinline__ void next_segment(const AttnParams &p, int upt, Walk &w)
       v.unit = 0;
       uint32_t st = 0;
       do {
-        v.r = request(p, upt, ++v.b, st);
+        v.r = request<kKeys>(p, upt, ++v.b, st);
       } while (v.r.weight == 0);
     }
     v.t0 = 0;                                // a later segment begins a unit
@@ -360,21 +369,28 @@ __device__ __forceinline__ Tile tile_of(const Walk &w) {
   return Tile{w.t0, w.t0, w.t1, w.b, w.h, w.mp, w.seg, w.r.kv_end, w.new0(), w.on, w.r.kv_end < w.r.L + w.r.n};
 }
 
+template <int kKeys>
 __device__ __forceinline__ void next_tile(const AttnParams &p, int upt, Walk &w, Tile &x) {
   if (++x.t < x.t1) return;
-  next_segment(p, upt, w);
+  next_segment<kKeys>(p, upt, w);
   x = tile_of(w);
 }
 
+// Tiles of a range whose walk begins.  They are loaded, widened and multiplied
+// in one order, at positions 0 .. 2n - 1: K0 V0 K1 V1 .. with one S (kPair),
+// K0 K1 V0 K2 V1 .. with two, K a tile ahead.
+__device__ __forceinline__ int count_of(const Walk &w) { return w.on ? w.left + w.t1 - w.t0 : 0; }
+
 // Range i's first tile, by a whole warp: the requests are spread over the
 // lanes, 32 at a time.
+template <int kKeys>
 __device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, int ranges, Walk &w, int &total) {
   const int lane = threadIdx.x & 31, B = p.bt.B;
   uint32_t st = 0;
-  const int mine = weight_of(p, upt, lane, st);  // requests 0 .. 31
+  const int mine = weight_of<kKeys>(p, upt, lane, st);  // requests 0 .. 31
   total = mine;
 #pragma unroll 1
-  for (int b = lane + 32; b < B; b += 32) total += weight_of(p, upt, b, st);
+  for (int b = lane + 32; b < B; b += 32) total += weight_of<kKeys>(p, upt, b, st);
   total = __reduce_add_sync(kFull, total);
   if (i == 0) report(p.bt.status, st);
   const int N = min(ranges, total);
@@ -389,7 +405,7 @@ __device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, 
     if (begin < base + sum) break;               // begin < total: it ends
     base += sum;
     c += 32;
-    x = weight_of(p, upt, c + lane, st);
+    x = weight_of<kKeys>(p, upt, c + lane, st);
   }
   int incl = x;
 #pragma unroll
@@ -401,7 +417,7 @@ __device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, 
   const int src = __ffs(__ballot_sync(kFull, begin >= excl && begin < excl + x)) - 1;
   const int rem = begin - __shfl_sync(kFull, excl, src);
   w.b = c + src;
-  w.r = request(p, upt, w.b, st);
+  w.r = request<kKeys>(p, upt, w.b, st);
   w.unit = rem / w.r.kt;
   w.t0 = rem - w.unit * w.r.kt;
   w.t1 = min(w.r.kt, w.t0 + w.left);
@@ -443,8 +459,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ Walk sh_walk[S::kStreams];
   __shared__ int seg_bad[S::kStreams][kSegRing];  // holds 1 + a marked segment's number
-  // kRaw: scale bytes that the stages of a K tile, and a segment's V, refer to.
-  __shared__ int k_scale[S::kStreams][4][2], v_scale[S::kStreams][kSegRing];
+  // kRaw: scale bytes that a K tile, and (plus 256) a segment's V, refer to.
+  __shared__ int k_scale[S::kStreams][kScaleRing], v_scale[S::kStreams][kSegRing];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t *const sq = smem;
@@ -469,10 +485,12 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       }
     }
     for (int s = 0; s < 2; ++s) {
-      sv::mbar_init(sv::smem_addr(&bars.s_full[s]), 1);
+      for (int i = 0; i < S::kBufs; ++i) {
+        sv::mbar_init(sv::smem_addr(&bars.s_full[s][i]), 1);
+        sv::mbar_init(sv::smem_addr(&bars.o_done[s][i]), 1);
+        sv::mbar_init(sv::smem_addr(&bars.p_ready[s][i]), 4);
+      }
       sv::mbar_init(sv::smem_addr(&bars.p_half[s]), 4);
-      sv::mbar_init(sv::smem_addr(&bars.p_ready[s]), 4);
-      sv::mbar_init(sv::smem_addr(&bars.o_done[s]), 1);
       sv::mbar_init(sv::smem_addr(&bars.q_full[s]), 1);
       sv::mbar_init(sv::smem_addr(&bars.q_ready[s]), 4);
       sv::mbar_init(sv::smem_addr(&bars.q_empty[s]), 1);
@@ -509,7 +527,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const int i = static_cast<int>(blockIdx.x + (warp - 8) * gridDim.x);
     Walk w;
     int total;
-    begin_walk(a, upt, i, p.ranges, w, total);
+    begin_walk<S::kKeys>(a, upt, i, p.ranges, w, total);
     if (lane == 0) {
       sh_walk[warp - 8] = w;
       // Range 0 is written even if there are no tiles: its total says so.
@@ -518,18 +536,14 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   }
   __syncthreads();
 
-  // A range's loads, in order: K of its first tile, then for each tile its V
-  // and the next tile's K; a tile's stages from its last keys (V: their P is
-  // ready first) or its first ones (K).
   if (warp < 8) {
     // ------------------------------------------------ softmax warpgroups ----
     const int s = warp >> 2;                 // stream
     const int wq = warp & 3;                 // TMEM lanes 32 wq ..
     const uint32_t lanes = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    const uint32_t col_s = lanes + kColS + 128u * s, col_o = lanes + kColO + 128u * s;
+    const uint32_t col_s0 = lanes + kColS + 128u * s, col_o = lanes + kColO + 128u * s;
     const int my = wq * 32 + lane;           // row of the 128-row tile
     const int rs = kPair ? 0 : s;            // range of the block
-    uint32_t ph_s = 0, ph_o = 0;
     // kRaw: Q as fp16, each row times a power of two that brings its largest
     // magnitude to 2^14 .. 2^15 (exact for elements down to 2^-31 of it, and
     // what is lost below is 2^-39 of it); c_next takes the power back.
@@ -585,20 +599,22 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
 #pragma unroll 1
       for (int j = 0; j < nt; ++j, ++tiles) {
         // Which of the tile's keys the row sees, while S is being computed.
-        const int k0 = (sg.t0 + j) * kTile;
-        const bool masked = k0 + kTile > full_end;
-        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+        const int k0 = (sg.t0 + j) * S::kKeys;
+        const uint32_t buf = tiles % S::kBufs, round = tiles / S::kBufs;
+        const uint32_t col_s = col_s0 + 64u * buf;
+        const bool masked = k0 + S::kKeys > full_end;
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};        // kKeys / 32 of them are used
         if (masked && active) {
           const int lim = min(r.kv_end, mrow ? r.L : r.L + t_row + 1) - k0;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < S::kKeys / 32; ++w) {
             const int n = min(max(lim - 32 * w, 0), 32);
             vis[w] = n == 32 ? ~0u : (1u << n) - 1u;
           }
           if (mrow) {
             // The row's bytes for new tokens [o0, o1), four at a time where
             // rows are whole words; bit c of the tile is new token k0 + c - L.
-            const int o0 = max(k0 - r.L, 0), o1 = min(min(r.kv_end, k0 + kTile) - r.L, r.n);
+            const int o0 = max(k0 - r.L, 0), o1 = min(min(r.kv_end, k0 + S::kKeys) - r.L, r.n);
             uint64_t lo = 0, hi = 0;
             const auto put = [&](uint64_t bits, int c) {
               if (c < 0) {
@@ -625,17 +641,19 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             }
             vis[0] |= static_cast<uint32_t>(lo);
             vis[1] |= static_cast<uint32_t>(lo >> 32);
-            vis[2] |= static_cast<uint32_t>(hi);
-            vis[3] |= static_cast<uint32_t>(hi >> 32);
+            if (S::kKeys == 128) {
+              vis[2] |= static_cast<uint32_t>(hi);
+              vis[3] |= static_cast<uint32_t>(hi >> 32);
+            }
           }
         }
-        if (!(ok = wait_warp(&bars.s_full[s], ph_s++, err))) break;
+        if (!(ok = wait_warp(&bars.s_full[s][buf], round, err))) break;
         __syncwarp();
         if (active) {
           tc_fence_after();
           if (masked) {  // scores that the row does not see become -inf, in place
 #pragma unroll 1
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < S::kKeys / 32; ++w) {
               const uint32_t bits = w == 0 ? vis[0] : w == 1 ? vis[1] : w == 2 ? vis[2] : vis[3];
               if (__all_sync(kFull, bits == ~0u)) continue;
               uint32_t y[32];
@@ -658,15 +676,11 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             tc_wait_ld(x);
           };
           // (kRaw: loops over chunks, for the instruction cache's sake.)
-          constexpr int kUnroll = S::kRaw ? 1 : kTile / W;
-          float mt = -INFINITY, cf[2] = {c_row, c_row};      // of the tile's halves
-          if constexpr (S::kRaw) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              cf[k] = fmaxf(c_row * scale_value(k_scale[rs][tiles & 3][S::kParts == 2 ? k : 0]), 1.2e-38f);
-          }
+          constexpr int kChunks = S::kKeys / W, kUnroll = S::kRaw ? 1 : kChunks;
+          float mt = -INFINITY, cf = c_row;
+          if constexpr (S::kRaw) cf = fmaxf(c_row * scale_value(k_scale[rs][tiles % kScaleRing]), 1.2e-38f);
 #pragma unroll kUnroll
-          for (int ch = 0; ch < kTile / W; ++ch) {
+          for (int ch = 0; ch < kChunks; ++ch) {
             load_s(ch);
             float q0 = -INFINITY, q1 = -INFINITY, q2 = -INFINITY, q3 = -INFINITY;
 #pragma unroll
@@ -676,7 +690,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
               q2 = fmaxf(q2, __uint_as_float(x[k + 2]));
               q3 = fmaxf(q3, __uint_as_float(x[k + 3]));
             }
-            mt = fmaxf(mt, fmaxf(fmaxf(q0, q1), fmaxf(q2, q3)) * (ch * W < 64 ? cf[0] : cf[1]));
+            mt = fmaxf(mt, fmaxf(fmaxf(q0, q1), fmaxf(q2, q3)) * cf);
           }
           // Raise the reference where the tile's maximum is more than 2^8
           // above it (or nothing was seen before).
@@ -690,6 +704,9 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             }
             __syncwarp();
             if (j > 0) {
+              // (kBufs == 2: the products of the tile before may still run.)
+              if (!(ok = wait_warp(&bars.o_done[s][(tiles - 1) % S::kBufs], (tiles - 1) / S::kBufs, err))) break;
+              tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -701,15 +718,13 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
               }
             }
           }
-          const uint64_t nm2 = f2_pack(-mc, -mc);
+          const uint64_t nm2 = f2_pack(-mc, -mc), c2 = f2_pack(cf, cf);
           uint64_t l2a = 0, l2b = 0;
           // The last chunk first: it is in registers, and P's columns are the
           // upper half of S, where a chunk's P covers only S already taken.
 #pragma unroll kUnroll
-          for (int ch = kTile / W - 1; ch >= 0; --ch) {
-            if (S::kRaw || ch < kTile / W - 1) load_s(ch);
-            const float cc = ch * W < 64 ? cf[0] : cf[1];
-            const uint64_t c2 = f2_pack(cc, cc);
+          for (int ch = kChunks - 1; ch >= 0; --ch) {
+            if (S::kRaw || ch < kChunks - 1) load_s(ch);
             uint32_t pk[W / 2];
 #pragma unroll
             for (int k = 0; k < W; k += 2) {
@@ -723,9 +738,9 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
               else l2b = f2_add(l2b, f2_pack(y0, y1));
               pk[k >> 1] = pack2<typename S::M>(y0, y1);
             }
-            if constexpr (W == 64) tc_st32(col_s + kPOff + ch * (W / 2), pk);
-            else tc_st16(col_s + kPOff + ch * (W / 2), pk);
-            if (ch * W == kTile / 2) {  // the upper half of P is complete: its products may start
+            if constexpr (W == 64) tc_st32(col_s + S::kPOff + ch * (W / 2), pk);
+            else tc_st16(col_s + S::kPOff + ch * (W / 2), pk);
+            if (S::kKeys == 128 && ch * W == 64) {  // the upper half of P is complete: its products may start
               tc_wait_st();
               tc_fence_before();
               __syncwarp();
@@ -739,16 +754,16 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           l += (e0 + e1) + (e2 + e3);
           tc_wait_st();
           tc_fence_before();
-        } else if (lane == 0) {
+        } else if (S::kKeys == 128 && lane == 0) {
           sv::mbar_arrive(sv::smem_addr(&bars.p_half[s]));
         }
         __syncwarp();
-        if (lane == 0) sv::mbar_arrive(sv::smem_addr(&bars.p_ready[s]));
+        if (lane == 0) sv::mbar_arrive(sv::smem_addr(&bars.p_ready[s][buf]));
       }
       if (!ok) break;
-      next_segment(a, upt, walk);
+      next_segment<S::kKeys>(a, upt, walk);
       if (S::kRaw && walk.on && !(ok = prepare_q(walk))) break;   // while the last products run
-      if (!(ok = wait_warp(&bars.o_done[s], ph_o++, err))) break;
+      if (!(ok = wait_warp(&bars.o_done[s][(tiles - 1) % S::kBufs], (tiles - 1) / S::kBufs, err))) break;
       tc_fence_after();
       const float vs = S::kRaw ? scale_value(v_scale[rs][seg % kSegRing] & 255) : 1.f;
       const bool bad = seg_bad[rs][seg % kSegRing] == seg + 1;
@@ -816,8 +831,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // One warp per stream, or (kPair) one for K and one for V.  Lane i looks
     // up box i of a tile, an elected lane issues the copies (~90 cycles each).
     const int s = warp - 8, rs = kPair ? 0 : s;
-    const int box = p.box, nb = kTile / box;                  // boxes of a tile, at most 16
-    const int nbp = nb / S::kParts;                           // and of a stage
+    const int box = p.box, nb = S::kKeys / box;               // boxes of a stage, at most 16
     constexpr int kRing = S::kRaw ? S::kRawStages : S::kStages;
     uint64_t *const fullb = S::kRaw ? rings[rs].rfull : rings[rs].full;
     uint64_t *const emptyb = S::kRaw ? rings[rs].rempty : rings[rs].empty;
@@ -825,66 +839,72 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
                                     : sv::smem_addr(ring0) + rs * (S::kStages * S::kStageBytes);
     constexpr int kRingBytes = S::kRaw ? S::kRawBytes : S::kStageBytes;
     int issued = -1, q_issued = 0;                      // last position, Q loads
-    // This lane's box of a tile: its block (-2: none) and the row in it.
+    // This lane's box of a tile: its block and the row in it (-1: no box).
     struct Box {
-      int id, row;
+      int id, row, h;
     };
+    const int32_t *table = nullptr;          // the segment's
+    int block = 0, row = 0;                  // of the lane's box in the tile
+    const int step_block = S::kKeys / a.c.bs, step_row = S::kKeys - step_block * a.c.bs;
     const auto fetch = [&](const Tile &w) {
-      Box x = {-2, 0};
-      const int pos = w.t * kTile + lane * box;
+      const int pos = w.t * S::kKeys + lane * box;
+      if (w.first()) {
+        table = a.c.tables + static_cast<size_t>(w.b) * a.c.max_blocks;
+        block = pos / a.c.bs;
+        row = pos - block * a.c.bs;
+      } else {
+        block += step_block;
+        row += step_row;
+        if (row >= a.c.bs) {
+          row -= a.c.bs;
+          ++block;
+        }
+      }
+      Box x = {0, -1, w.h};
       if (w.on && lane < nb && pos < w.kv_end) {
-        const int j = pos / a.c.bs;
-        x.row = pos - j * a.c.bs;
-        x.id = ld32(a.c.tables + static_cast<size_t>(w.b) * a.c.max_blocks + j);
+        x.row = row;
+        x.id = ld32(table + block);
       }
       return x;
     };
     // A block that is not there marks the segment, whose unit is recomputed;
     // any block is loaded in its place.
     const auto settle = [&](Box &x, const Tile &w) {
-      const bool in = lane < nb && w.t * kTile + lane * box < w.kv_end;
-      if (in && (x.id < 0 || x.id >= a.c.num_blocks)) {
+      if (x.row >= 0 && static_cast<uint32_t>(x.id) >= static_cast<uint32_t>(a.c.num_blocks)) {
         report(a.bt.status, x.id == -1 ? SV_KV_MISSING_BLOCK : SV_KV_BAD_BLOCK);
         seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
         x.id = 0;
       }
-      if (!in) x.id = -2;
     };
-    // A tile's K or V into the stages from position `pos` on.
-    const auto load = [&](const Box &x, int h, bool is_v, int pos) {
+    // A tile's K or V into the stage of position `pos`.
+    const auto load = [&](const Box &x, bool is_v, int pos) {
       const CUtensorMap *map = is_v ? &p.vmap : &p.kmap;
       constexpr int srow = D / SV_KV_GROUP;
       const uint32_t box_bytes = S::kRaw ? box * (D + srow) : S::kHalves * box * 128;
-      const int boxes = __popc(__ballot_sync(kFull, x.id >= 0));   // the first ones
+      const int boxes = __popc(__ballot_sync(kFull, x.row >= 0));  // the first ones
+      const uint8_t *scales = S::kRaw ? (is_v ? a.c.vs : a.c.ks) + static_cast<int64_t>(x.h) * a.c.bs * srow : nullptr;
+      const int st = pos % kRing;
+      if (pos >= kRing && !wait_warp(&emptyb[st], pos / kRing - 1, err)) return false;
+      const uint32_t bar = sv::smem_addr(&fullb[st]), dst = stage0 + st * kRingBytes;
+      if (elect_one()) sv::mbar_arrive_expect_tx(bar, boxes * box_bytes);
+      __syncwarp();
 #pragma unroll 1
-      for (int q = 0; q < S::kParts; ++q, ++pos) {
-        const int part = is_v ? S::kParts - 1 - q : q, st = pos % kRing;
-        if (pos >= kRing && !wait_warp(&emptyb[st], pos / kRing - 1, err)) return false;
-        const uint32_t bar = sv::smem_addr(&fullb[st]), dst = stage0 + st * kRingBytes;
-        const int i0 = part * nbp, i1 = min(i0 + nbp, boxes);
-        if (elect_one()) sv::mbar_arrive_expect_tx(bar, max(i1 - i0, 0) * box_bytes);
-        __syncwarp();
-#pragma unroll 1
-        for (int i = i0; i < i1; ++i) {
-          const int id = __shfl_sync(kFull, x.id, i), row = __shfl_sync(kFull, x.row, i);
-          const int at = (i - i0) * box;     // row in the stage
-          if (elect_one()) {
-            if constexpr (S::kRaw) {
-              tma_4d(dst + at * D, map, 0, row, h, id, bar);
-              bulk_1d(dst + S::kRawData + at * srow,
-                      (is_v ? a.c.vs : a.c.ks) + id * a.c.sblock_bytes +
-                          (static_cast<int64_t>(h) * a.c.bs + row) * srow,
-                      box * srow, bar);
-            } else {
+      for (int i = 0; i < boxes; ++i) {
+        const int id = __shfl_sync(kFull, x.id, i), row = __shfl_sync(kFull, x.row, i);
+        const int at = i * box;              // row in the stage
+        if (elect_one()) {
+          if constexpr (S::kRaw) {
+            tma_4d(dst + at * D, map, 0, row, x.h, id, bar);
+            bulk_1d(dst + S::kRawData + at * srow, scales + id * a.c.sblock_bytes + row * srow, box * srow, bar);
+          } else {
 #pragma unroll
-              for (int hf = 0; hf < S::kHalves; ++hf)
-                tma_4d(dst + hf * S::kHalf + at * 128, map, hf * 64, row, h, id, bar);
-            }
+            for (int hf = 0; hf < S::kHalves; ++hf)
+              tma_4d(dst + hf * S::kHalf + at * 128, map, hf * 64, row, x.h, id, bar);
           }
-          __syncwarp();
         }
-        issued = pos;
+        __syncwarp();
       }
+      issued = pos;
       return true;
     };
     // A segment's queries: whole tokens, G heads each, in the swizzled layout.
@@ -908,39 +928,26 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     };
     Walk walk = sh_walk[rs];
     Tile w = tile_of(walk);
-    Box x = fetch(w);
-    if constexpr (kPair) {
+    const int n = count_of(walk);
+    Box x = fetch(w), b0 = x, b1 = x;        // of the next K; of the two tiles before
+    const int last = kPair ? 2 * n + s : 2 * n;
 #pragma unroll 1
-      for (int i = 0; ok && w.on; ++i) {
-        Box now = x;
-        settle(now, w);
-        const Tile at = w;
-        next_tile(a, upt, walk, w);
-        x = fetch(w);                        // on its way while the stage is waited for
-        ok = load(now, at.h, s == 1, 2 * i + s);
-        if (ok && at.first() && s == 0) ok = load_q(at);
-      }
-    } else {
-      // Turn -1: K of the first tile; then a tile's V and the next tile's K.
-      int pos = 0;
+    for (int pos = kPair ? s : 0; ok && pos < last; pos += kPair ? 2 : 1) {
+      const bool is_v = kPair ? s == 1 : (pos >= 2 && !(pos & 1)) || pos == 2 * n - 1;
+      Box now = pos == 2 * n - 1 ? b1 : b0;
+      bool q = false;
       Tile at = w;
-      Box now = x;
-#pragma unroll 1
-      for (bool begun = false; ok; begun = true) {
-        if (begun) {
-          ok = load(now, at.h, true, pos);
-          pos += S::kParts;
-        }
-        if (!ok || !w.on) break;
-        at = w;
+      if (kPair || !is_v) {
         now = x;
-        settle(now, at);
-        next_tile(a, upt, walk, w);
+        settle(now, w);
+        b0 = b1;
+        b1 = now;
+        q = w.first() && !is_v;
+        next_tile<S::kKeys>(a, upt, walk, w);
         x = fetch(w);                        // on its way while stages are waited for
-        ok = load(now, at.h, false, pos);
-        pos += S::kParts;
-        if (ok && at.first()) ok = load_q(at);
       }
+      ok = load(now, is_v, pos);
+      if (ok && q) ok = load_q(at);
     }
     if (!ok) {  // copies in flight land before the block ends (a position not issued: the wait gives up)
 #pragma unroll 1
@@ -959,7 +966,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const uint64_t k_desc = smem_desc(sv::smem_addr(ring), 16);
     const uint64_t v_desc = smem_desc(sv::smem_addr(ring), S::kHalf);
     const uint32_t ts = tmem + kColS + 128u * s, to = tmem + kColO + 128u * s;
-    uint32_t ph_p = 0, fix = 0;    // parities: of P, of the repairs per stage
+    uint32_t fix = 0;              // parities of the repairs, per stage
+    uint32_t nk = 0, nv = 0;       // tiles multiplied so far
     const auto take = [&](int pos) {
       const bool good = wait_warp(&rb.full[pos % S::kStages], pos / S::kStages, err);
       tc_fence_after();
@@ -991,75 +999,67 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // S of the tile whose K is at `pos`.
     const auto qk = [&](const Tile &w, int pos) {
       if (w.first() && !wait_warp(S::kRaw ? &bars.q_ready[s] : &bars.q_full[rs], w.seg, err)) return false;
-#pragma unroll 1
-      for (int part = 0; part < S::kParts; ++part, ++pos) {
-        if (!take(pos)) return false;
-        const uint64_t kd = k_desc + (pos % S::kStages) * (S::kStageBytes >> 4);
-        if (elect_one()) {
+      if (!take(pos)) return false;
+      const uint64_t kd = k_desc + (pos % S::kStages) * (S::kStageBytes >> 4);
+      const uint32_t buf = nk % S::kBufs;
+      if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc_mma_ss(ts + part * S::kKeys, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
-                      kd + (((k >> 2) * S::kHalf + (k & 3) * 32) >> 4), kQK, k > 0);
-          tc_commit(sv::smem_addr(&rb.empty[pos % S::kStages]));
-          if (part == S::kParts - 1) {
-            tc_commit(sv::smem_addr(&bars.s_full[s]));
-            if (w.last()) tc_commit(sv::smem_addr(&bars.q_empty[s]));
-          }
-        }
-        __syncwarp();
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma_ss(ts + 64u * buf, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
+                    kd + (((k >> 2) * S::kHalf + (k & 3) * 32) >> 4), kQK, k > 0);
+        tc_commit(sv::smem_addr(&rb.empty[pos % S::kStages]));
+        tc_commit(sv::smem_addr(&bars.s_full[s][buf]));
+        if (w.last()) tc_commit(sv::smem_addr(&bars.q_empty[s]));
       }
+      __syncwarp();
+      ++nk;
       return true;
     };
-    // O += P V, keys 64 .. 127 of the tile first: their P is ready first.
+    // O += P V; of 128 keys the upper half first: its P is ready first.
     const auto pv = [&](const Tile &w, int pos) {
-#pragma unroll 1
-      for (int half = 1; half >= 0; --half) {
-        const int st = pos % S::kStages;
-        if (half == 1 || S::kParts == 2) {            // a stage begins
-          if (!take(pos)) return false;
-          const int k0 = w.t * kTile + (S::kParts == 2 ? half * S::kKeys : 0);
-          if (!S::kRaw && k0 + S::kKeys > w.new0) {
-            if (!kPair || s == 0) {
-              repair(w, k0, st);
-              if (kPair && lane == 0) sv::mbar_arrive(sv::smem_addr(&rb.fixed[st]));
-            } else {
-              if (!wait_warp(&rb.fixed[st], fix >> st, err)) return false;
-              fix ^= 1u << st;
-            }
-          }
+      const int st = pos % S::kStages, k0 = w.t * S::kKeys;
+      if (!take(pos)) return false;
+      if (!S::kRaw && k0 + S::kKeys > w.new0) {
+        if (!kPair || s == 0) {
+          repair(w, k0, st);
+          if (kPair && lane == 0) sv::mbar_arrive(sv::smem_addr(&rb.fixed[st]));
+        } else {
+          if (!wait_warp(&rb.fixed[st], fix >> st, err)) return false;
+          fix ^= 1u << st;
         }
-        if (!wait_warp(half ? &bars.p_half[s] : &bars.p_ready[s], ph_p, err)) return false;
+      }
+      const uint32_t buf = nv % S::kBufs;
+#pragma unroll 1
+      for (int half = S::kKeys / 64 - 1; half >= 0; --half) {
+        if (!wait_warp(half ? &bars.p_half[s] : &bars.p_ready[s][buf], half ? nv : nv / S::kBufs, err)) return false;
         tc_fence_after();
-        // Its 64 keys: rows 64 * half .. of a whole tile, or all of a half one.
-        const uint64_t vd = v_desc + st * (S::kStageBytes >> 4) + (S::kParts == 1 ? half * (64 * 128 >> 4) : 0);
-        const uint32_t first = w.first() && half == 1;
+        const uint64_t vd = v_desc + st * (S::kStageBytes >> 4) + half * (64 * 128 >> 4);
+        const uint32_t first = w.first() && half == S::kKeys / 64 - 1;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma_ts(to, ts + kPOff + 32u * half + 8u * k, vd + k * (2048 >> 4), kPV, !(first && k == 0));
-          if (half == 0 || S::kParts == 2) tc_commit(sv::smem_addr(&rb.empty[st]));
-          if (half == 0 && w.last()) tc_commit(sv::smem_addr(&bars.o_done[s]));
+            tc_mma_ts(to, ts + 64u * buf + S::kPOff + 32u * half + 8u * k, vd + k * (2048 >> 4), kPV,
+                      !(first && k == 0));
+          if (half == 0) {
+            tc_commit(sv::smem_addr(&rb.empty[st]));
+            tc_commit(sv::smem_addr(&bars.o_done[s][buf]));
+          }
         }
         __syncwarp();
-        if (S::kParts == 2) ++pos;
       }
-      ph_p ^= 1u;
+      ++nv;
       return true;
     };
     Walk walk = sh_walk[rs];
-    Tile w = tile_of(walk);
-    int pos = 0;
+    Tile w = tile_of(walk), behind = w;
+    const int n = count_of(walk);
 #pragma unroll 1
-    for (bool begun = false; ok; begun = true) {
-      if (begun) {
-        ok = pv(w, pos);
-        pos += S::kParts;
-        if (!ok) break;
-        next_tile(a, upt, walk, w);
-      }
-      if (!w.on) break;
-      ok = qk(w, pos);
-      pos += S::kParts;
+    for (int i = 0, pos = 0; ok && i < n + S::kBufs - 1; ++i) {
+      if (i < n) ok = qk(w, pos++);
+      if (kPair) behind = w;
+      if (ok && (kPair || i > 0)) ok = pv(behind, pos++);
+      behind = w;
+      if (i < n) next_tile<S::kKeys>(a, upt, walk, w);
     }
     if (!ok) {  // issued products end before TMEM is freed
       if (elect_one()) tc_commit(sv::smem_addr(&bars.drain[s]));
@@ -1096,7 +1096,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     RingBars &rb = rings[rs];
     uint8_t *const ring = ring0 + rs * (S::kStages * S::kStageBytes);
     uint8_t *const raw = raw0 + rs * (S::kRawStages * S::kRawBytes);
-    int v_ref = 0, k_tile = 0;
+    int v_ref = 0;
     // This thread's chunks: 16 codes (column group ch) of every kRowStep-th row.
     // Eight lanes write 4 chunks of one row and 4 of the next, whose swizzles
     // differ in the lowest bit: eight different 16-byte columns of the banks.
@@ -1107,10 +1107,10 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const int from = row0 * D + ch * 16;
     const int to_row = (ch >> 2) * S::kHalf + row0 * 128, c0 = (ch & 3) * 2;
     const int to_lo = to_row + ((c0 ^ (row0 & 7)) << 4), to_hi = to_row + (((c0 + 1) ^ (row0 & 7)) << 4);
-    // Stage q of a tile's K or V, at position `pos`.
-    const auto widen = [&](const Tile &w, bool is_v, int q, int pos) {
+    // A tile's K (the range's k-th) or V, at position `pos`.
+    const auto widen = [&](const Tile &w, bool is_v, int pos, int k) {
       const int st = pos % S::kStages, rst = pos % kRS;
-      const int k0 = w.t * kTile + (is_v ? S::kParts - 1 - q : q) * S::kKeys;
+      const int k0 = w.t * S::kKeys;
       if (pos >= S::kStages && !wait_warp(&rb.empty[st], pos / S::kStages - 1, err)) return false;
       if (!wait_warp(&rb.rfull[rst], pos / kRS, err)) return false;
       const uint8_t *src = raw + rst * S::kRawBytes;
@@ -1120,10 +1120,10 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       const int live = min(w.kv_end - k0, S::kKeys);  // rows that hold tokens
       int *const vs = &v_scale[rs][w.seg % kSegRing];
       if (is_v) {
-        if (w.first()) v_ref = 0;
-        if (v_ref == 0 && !(w.first() && q == 0) && S::kParts == 2) {  // the other group may have set it, in V's last stage
-          const int last = q == 0 ? pos - 3 : pos - 1;
-          if (!wait_warp(&rb.full[last % S::kStages], last / S::kStages, err)) return false;
+        if (w.first()) {
+          v_ref = 0;
+        } else if (!kPair && grp) {                   // a range's last V: the other group had the one before
+          if (!wait_warp(&rb.full[(pos - 1) % S::kStages], (pos - 1) / S::kStages, err)) return false;
           const int x = *vs;
           v_ref = x & 256 ? x & 255 : 0;
         }
@@ -1152,15 +1152,14 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           __syncwarp();
           if (ht == 0) *vs = v_ref ? 256 + ref : ref;
         } else if (ht == 0) {
-          k_scale[rs][k_tile & 3][q] = ref;
+          k_scale[rs][k % kScaleRing] = ref;
         }
       }
-      // Scales that the products cannot hold (448 * 2^7 is below fp16's
-      // largest), and NaN: the unit is recomputed.
-      const int below = ref - (is_v ? 16 : 24), above = min(is_v ? ref + 7 : ref, 254);
-      bool found = false;
       // A turn's chunks together, loads first: a chunk alone is a chain of
       // latencies.
+      bool found = false;
+      const int least = ref - 14;
+      const uint32_t span = min(is_v ? 14 + 7 : 14, 254 - least);   // 255: NaN
 #pragma unroll 1
       for (int t0 = 0; t0 < kRows; t0 += kTurn) {
         uint4 c[kTurn];
@@ -1170,20 +1169,36 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           c[t] = *reinterpret_cast<const uint4 *>(src + from + (t0 + t) * kRowStep * D);
           x[t] = sc[row0 * kSc + (ch >> 1) + (t0 + t) * kRowStep * kSc];
         }
+        // 2^(e - E) as fp16, twice: where it is a normal number, its exponent
+        // field; else (rows behind the last token, zeros, scales far apart)
+        // rounded as fp32 is, a subnormal number or 0 where it is that small.
+        uint32_t far = 0, m[kTurn];
 #pragma unroll
         for (int t = 0; t < kTurn; ++t) {
-          found = found || (row0 + (t0 + t) * kRowStep < live && x[t] > 7 && (x[t] < below || x[t] > above));
-          // 2^(e - E), rounded to fp16 as fp32 is: a subnormal number or 0 where
-          // it is that small.
-          const float mf = __uint_as_float(static_cast<uint32_t>(min(max(x[t] - ref + 127, 0), 254)) << 23);
-          const __half2 m = __float2half2_rn(mf);
+          far = max(far, static_cast<uint32_t>(x[t] - least));
+          m[t] = (x[t] - least + 1) * 0x04000400u;
+        }
+        if (__any_sync(kFull, far > span)) {
+          // Scales that the products cannot hold (448 * 2^7 is below fp16's
+          // largest), and NaN: the unit is recomputed.
+          const int below = ref - (is_v ? 16 : 24), above = min(is_v ? ref + 7 : ref, 254);
+#pragma unroll
+          for (int t = 0; t < kTurn; ++t) {
+            found = found || (row0 + (t0 + t) * kRowStep < live && x[t] > 7 && (x[t] < below || x[t] > above));
+            const float mf = __uint_as_float(static_cast<uint32_t>(min(max(x[t] - ref + 127, 0), 254)) << 23);
+            m[t] = pack2<F16>(mf, mf);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < kTurn; ++t) {
+          const __half2 mul = *reinterpret_cast<const __half2 *>(&m[t]);
           const uint32_t u[4] = {c[t].x, c[t].y, c[t].z, c[t].w};
           uint32_t o[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
                 static_cast<__nv_fp8x2_storage_t>(u[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
-            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), m);
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), mul);
             o[k] = *reinterpret_cast<const uint32_t *>(&y);
           }
           uint8_t *to = dst + (t0 + t) * kRowStep * 128;
@@ -1216,15 +1231,16 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     };
     Walk walk = sh_walk[rs];
     Tile w = tile_of(walk);
-    // Whole tiles: group 0 has their K, group 1 their V; half ones: a half of both each.
+    const int n = count_of(walk);
+    // kPair: one group has K, the other V.  Else group 0 has K0 V0 V1 .., group
+    // 1 K1 K2 .. and the last V.
+    bool step = !kPair && grp && n > 1;      // to the next tile
 #pragma unroll 1
-    for (int i = 0; ok && w.on; ++i) {
-      const bool is_v = kPair ? grp == 1 : i & 1;
-      ok = widen(w, is_v, kPair ? 0 : grp, 2 * i + grp);
-      if (kPair || is_v) {
-        ++k_tile;
-        next_tile(a, upt, walk, w);
-      }
+    for (int i = 0; ok && i < n; ++i) {
+      if (step) next_tile<S::kKeys>(a, upt, walk, w);
+      const bool is_v = kPair ? grp : grp ? i == n - 1 : i > 0;
+      ok = widen(w, is_v, 2 * i + grp, kPair || !grp ? i : i + 1);
+      step = kPair || (grp ? i + 2 < n : i > 0);
     }
   }
 

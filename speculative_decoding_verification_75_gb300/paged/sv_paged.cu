@@ -302,7 +302,7 @@ bool tc_takes(const sv_tree_attention_args *a, const AttnParams &p, const TcLayo
   if (p.c.bs % 8 || p.c.num_blocks < 1 || p.G > kTile || !p.qvec) return false;
   if (a->cache.dtype == SV_E4M3 && (a->dtype != SV_BF16 || p.c.sblock_bytes % 16)) return false;
   if (p.c.block_bytes >= (int64_t{1} << 40)) return false;
-  const int64_t tiles = std::max<int64_t>((static_cast<int64_t>(p.c.max_blocks) * p.c.bs + kTile - 1) / kTile, 1);
+  const int64_t tiles = std::max<int64_t>((static_cast<int64_t>(p.c.max_blocks) * p.c.bs + 63) / 64, 1);   // of 64 keys
   const int64_t units = static_cast<int64_t>(p.bt.B) * p.c.heads * w.MP;
   return units <= INT_MAX / tiles;
 }
@@ -354,7 +354,7 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
   p.slot_floats = w.slot_floats;
   const bool pair = ap.bt.T > w.TT;
   p.box = 8;  // a power of two that divides the block size, at most a stage
-  while (p.box < (pair ? kTile : kTile / 2) && ap.c.bs % (2 * p.box) == 0) p.box *= 2;
+  while (p.box < (pair ? 128 : 64) && ap.c.bs % (2 * p.box) == 0) p.box *= 2;
   p.c = std::max(std::fabs(ap.scale_log2), 1.2e-38f);  // not 0: -inf times it stays -inf
   p.negate = ap.scale_log2 < 0.f;
   p.TT = w.TT;
