@@ -876,35 +876,48 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         x.id = 0;
       }
     };
-    // A tile's K or V into the stage of position `pos`.
-    const auto load = [&](const Box &x, bool is_v, int pos) {
+    // A tile's K or V into the next stage.
+    int st = kPair ? s : 0, round = 0;       // of the next position
+    const uint32_t sblock = static_cast<uint32_t>(a.c.sblock_bytes);   // < 2^31
+    const auto load = [&](const Box &x, bool is_v) {
       const CUtensorMap *map = is_v ? &p.vmap : &p.kmap;
       constexpr int srow = D / SV_KV_GROUP;
       const uint32_t box_bytes = S::kRaw ? box * (D + srow) : S::kHalves * box * 128;
       const int boxes = __popc(__ballot_sync(kFull, x.row >= 0));  // the first ones
-      const uint8_t *scales = S::kRaw ? (is_v ? a.c.vs : a.c.ks) + static_cast<int64_t>(x.h) * a.c.bs * srow : nullptr;
-      const int st = pos % kRing;
-      if (pos >= kRing && !wait_warp(&emptyb[st], pos / kRing - 1, err)) return false;
-      const uint32_t bar = sv::smem_addr(&fullb[st]), dst = stage0 + st * kRingBytes;
-      if (elect_one()) sv::mbar_arrive_expect_tx(bar, boxes * box_bytes);
-      __syncwarp();
-#pragma unroll 1
-      for (int i = 0; i < boxes; ++i) {
-        const int id = __shfl_sync(kFull, x.id, i), row = __shfl_sync(kFull, x.row, i);
+      const uint8_t *scales = is_v ? a.c.vs : a.c.ks;
+      if (round > 0 && !wait_warp(&emptyb[st], round - 1, err)) return false;
+      const uint32_t bar = sv::smem_addr(fullb) + 8u * st, dst = stage0 + st * kRingBytes;
+      const auto issue = [&](int i, int id, int row) {
         const int at = i * box;              // row in the stage
-        if (elect_one()) {
-          if constexpr (S::kRaw) {
-            tma_4d(dst + at * D, map, 0, row, x.h, id, bar);
-            bulk_1d(dst + S::kRawData + at * srow, scales + id * a.c.sblock_bytes + row * srow, box * srow, bar);
-          } else {
+        if constexpr (S::kRaw) {
+          tma_4d(dst + at * D, map, 0, row, x.h, id, bar);
+          bulk_1d(dst + S::kRawData + at * srow,
+                  scales + static_cast<uint64_t>(static_cast<uint32_t>(id)) * sblock + (x.h * a.c.bs + row) * srow,
+                  box * srow, bar);
+        } else {
 #pragma unroll
-            for (int hf = 0; hf < S::kHalves; ++hf)
-              tma_4d(dst + hf * S::kHalf + at * 128, map, hf * 64, row, x.h, id, bar);
-          }
+          for (int hf = 0; hf < S::kHalves; ++hf)
+            tma_4d(dst + hf * S::kHalf + at * 128, map, hf * 64, row, x.h, id, bar);
+        }
+      };
+      int i = 0;
+#pragma unroll 1
+      do {                                   // two boxes at a time: their look-ups overlap
+        const int id0 = __shfl_sync(kFull, x.id, i), id1 = __shfl_sync(kFull, x.id, i + 1);
+        const int row0 = __shfl_sync(kFull, x.row, i), row1 = __shfl_sync(kFull, x.row, i + 1);
+        if (elect_one()) {
+          if (i == 0) sv::mbar_arrive_expect_tx(bar, boxes * box_bytes);
+          if (i < boxes) issue(i, id0, row0);
+          if (i + 1 < boxes) issue(i + 1, id1, row1);
         }
         __syncwarp();
+      } while ((i += 2) < boxes);
+      issued = round * kRing + st;
+      st += kPair ? 2 : 1;
+      if (st >= kRing) {
+        st -= kRing;
+        ++round;
       }
-      issued = pos;
       return true;
     };
     // A segment's queries: whole tokens, G heads each, in the swizzled layout.
@@ -928,26 +941,35 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     };
     Walk walk = sh_walk[rs];
     Tile w = tile_of(walk);
-    const int n = count_of(walk);
-    Box x = fetch(w), b0 = x, b1 = x;        // of the next K; of the two tiles before
-    const int last = kPair ? 2 * n + s : 2 * n;
+    Box x = fetch(w);                        // of the next K
+    if constexpr (kPair) {
 #pragma unroll 1
-    for (int pos = kPair ? s : 0; ok && pos < last; pos += kPair ? 2 : 1) {
-      const bool is_v = kPair ? s == 1 : (pos >= 2 && !(pos & 1)) || pos == 2 * n - 1;
-      Box now = pos == 2 * n - 1 ? b1 : b0;
-      bool q = false;
-      Tile at = w;
-      if (kPair || !is_v) {
-        now = x;
+      while (ok && w.on) {
+        const Tile at = w;
+        Box now = x;
         settle(now, w);
-        b0 = b1;
-        b1 = now;
-        q = w.first() && !is_v;
         next_tile<S::kKeys>(a, upt, walk, w);
-        x = fetch(w);                        // on its way while stages are waited for
+        x = fetch(w);                        // on its way while the stage is waited for
+        ok = load(now, s == 1);
+        if (ok && at.first() && s == 0) ok = load_q(at);
       }
-      ok = load(now, is_v, pos);
-      if (ok && q) ok = load_q(at);
+    } else {
+      const int n2 = 2 * count_of(walk);
+      Box b0 = x, b1 = x;                    // of the two tiles before
+#pragma unroll 1
+      for (int pos = 0; ok && pos < n2; ++pos) {
+        if ((pos & 1 || pos == 0) && pos + 1 < n2) {
+          b0 = b1;
+          settle(x, w);
+          b1 = x;
+          ok = load(x, false);
+          if (ok && w.first()) ok = load_q(w);
+          next_tile<S::kKeys>(a, upt, walk, w);
+          x = fetch(w);                      // on its way while a V is loaded
+        } else {
+          ok = load(pos + 1 < n2 ? b0 : b1, true);
+        }
+      }
     }
     if (!ok) {  // copies in flight land before the block ends (a position not issued: the wait gives up)
 #pragma unroll 1
@@ -1107,12 +1129,12 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const int from = row0 * D + ch * 16;
     const int to_row = (ch >> 2) * S::kHalf + row0 * 128, c0 = (ch & 3) * 2;
     const int to_lo = to_row + ((c0 ^ (row0 & 7)) << 4), to_hi = to_row + (((c0 + 1) ^ (row0 & 7)) << 4);
-    // A tile's K (the range's k-th) or V, at position `pos`.
-    const auto widen = [&](const Tile &w, bool is_v, int pos, int k) {
-      const int st = pos % S::kStages, rst = pos % kRS;
+    // A tile's K (the range's k-th) or V, at the group's next position.
+    int st = grp, round = 0, rst = grp, rround = 0;
+    const auto widen = [&](const Tile &w, bool is_v, int k) {
       const int k0 = w.t * S::kKeys;
-      if (pos >= S::kStages && !wait_warp(&rb.empty[st], pos / S::kStages - 1, err)) return false;
-      if (!wait_warp(&rb.rfull[rst], pos / kRS, err)) return false;
+      if (round > 0 && !wait_warp(&rb.empty[st], round - 1, err)) return false;
+      if (!wait_warp(&rb.rfull[rst], rround, err)) return false;
       const uint8_t *src = raw + rst * S::kRawBytes;
       const uint8_t *sc = src + S::kRawData;
       uint8_t *dst = ring + st * S::kStageBytes;
@@ -1123,7 +1145,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         if (w.first()) {
           v_ref = 0;
         } else if (!kPair && grp) {                   // a range's last V: the other group had the one before
-          if (!wait_warp(&rb.full[(pos - 1) % S::kStages], (pos - 1) / S::kStages, err)) return false;
+          const int pos = round * S::kStages + st - 1;
+          if (!wait_warp(&rb.full[pos % S::kStages], pos / S::kStages, err)) return false;
           const int x = *vs;
           v_ref = x & 256 ? x & 255 : 0;
         }
@@ -1227,6 +1250,14 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         sv::mbar_arrive(sv::smem_addr(&rb.full[st]));
         sv::mbar_arrive(sv::smem_addr(&rb.rempty[rst]));
       }
+      if ((st += 2) >= S::kStages) {
+        st -= S::kStages;
+        ++round;
+      }
+      if ((rst += 2) >= kRS) {
+        rst -= kRS;
+        ++rround;
+      }
       return true;
     };
     Walk walk = sh_walk[rs];
@@ -1239,7 +1270,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     for (int i = 0; ok && i < n; ++i) {
       if (step) next_tile<S::kKeys>(a, upt, walk, w);
       const bool is_v = kPair ? grp : grp ? i == n - 1 : i > 0;
-      ok = widen(w, is_v, 2 * i + grp, kPair || !grp ? i : i + 1);
+      ok = widen(w, is_v, kPair || !grp ? i : i + 1);
       step = kPair || (grp ? i + 2 < n : i > 0);
     }
   }

@@ -301,7 +301,9 @@ bool tc_takes(const sv_tree_attention_args *a, const AttnParams &p, const TcLayo
   if (p.c.D != 64 && p.c.D != 128) return false;
   if (p.c.bs % 8 || p.c.num_blocks < 1 || p.G > kTile || !p.qvec) return false;
   if (a->cache.dtype == SV_E4M3 && (a->dtype != SV_BF16 || p.c.sblock_bytes % 16)) return false;
-  if (p.c.block_bytes >= (int64_t{1} << 40)) return false;
+  if (p.c.block_bytes >= (int64_t{1} << 40) || p.c.sblock_bytes > INT_MAX ||
+      static_cast<int64_t>(p.c.heads) * p.c.bs * (p.c.D / SV_KV_GROUP) > INT_MAX)
+    return false;
   const int64_t tiles = std::max<int64_t>((static_cast<int64_t>(p.c.max_blocks) * p.c.bs + 63) / 64, 1);   // of 64 keys
   const int64_t units = static_cast<int64_t>(p.bt.B) * p.c.heads * w.MP;
   return units <= INT_MAX / tiles;
