@@ -61,7 +61,7 @@ struct TcParams {
   uint32_t *err;       // SV_FAULT_TIMEOUT goes here
   Cut *cuts;           // [ranges] where each range begins
   float *slots;        // [ranges * 2] partial results
-  int ranges;
+  int ranges, grid;    // of the tiles; thread blocks at most
   int slot_rows;       // rows of a slot
   int slot_floats;
   int box;             // rows of a TMA box of the cache
@@ -315,10 +315,18 @@ __device__ __forceinline__ int weight_of(const AttnParams &p, int upt, int b, ui
 // Range i of N <= total over `total` tiles is [start(i), start(i + 1)): none is
 // empty.  Range i belongs to stream i / gridDim.x of block i % gridDim.x, so
 // that few tiles spread over many blocks.
-__device__ __forceinline__ int range_start(int i, int N, int total) {
-  const int q = total / N;                   // i < N <= 304: no product passes 2^31
-  return i * q + i * (total - q * N) / N;
-}
+struct Ranges {
+  int N, q, rest;
+  float inv;
+
+  __device__ __forceinline__ Ranges(int n, int total) : N(max(n, 1)), q(total / N), rest(total - q * N), inv(1.f / N) {}
+  // i * q + i * rest / N.  i, rest < N <= 304: the quotient is an integer or at
+  // least 1 / 304 from the next, the product with the reciprocal off by less
+  // than 2^-14.
+  __device__ __forceinline__ int start(int i) const {
+    return i * q + static_cast<int>((static_cast<float>(i * rest) + 0.5f) * inv);
+  }
+};
 
 // A walk over a range's tiles, unit after unit: where it stands, and the
 // segment (a run of key tiles of one unit) it is in.
@@ -384,7 +392,7 @@ __device__ __forceinline__ int count_of(const Walk &w) { return w.on ? w.left + 
 // Range i's first tile, by a whole warp: the requests are spread over the
 // lanes, 32 at a time.
 template <int kKeys>
-__device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, int ranges, Walk &w, int &total) {
+__device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, int limit, Walk &w, int &total) {
   const int lane = threadIdx.x & 31, B = p.bt.B;
   uint32_t st = 0;
   const int mine = weight_of<kKeys>(p, upt, lane, st);  // requests 0 .. 31
@@ -393,11 +401,12 @@ __device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, 
   for (int b = lane + 32; b < B; b += 32) total += weight_of<kKeys>(p, upt, b, st);
   total = __reduce_add_sync(kFull, total);
   if (i == 0) report(p.bt.status, st);
-  const int N = min(ranges, total);
+  const int N = min(limit, total);
   w = Walk{};
   if (i >= N) return;
-  const int begin = range_start(i, N, total);
-  w.left = range_start(i + 1, N, total) - begin;
+  const Ranges ranges(N, total);
+  const int begin = ranges.start(i);
+  w.left = ranges.start(i + 1) - begin;
   int base = 0, x = mine, c = 0;
 #pragma unroll 1
   for (;;) {
@@ -1287,12 +1296,14 @@ constexpr int kJoinThreads = 256;
 
 // Joins the partial results of a unit that range ends cut: block (x, y) looks
 // at the cut where range x + 1 begins and, if it is the unit's first, joins
-// part y of the unit's rows x D / 4 columns.  K threads share an output, each
-// with every K-th range.
-template <typename Q, typename C, int D, bool kPair>
+// part y of the unit's rows x D / 4 columns.  Each thread has E columns of a
+// row, so that their loads are in flight together (4 where rows are many: of
+// the 112 us that 16 trees of 64 nodes took with one column, JOIN_US), or K
+// threads share one column, each with every K-th range (few units in many parts).
+template <typename Q, typename C, int D, bool kPair, int E>
 __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid_constant__ TcParams p, const int K) {
-  __shared__ float4 so[kJoinThreads];
-  __shared__ float sm[kJoinThreads], sl[kJoinThreads];
+  __shared__ float4 so[E == 1 ? kJoinThreads : 1];
+  __shared__ float sm[E == 1 ? kJoinThreads : 1], sl[E == 1 ? kJoinThreads : 1];
   const AttnParams &a = p.a;
   const int i = static_cast<int>(blockIdx.x) + 1, tid = threadIdx.x;
   sv::pdl_wait();
@@ -1301,15 +1312,16 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
   const int4 z = __ldcg(cp + 1), u0 = __ldcg(cp + 2 * i), u1 = __ldcg(cp + 2 * i + 1);
   const int total = z.z, N = min(p.ranges, total);
   if (i >= N || u1.x == 0) return;                    // no such range, or a unit begins with it
+  const Ranges ranges(N, total);
   const int b = u0.x, h = u0.y, mp = u0.z, n = u0.w, kt = u1.y;
-  const int start = range_start(i, N, total) - u1.x;
-  if (range_start(i - 1, N, total) > start) return;   // cut before as well: another block's
-  const int c0 = i - 1, late = range_start(c0, N, total) == start ? 0 : 1;
+  const int start = ranges.start(i) - u1.x, c0 = i - 1, before = ranges.start(c0);
+  if (before > start) return;                         // cut before as well: another block's
+  const int late = before == start ? 0 : 1;
   // The range of the unit's last tile: an estimate, put right.
   const int end = start + kt - 1;
   int c1 = min(N - 1, static_cast<int>(static_cast<float>(end) * N / static_cast<float>(total)));
-  while (range_start(c1, N, total) > end) --c1;
-  while (c1 + 1 < N && range_start(c1 + 1, N, total) <= end) ++c1;
+  while (ranges.start(c1) > end) --c1;
+  while (c1 + 1 < N && ranges.start(c1 + 1) <= end) ++c1;
   const int upt = p.TT * (kPair ? 2 : 1), tok0 = mp * upt, rows = min(upt, n - tok0) * a.G;
   const auto slot_of = [&](int c) {
     return p.slots + (static_cast<size_t>(c) * 2 + (c == c0 ? late : 0)) * p.slot_floats;
@@ -1317,48 +1329,65 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
   int bad = 0;
   for (int c = c0 + tid % 32; c <= c1; c += 32)
     bad |= __ldcg(reinterpret_cast<const int32_t *>(slot_of(c)) + (D + 2) * p.slot_rows);
-  if (__any_sync(kFull, bad)) {                       // the same for every warp
-    constexpr int warps = kJoinThreads / 32;
-    for (int row = blockIdx.y * warps + tid / 32; row < rows; row += gridDim.y * warps)
-      recompute_row<Q, C, D>(a, b, tok0 + row / a.G, h * a.G + row % a.G);
-    return;
-  }
+  constexpr int kCols = D / 4 / E;                    // columns e * kCols + d4, of 4 elements
   const int per = kJoinThreads / K, k = tid / per, o = blockIdx.y * per + tid % per;
-  const bool in = o < rows * (D / 4);
-  const int row = in ? o % rows : 0, d4 = in ? o / rows : 0;
+  const bool in = o < rows * kCols;
+  const int d4 = in ? o / rows : 0, row = in ? o - d4 * rows : 0;
   // Rows of the second tile start at row 128 of a slot.
   const int tile_rows = p.TT * a.G, srow = row < tile_rows ? row : kTile + row - tile_rows;
   float m = -INFINITY, l = 0.f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  const auto add = [&](float m2, float l2, float4 w) {
+  float4 v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const auto add = [&](float m2, float l2, const float4 (&w)[E]) {
     const float nm = fmaxf(m, m2), nb = nm == -INFINITY ? 0.f : nm;
     const float f = sv::ex2(m - nb), g = sv::ex2(m2 - nb);
     m = nm;
     l = l * f + l2 * g;
-    v = make_float4(v.x * f + w.x * g, v.y * f + w.y * g, v.z * f + w.z * g, v.w * f + w.w * g);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      v[e] = make_float4(v[e].x * f + w[e].x * g, v[e].y * f + w[e].y * g, v[e].z * f + w[e].z * g,
+                         v[e].w * f + w[e].w * g);
   };
   if (in) {
-#pragma unroll 4
+#pragma unroll(E == 1 ? 4 : 2)
     for (int c = c0 + k; c <= c1; c += K) {
       const float *s = slot_of(c);
-      add(__ldcg(s + D * p.slot_rows + srow), __ldcg(s + (D + 1) * p.slot_rows + srow),
-          __ldcg(reinterpret_cast<const float4 *>(s) + static_cast<size_t>(d4) * p.slot_rows + srow));
+      const float m2 = __ldcg(s + D * p.slot_rows + srow), l2 = __ldcg(s + (D + 1) * p.slot_rows + srow);
+      float4 w[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        w[e] = __ldcg(reinterpret_cast<const float4 *>(s) + static_cast<size_t>(e * kCols + d4) * p.slot_rows + srow);
+      add(m2, l2, w);
     }
   }
-  if (K > 1) {
-    so[tid] = v;
-    sm[tid] = m;
-    sl[tid] = l;
-    __syncthreads();
-    if (k > 0) return;
-    for (int q = 1; q < K; ++q) add(sm[q * per + tid], sl[q * per + tid], so[q * per + tid]);
+  if (__any_sync(kFull, bad)) {                       // the same for every warp
+    constexpr int warps = kJoinThreads / 32;
+    for (int r = blockIdx.y * warps + tid / 32; r < rows; r += gridDim.y * warps)
+      recompute_row<Q, C, D>(a, b, tok0 + r / a.G, h * a.G + r % a.G);
+    return;
+  }
+  if constexpr (E == 1) {
+    if (K > 1) {
+      so[tid] = v[0];
+      sm[tid] = m;
+      sl[tid] = l;
+      __syncthreads();
+      if (k > 0) return;
+      for (int q = 1; q < K; ++q) {
+        const float4 w[1] = {so[q * per + tid]};
+        add(sm[q * per + tid], sl[q * per + tid], w);
+      }
+    }
   }
   if (!in) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int t = tok0 + row / a.G, g = row % a.G;
   const int64_t orow = (static_cast<int64_t>(b) * a.bt.T + t) * a.Hq + h * a.G + g;
-  *reinterpret_cast<uint2 *>(a.out + orow * (D * 2) + d4 * 8) =
-      make_uint2(pack2<Q>(v.x * inv, v.y * inv), pack2<Q>(v.z * inv, v.w * inv));
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    *reinterpret_cast<uint2 *>(a.out + orow * (D * 2) + (e * kCols + d4) * 8) =
+        make_uint2(pack2<Q>(v[e].x * inv, v[e].y * inv), pack2<Q>(v[e].z * inv, v[e].w * inv));
   if (a.lse && d4 == 0) a.lse[orow] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 

@@ -293,6 +293,11 @@ TcLayout tc_layout(int64_t T, int64_t G, int64_t D) {
   return w;
 }
 
+// Key tiles of a request whose table is full.
+int64_t tc_tiles(const Cache &c, int keys) {
+  return std::max<int64_t>((static_cast<int64_t>(c.max_blocks) * c.bs + keys - 1) / keys, 1);
+}
+
 // What the tensor-core kernel takes: whole 8-row swizzle atoms per page,
 // query rows on 16-byte boundaries and a token's heads within a tile, 16-bit
 // tiles of the query's own type (an e4m3 code times its scale is a bf16
@@ -304,9 +309,8 @@ bool tc_takes(const sv_tree_attention_args *a, const AttnParams &p, const TcLayo
   if (p.c.block_bytes >= (int64_t{1} << 40) || p.c.sblock_bytes > INT_MAX ||
       static_cast<int64_t>(p.c.heads) * p.c.bs * (p.c.D / SV_KV_GROUP) > INT_MAX)
     return false;
-  const int64_t tiles = std::max<int64_t>((static_cast<int64_t>(p.c.max_blocks) * p.c.bs + 63) / 64, 1);   // of 64 keys
   const int64_t units = static_cast<int64_t>(p.bt.B) * p.c.heads * w.MP;
-  return units <= INT_MAX / tiles;
+  return units <= INT_MAX / tc_tiles(p.c, 64);
 }
 
 template <typename Q, typename C, int D, bool kPair>
@@ -320,17 +324,21 @@ sv_status tc_launch(const TcParams &p, int64_t units, int dev, sv_stream_t strea
       return SV_ERR_CUDA;
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  const int grid = p.ranges / S::kStreams;
-  if (const sv_status s = launch(k, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, stream, p))
+  if (const sv_status s = launch(k, dim3(static_cast<unsigned>(std::min(p.ranges, p.grid))), S::kThreads, S::kSmem,
+                                 stream, p))
     return s;
   if (p.ranges < 2) return SV_OK;  // nothing is cut
   // Few units are cut into many parts: then more threads share an output.
   int K = 1;
   while (K < 8 && K * 4 * units <= p.ranges) K *= 2;
-  const int per = kJoinThreads / K, rows = std::min(p.a.bt.T, p.TT * S::kTilesPerUnit) * p.a.G;
-  return launch(sv_attn_join_kernel<Q, C, D, kPair>,
-                dim3(static_cast<unsigned>(p.ranges - 1), static_cast<unsigned>((rows * (D / 4) + per - 1) / per)),
-                kJoinThreads, 0, stream, p, K);
+  const int rows = std::min(p.a.bt.T, p.TT * S::kTilesPerUnit) * p.a.G;
+  const auto join = [&](auto *kernel, int E) {
+    const int per = kJoinThreads / K;
+    return launch(kernel, dim3(static_cast<unsigned>(p.ranges - 1), static_cast<unsigned>((rows * (D / 4 / E) + per - 1) / per)),
+                  kJoinThreads, 0, stream, p, K);
+  };
+  return K == 1 && rows >= 32 ? join(sv_attn_join_kernel<Q, C, D, kPair, 4>, 4)
+                              : join(sv_attn_join_kernel<Q, C, D, kPair, 1>, 1);
 }
 
 template <typename Q, typename C>
@@ -365,9 +373,12 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
            make_map(p.vmap, ap.c, ap.c.v, a->cache.dtype, p.box) &&
            make_query_map(p.qmap, ap, a->dtype, p.qbox);
   if (!*taken) return SV_OK;  // strides that no tensor map describes
-  p.ranges = std::min(nsm, kMaxGrid) * (pair ? 1 : 2);
-  p.mvec = ap.mask && ap.bt.T % 4 == 0 && aligned(ap.mask, 4) && ap.msb % 4 == 0;
+  // At most one range per tile that the table has room for.
   const int64_t units = static_cast<int64_t>(ap.bt.B) * ap.c.heads * w.MP;
+  const int64_t tiles = units * tc_tiles(ap.c, pair ? 128 : 64);
+  p.grid = std::min(nsm, kMaxGrid);
+  p.ranges = static_cast<int>(std::min<int64_t>(p.grid * (pair ? 1 : 2), tiles));
+  p.mvec = ap.mask && ap.bt.T % 4 == 0 && aligned(ap.mask, 4) && ap.msb % 4 == 0;
   if (a->cache.dtype == SV_E4M3) return tc_pick<BF16, E4M3>(p, pair, units, dev, stream);
   return a->dtype == SV_BF16 ? tc_pick<BF16, BF16>(p, pair, units, dev, stream)
                              : tc_pick<F16, F16>(p, pair, units, dev, stream);
