@@ -1296,14 +1296,18 @@ constexpr int kJoinThreads = 256;
 
 // Joins the partial results of a unit that range ends cut: block (x, y) looks
 // at the cut where range x + 1 begins and, if it is the unit's first, joins
-// part y of the unit's rows x D / 4 columns.  Each thread has E columns of a
-// row, so that their loads are in flight together (4 where rows are many: of
-// the 112 us that 16 trees of 64 nodes took with one column, JOIN_US), or K
-// threads share one column, each with every K-th range (few units in many parts).
-template <typename Q, typename C, int D, bool kPair, int E>
+// part y of the unit's rows x D / 4 columns.  Each thread has E = 4 columns of a
+// row, whose loads are in flight together, and the grid is a quarter of what it
+// is with one (8 chains of 6 tokens: 28 us of both kernels together, 32.5 with
+// one; 16 trees of 64 nodes: 100 and 111), and K threads share them, each with
+// every K-th range.
+constexpr int kJoinCols = 4;
+
+template <typename Q, typename C, int D, bool kPair>
 __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid_constant__ TcParams p, const int K) {
-  __shared__ float4 so[E == 1 ? kJoinThreads : 1];
-  __shared__ float sm[E == 1 ? kJoinThreads : 1], sl[E == 1 ? kJoinThreads : 1];
+  constexpr int E = kJoinCols;
+  __shared__ float4 so[E][kJoinThreads];
+  __shared__ float sm[kJoinThreads], sl[kJoinThreads];
   const AttnParams &a = p.a;
   const int i = static_cast<int>(blockIdx.x) + 1, tid = threadIdx.x;
   sv::pdl_wait();
@@ -1350,7 +1354,7 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
                          v[e].w * f + w[e].w * g);
   };
   if (in) {
-#pragma unroll(E == 1 ? 4 : 2)
+#pragma unroll 2
     for (int c = c0 + k; c <= c1; c += K) {
       const float *s = slot_of(c);
       const float m2 = __ldcg(s + D * p.slot_rows + srow), l2 = __ldcg(s + (D + 1) * p.slot_rows + srow);
@@ -1367,17 +1371,18 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
       recompute_row<Q, C, D>(a, b, tok0 + r / a.G, h * a.G + r % a.G);
     return;
   }
-  if constexpr (E == 1) {
-    if (K > 1) {
-      so[tid] = v[0];
-      sm[tid] = m;
-      sl[tid] = l;
-      __syncthreads();
-      if (k > 0) return;
-      for (int q = 1; q < K; ++q) {
-        const float4 w[1] = {so[q * per + tid]};
-        add(sm[q * per + tid], sl[q * per + tid], w);
-      }
+  if (K > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[e][tid] = v[e];
+    sm[tid] = m;
+    sl[tid] = l;
+    __syncthreads();
+    if (k > 0) return;
+    for (int q = 1; q < K; ++q) {
+      float4 w[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[e] = so[e][q * per + tid];
+      add(sm[q * per + tid], sl[q * per + tid], w);
     }
   }
   if (!in) return;

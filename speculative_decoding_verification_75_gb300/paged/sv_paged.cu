@@ -328,17 +328,15 @@ sv_status tc_launch(const TcParams &p, int64_t units, int dev, sv_stream_t strea
                                  stream, p))
     return s;
   if (p.ranges < 2) return SV_OK;  // nothing is cut
-  // Few units are cut into many parts: then more threads share an output.
+  // Few units are cut into many parts: then more threads share an output, and
+  // so do those of a block that would have none.
+  const int outputs = std::min(p.a.bt.T, p.TT * S::kTilesPerUnit) * p.a.G * (D / 4 / kJoinCols);
   int K = 1;
-  while (K < 8 && K * 4 * units <= p.ranges) K *= 2;
-  const int rows = std::min(p.a.bt.T, p.TT * S::kTilesPerUnit) * p.a.G;
-  const auto join = [&](auto *kernel, int E) {
-    const int per = kJoinThreads / K;
-    return launch(kernel, dim3(static_cast<unsigned>(p.ranges - 1), static_cast<unsigned>((rows * (D / 4 / E) + per - 1) / per)),
-                  kJoinThreads, 0, stream, p, K);
-  };
-  return K == 1 && rows >= 32 ? join(sv_attn_join_kernel<Q, C, D, kPair, 4>, 4)
-                              : join(sv_attn_join_kernel<Q, C, D, kPair, 1>, 1);
+  while (K < 8 && K * units <= p.ranges && (K * 4 * units <= p.ranges || outputs * 2 * K <= kJoinThreads)) K *= 2;
+  const int per = kJoinThreads / K;
+  return launch(sv_attn_join_kernel<Q, C, D, kPair>,
+                dim3(static_cast<unsigned>(p.ranges - 1), static_cast<unsigned>((outputs + per - 1) / per)), kJoinThreads,
+                0, stream, p, K);
 }
 
 template <typename Q, typename C>
