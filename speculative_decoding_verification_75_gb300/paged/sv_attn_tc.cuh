@@ -46,8 +46,12 @@ namespace svp {
 
 constexpr int kMaxGrid = 152;   // thread blocks, one per SM
 constexpr int kTile = 128;      // rows of a tile
+// Keys of a step, and of a stage.  A stream has two S of 64 keys, so that Q K^T
+// is a step ahead of the softmax.  (One S of 128 keys made Q K^T, softmax and
+// P V a chain that set the pace: TREE_US.)
+constexpr int kKeys = 64, kBufs = 2;
 constexpr int kScaleRing = 16;  // K tiles that are widened and not yet used, at most 7
-constexpr int kSegRing = 16;    // more segments than any role is ahead of another
+constexpr int kSegRing = 32;    // more segments than any role is ahead of another
 
 // The first segment of a range: its unit, the tile of the unit it begins at,
 // and the unit's tiles; `total` tiles of all ranges.
@@ -248,27 +252,20 @@ struct Shape {
   static constexpr int kStreams = kPair ? 1 : 2;    // ranges of a block
   static constexpr int kQTile = kTile * D * 2;
   static constexpr int kQBytes = 2 * kQTile;        // a Q tile per stream
-  // Keys of a step, and of a stage.  A pair shares 128 and has one S each; two
-  // streams have 64 and two S each, so that Q K^T is a step ahead of the softmax
-  // (with one S of 128 the chain Q K^T, softmax, P V set the pace: 413 us for
-  // 128 e4m3 requests).
-  static constexpr int kKeys = kPair ? 128 : 64;
-  static constexpr int kBufs = kPair ? 1 : 2;
   // Each range has a ring of its own, with one order of loads: a parity tells
   // two phases of a barrier apart only if no one is a whole round ahead.
-  static constexpr uint32_t kPOff = kKeys / 2;      // P in the upper half of its S
   static constexpr int kStageBytes = kKeys * D * 2;
   static constexpr int kHalf = kKeys * 128;                 // bytes of a stage's 64 columns
   static constexpr int kRawData = kKeys * D, kRawScale = kKeys * (D / SV_KV_GROUP);
   static constexpr int kRawBytes = kRawData + kRawScale;
   // Stages of a ring: as many as 227 KB hold (about 200 KB where tiles are
   // small); raw stages first, they are what is in flight.
-  static constexpr int kStages = kRaw ? 3 : D == 128 ? 5 : 11;
-  static constexpr int kRawStages = kRaw ? (D == 128 ? 3 : 10) : 0;
+  static constexpr int kStages = (kRaw ? 3 : D == 128 ? 5 : 11) * (kPair ? 2 : 1);
+  static constexpr int kRawStages = kRaw ? (D == 128 ? 3 : 10) * (kPair ? 2 : 1) : 0;
   static constexpr int kChunk = kRaw ? 32 : 64;     // S columns in registers at once
   static constexpr int kTilesPerUnit = kPair ? 2 : 1;
-  // Warps: 8 softmax, 2 producers, 2 for the products, and 8 that widen: 3 or
-  // 5 on each scheduler (4 wideners were bound by their latencies).
+  // Warps: 8 softmax, 2 producers, 2 for the products, and 8 that widen: 3 or 5
+  // on each scheduler (4 wideners were bound by their latencies).
   static constexpr int kWideners = kRaw ? 8 : 0;
   static constexpr int kWarps = 12 + kWideners;
   static constexpr int kThreads = 32 * kWarps;
@@ -278,14 +275,16 @@ struct Shape {
 
 // TMEM columns.
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream (S: + 64 * buffer)
+constexpr uint32_t kPOff = kKeys / 2;       // P in the upper half of its S
 
+template <int N, int R>
 struct RingBars {
-  uint64_t full[11], empty[11], fixed[11], rfull[10], rempty[10];
+  uint64_t full[N], empty[N], fixed[N], rfull[R], rempty[R];
 };
 // One barrier of s_full, p_ready and o_done per S buffer: of the tile two before,
 // all three are done when a tile's S is, and none of the tile two behind can be.
 struct Bars {
-  uint64_t s_full[2][2], p_half[2], p_ready[2][2], o_done[2][2], q_full[2], q_ready[2], q_empty[2], drain[2];
+  uint64_t s_full[2][2], p_ready[2][2], o_done[2][2], q_full[2], q_ready[2], q_empty[2], drain[2];
 };
 
 // ----------------------------------------------------------------- work ----
@@ -296,7 +295,6 @@ struct Req {
 
 // Tiles of a request: its units (KV head, group of row tiles) times its key
 // tiles.  upt: new tokens of a unit.
-template <int kKeys>
 __device__ __forceinline__ Req request(const AttnParams &p, int upt, int b, uint32_t &st) {
   Req r;
   lengths(p.bt, b, r.L, r.n, st);
@@ -307,9 +305,8 @@ __device__ __forceinline__ Req request(const AttnParams &p, int upt, int b, uint
   return r;
 }
 
-template <int kKeys>
 __device__ __forceinline__ int weight_of(const AttnParams &p, int upt, int b, uint32_t &st) {
-  return b < p.bt.B ? request<kKeys>(p, upt, b, st).weight : 0;
+  return b < p.bt.B ? request(p, upt, b, st).weight : 0;
 }
 
 // Range i of N <= total over `total` tiles is [start(i), start(i + 1)): none is
@@ -341,7 +338,6 @@ struct Walk {
 
 // To the next segment.  Not inlined: every role of the kernel walks, and the
 // copies together would crowd the instruction cache.
-template <int kKeys>
 __device__ __noinline__ void next_segment(const AttnParams &p, int upt, Walk &w) {
   Walk v = w;
   v.on = v.left > 0;
@@ -350,7 +346,7 @@ __device__ __noinline__ void next_segment(const AttnParams &p, int upt, Walk &w)
       v.unit = 0;
       uint32_t st = 0;
       do {
-        v.r = request<kKeys>(p, upt, ++v.b, st);
+        v.r = request(p, upt, ++v.b, st);
       } while (v.r.weight == 0);
     }
     v.t0 = 0;                                // a later segment begins a unit
@@ -377,28 +373,26 @@ __device__ __forceinline__ Tile tile_of(const Walk &w) {
   return Tile{w.t0, w.t0, w.t1, w.b, w.h, w.mp, w.seg, w.r.kv_end, w.new0(), w.on, w.r.kv_end < w.r.L + w.r.n};
 }
 
-template <int kKeys>
 __device__ __forceinline__ void next_tile(const AttnParams &p, int upt, Walk &w, Tile &x) {
   if (++x.t < x.t1) return;
-  next_segment<kKeys>(p, upt, w);
+  next_segment(p, upt, w);
   x = tile_of(w);
 }
 
 // Tiles of a range whose walk begins.  They are loaded, widened and multiplied
-// in one order, at positions 0 .. 2n - 1: K0 V0 K1 V1 .. with one S (kPair),
-// K0 K1 V0 K2 V1 .. with two, K a tile ahead.
+// in one order, K a tile ahead: K0 K1 V0 K2 V1 .. at positions 0 .. 2n - 1.  Even
+// positions are K0 V0 V1 .., odd ones K1 K2 .. and the last V.
 __device__ __forceinline__ int count_of(const Walk &w) { return w.on ? w.left + w.t1 - w.t0 : 0; }
 
 // Range i's first tile, by a whole warp: the requests are spread over the
 // lanes, 32 at a time.
-template <int kKeys>
 __device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, int limit, Walk &w, int &total) {
   const int lane = threadIdx.x & 31, B = p.bt.B;
   uint32_t st = 0;
-  const int mine = weight_of<kKeys>(p, upt, lane, st);  // requests 0 .. 31
+  const int mine = weight_of(p, upt, lane, st);  // requests 0 .. 31
   total = mine;
 #pragma unroll 1
-  for (int b = lane + 32; b < B; b += 32) total += weight_of<kKeys>(p, upt, b, st);
+  for (int b = lane + 32; b < B; b += 32) total += weight_of(p, upt, b, st);
   total = __reduce_add_sync(kFull, total);
   if (i == 0) report(p.bt.status, st);
   const int N = min(limit, total);
@@ -414,7 +408,7 @@ __device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, 
     if (begin < base + sum) break;               // begin < total: it ends
     base += sum;
     c += 32;
-    x = weight_of<kKeys>(p, upt, c + lane, st);
+    x = weight_of(p, upt, c + lane, st);
   }
   int incl = x;
 #pragma unroll
@@ -426,7 +420,7 @@ __device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, 
   const int src = __ffs(__ballot_sync(kFull, begin >= excl && begin < excl + x)) - 1;
   const int rem = begin - __shfl_sync(kFull, excl, src);
   w.b = c + src;
-  w.r = request<kKeys>(p, upt, w.b, st);
+  w.r = request(p, upt, w.b, st);
   w.unit = rem / w.r.kt;
   w.t0 = rem - w.unit * w.r.kt;
   w.t1 = min(w.r.kt, w.t0 + w.left);
@@ -464,7 +458,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   using S = Shape<Q, C, D, kPair>;
   extern __shared__ __align__(1024) uint8_t smem[];   // swizzle atoms: 1024 bytes
   __shared__ Bars bars;
-  __shared__ RingBars rings[S::kStreams];
+  using Ring = RingBars<S::kStages, S::kRaw ? S::kRawStages : 1>;
+  __shared__ Ring rings[S::kStreams];
   __shared__ uint32_t tmem_slot;
   __shared__ Walk sh_walk[S::kStreams];
   __shared__ int seg_bad[S::kStreams][kSegRing];  // holds 1 + a marked segment's number
@@ -494,12 +489,11 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       }
     }
     for (int s = 0; s < 2; ++s) {
-      for (int i = 0; i < S::kBufs; ++i) {
+      for (int i = 0; i < kBufs; ++i) {
         sv::mbar_init(sv::smem_addr(&bars.s_full[s][i]), 1);
         sv::mbar_init(sv::smem_addr(&bars.o_done[s][i]), 1);
         sv::mbar_init(sv::smem_addr(&bars.p_ready[s][i]), 4);
       }
-      sv::mbar_init(sv::smem_addr(&bars.p_half[s]), 4);
       sv::mbar_init(sv::smem_addr(&bars.q_full[s]), 1);
       sv::mbar_init(sv::smem_addr(&bars.q_ready[s]), 4);
       sv::mbar_init(sv::smem_addr(&bars.q_empty[s]), 1);
@@ -536,7 +530,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const int i = static_cast<int>(blockIdx.x + (warp - 8) * gridDim.x);
     Walk w;
     int total;
-    begin_walk<S::kKeys>(a, upt, i, p.ranges, w, total);
+    begin_walk(a, upt, i, p.ranges, w, total);
     if (lane == 0) {
       sh_walk[warp - 8] = w;
       // Range 0 is written even if there are no tiles: its total says so.
@@ -608,33 +602,24 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
 #pragma unroll 1
       for (int j = 0; j < nt; ++j, ++tiles) {
         // Which of the tile's keys the row sees, while S is being computed.
-        const int k0 = (sg.t0 + j) * S::kKeys;
-        const uint32_t buf = tiles % S::kBufs, round = tiles / S::kBufs;
+        const int k0 = (sg.t0 + j) * kKeys;
+        const uint32_t buf = tiles % kBufs, round = tiles / kBufs;
         const uint32_t col_s = col_s0 + 64u * buf;
-        const bool masked = k0 + S::kKeys > full_end;
-        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};        // kKeys / 32 of them are used
+        const bool masked = k0 + kKeys > full_end;
+        uint32_t vis[2] = {~0u, ~0u};
         if (masked && active) {
           const int lim = min(r.kv_end, mrow ? r.L : r.L + t_row + 1) - k0;
 #pragma unroll
-          for (int w = 0; w < S::kKeys / 32; ++w) {
+          for (int w = 0; w < 2; ++w) {
             const int n = min(max(lim - 32 * w, 0), 32);
             vis[w] = n == 32 ? ~0u : (1u << n) - 1u;
           }
           if (mrow) {
             // The row's bytes for new tokens [o0, o1), four at a time where
             // rows are whole words; bit c of the tile is new token k0 + c - L.
-            const int o0 = max(k0 - r.L, 0), o1 = min(min(r.kv_end, k0 + S::kKeys) - r.L, r.n);
-            uint64_t lo = 0, hi = 0;
-            const auto put = [&](uint64_t bits, int c) {
-              if (c < 0) {
-                lo |= bits >> -c;
-              } else if (c < 64) {
-                lo |= bits << c;
-                if (c > 60) hi |= bits >> (64 - c);
-              } else {
-                hi |= bits << (c - 64);
-              }
-            };
+            const int o0 = max(k0 - r.L, 0), o1 = min(min(r.kv_end, k0 + kKeys) - r.L, r.n);
+            uint64_t lo = 0;
+            const auto put = [&](uint64_t bits, int c) { lo |= c < 0 ? bits >> -c : bits << c; };
             if (p.mvec) {
 #pragma unroll 4
               for (int o = o0 & ~3; o < o1; o += 4) {
@@ -650,10 +635,6 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             }
             vis[0] |= static_cast<uint32_t>(lo);
             vis[1] |= static_cast<uint32_t>(lo >> 32);
-            if (S::kKeys == 128) {
-              vis[2] |= static_cast<uint32_t>(hi);
-              vis[3] |= static_cast<uint32_t>(hi >> 32);
-            }
           }
         }
         if (!(ok = wait_warp(&bars.s_full[s][buf], round, err))) break;
@@ -662,8 +643,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           tc_fence_after();
           if (masked) {  // scores that the row does not see become -inf, in place
 #pragma unroll 1
-            for (int w = 0; w < S::kKeys / 32; ++w) {
-              const uint32_t bits = w == 0 ? vis[0] : w == 1 ? vis[1] : w == 2 ? vis[2] : vis[3];
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t bits = w == 0 ? vis[0] : vis[1];
               if (__all_sync(kFull, bits == ~0u)) continue;
               uint32_t y[32];
               tc_ld32(col_s + 32u * w, y);
@@ -685,7 +666,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             tc_wait_ld(x);
           };
           // (kRaw: loops over chunks, for the instruction cache's sake.)
-          constexpr int kChunks = S::kKeys / W, kUnroll = S::kRaw ? 1 : kChunks;
+          constexpr int kChunks = kKeys / W, kUnroll = S::kRaw ? 1 : kChunks;
           float mt = -INFINITY, cf = c_row;
           if constexpr (S::kRaw) cf = fmaxf(c_row * scale_value(k_scale[rs][tiles % kScaleRing]), 1.2e-38f);
 #pragma unroll kUnroll
@@ -713,8 +694,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             }
             __syncwarp();
             if (j > 0) {
-              // (kBufs == 2: the products of the tile before may still run.)
-              if (!(ok = wait_warp(&bars.o_done[s][(tiles - 1) % S::kBufs], (tiles - 1) / S::kBufs, err))) break;
+              // The products of the tile before may still run.
+              if (!(ok = wait_warp(&bars.o_done[s][(tiles - 1) % kBufs], (tiles - 1) / kBufs, err))) break;
               tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
@@ -747,15 +728,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
               else l2b = f2_add(l2b, f2_pack(y0, y1));
               pk[k >> 1] = pack2<typename S::M>(y0, y1);
             }
-            if constexpr (W == 64) tc_st32(col_s + S::kPOff + ch * (W / 2), pk);
-            else tc_st16(col_s + S::kPOff + ch * (W / 2), pk);
-            if (S::kKeys == 128 && ch * W == 64) {  // the upper half of P is complete: its products may start
-              tc_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) sv::mbar_arrive(sv::smem_addr(&bars.p_half[s]));
-              __syncwarp();
-            }
+            if constexpr (W == 64) tc_st32(col_s + kPOff + ch * (W / 2), pk);
+            else tc_st16(col_s + kPOff + ch * (W / 2), pk);
           }
           float e0, e1, e2, e3;
           f2_unpack(l2a, e0, e1);
@@ -763,16 +737,14 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           l += (e0 + e1) + (e2 + e3);
           tc_wait_st();
           tc_fence_before();
-        } else if (S::kKeys == 128 && lane == 0) {
-          sv::mbar_arrive(sv::smem_addr(&bars.p_half[s]));
         }
         __syncwarp();
         if (lane == 0) sv::mbar_arrive(sv::smem_addr(&bars.p_ready[s][buf]));
       }
       if (!ok) break;
-      next_segment<S::kKeys>(a, upt, walk);
+      next_segment(a, upt, walk);
       if (S::kRaw && walk.on && !(ok = prepare_q(walk))) break;   // while the last products run
-      if (!(ok = wait_warp(&bars.o_done[s][(tiles - 1) % S::kBufs], (tiles - 1) / S::kBufs, err))) break;
+      if (!(ok = wait_warp(&bars.o_done[s][(tiles - 1) % kBufs], (tiles - 1) / kBufs, err))) break;
       tc_fence_after();
       const float vs = S::kRaw ? scale_value(v_scale[rs][seg % kSegRing] & 255) : 1.f;
       const bool bad = seg_bad[rs][seg % kSegRing] == seg + 1;
@@ -837,26 +809,28 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     }
   } else if (warp < 10) {
     // -------------------------------------------------------- producers ----
-    // One warp per stream, or (kPair) one for K and one for V.  Lane i looks
-    // up box i of a tile, an elected lane issues the copies (~90 cycles each).
-    const int s = warp - 8, rs = kPair ? 0 : s;
-    const int box = p.box, nb = S::kKeys / box;               // boxes of a stage, at most 16
+    // One warp per ring (two were no faster: 122 us for 32 x 32 heads that share
+    // nothing, 115 with one), or (kPair) one for its even and one for its odd
+    // positions.  Lane i looks up box i of a tile, an elected lane issues the
+    // copies (~90 cycles each).
+    const int rs = kPair ? 0 : warp - 8, grp = kPair ? warp - 8 : 0;
+    const int box = p.box, nb = kKeys / box;               // boxes of a stage, at most 8
     constexpr int kRing = S::kRaw ? S::kRawStages : S::kStages;
     uint64_t *const fullb = S::kRaw ? rings[rs].rfull : rings[rs].full;
     uint64_t *const emptyb = S::kRaw ? rings[rs].rempty : rings[rs].empty;
     const uint32_t stage0 = S::kRaw ? sv::smem_addr(raw0) + rs * (S::kRawStages * S::kRawBytes)
                                     : sv::smem_addr(ring0) + rs * (S::kStages * S::kStageBytes);
     constexpr int kRingBytes = S::kRaw ? S::kRawBytes : S::kStageBytes;
-    int issued = -1, q_issued = 0;                      // last position, Q loads
+    int issued = -1, q_last = -1;                       // last position, last segment's Q
     // This lane's box of a tile: its block and the row in it (-1: no box).
     struct Box {
       int id, row, h;
     };
     const int32_t *table = nullptr;          // the segment's
     int block = 0, row = 0;                  // of the lane's box in the tile
-    const int step_block = S::kKeys / a.c.bs, step_row = S::kKeys - step_block * a.c.bs;
+    const int step_block = kKeys / a.c.bs, step_row = kKeys - step_block * a.c.bs;
     const auto fetch = [&](const Tile &w) {
-      const int pos = w.t * S::kKeys + lane * box;
+      const int pos = w.t * kKeys + lane * box;
       if (w.first()) {
         table = a.c.tables + static_cast<size_t>(w.b) * a.c.max_blocks;
         block = pos / a.c.bs;
@@ -886,7 +860,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       }
     };
     // A tile's K or V into the next stage.
-    int st = kPair ? s : 0, round = 0;       // of the next position
+    int st = grp, round = 0;                 // of the next position
     const uint32_t sblock = static_cast<uint32_t>(a.c.sblock_bytes);   // < 2^31
     const auto load = [&](const Box &x, bool is_v) {
       const CUtensorMap *map = is_v ? &p.vmap : &p.kmap;
@@ -945,54 +919,62 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
                    hf * 64, w.h * a.G, w.mp * upt + i * p.TT, w.b, bar);
       }
       __syncwarp();
-      ++q_issued;
+      q_last = w.seg;
       return true;
     };
     Walk walk = sh_walk[rs];
     Tile w = tile_of(walk);
-    Box x = fetch(w);                        // of the next K
+    Box x = fetch(w);                        // of the next tile
+    const int n = count_of(walk);
     if constexpr (kPair) {
+      if (grp && n > 1) {
+        next_tile(a, upt, walk, w);
+        x = fetch(w);
+      }
 #pragma unroll 1
-      while (ok && w.on) {
+      for (int i = 0; ok && i < n; ++i) {
+        const bool is_v = grp ? i == n - 1 : i > 0;
         const Tile at = w;
         Box now = x;
         settle(now, w);
-        next_tile<S::kKeys>(a, upt, walk, w);
-        x = fetch(w);                        // on its way while the stage is waited for
-        ok = load(now, s == 1);
-        if (ok && at.first() && s == 0) ok = load_q(at);
+        if (grp ? i + 2 < n : i > 0) {
+          next_tile(a, upt, walk, w);
+          x = fetch(w);                      // on its way while the stage is waited for
+        }
+        ok = load(now, is_v);
+        if (ok && !is_v && at.first()) ok = load_q(at);
       }
     } else {
-      const int n2 = 2 * count_of(walk);
       Box b0 = x, b1 = x;                    // of the two tiles before
 #pragma unroll 1
-      for (int pos = 0; ok && pos < n2; ++pos) {
-        if ((pos & 1 || pos == 0) && pos + 1 < n2) {
+      for (int pos = 0; ok && pos < 2 * n; ++pos) {
+        const bool tail = pos + 1 == 2 * n;  // the last V
+        if ((pos & 1 || pos == 0) && !tail) {
           b0 = b1;
           settle(x, w);
           b1 = x;
           ok = load(x, false);
           if (ok && w.first()) ok = load_q(w);
-          next_tile<S::kKeys>(a, upt, walk, w);
+          next_tile(a, upt, walk, w);
           x = fetch(w);                      // on its way while a V is loaded
         } else {
-          ok = load(pos + 1 < n2 ? b0 : b1, true);
+          ok = load(tail ? b1 : b0, true);
         }
       }
     }
     if (!ok) {  // copies in flight land before the block ends (a position not issued: the wait gives up)
 #pragma unroll 1
       for (int k = max(0, issued - kRing + 1); k <= issued; ++k) wait_warp(&fullb[k % kRing], k / kRing, err);
-      if (q_issued > 0) wait_warp(&bars.q_full[rs], q_issued - 1, err);
+      if (q_last >= 0) wait_warp(&bars.q_full[rs], q_last, err);
     }
   } else if (warp < 12) {
     // -------------------------------------------------------- products ----
     // One warp per stream issues its Q K^T and P V, in order.
     const int s = warp - 10, rs = kPair ? 0 : s;
-    const uint32_t kQK = mma_desc<typename S::M>(S::kKeys, false) | (p.negate ? kNegateA : 0u);
+    const uint32_t kQK = mma_desc<typename S::M>(kKeys, false) | (p.negate ? kNegateA : 0u);
     constexpr uint32_t kPV = mma_desc<typename S::M>(D, true);
     uint8_t *const ring = ring0 + rs * (S::kStages * S::kStageBytes);
-    RingBars &rb = rings[rs];
+    Ring &rb = rings[rs];
     const uint64_t q_desc = smem_desc(sv::smem_addr(sq) + s * S::kQTile, 16);
     const uint64_t k_desc = smem_desc(sv::smem_addr(ring), 16);
     const uint64_t v_desc = smem_desc(sv::smem_addr(ring), S::kHalf);
@@ -1013,7 +995,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       constexpr int kCh = S::kHalves * 8;
       bool found = false;
 #pragma unroll 2
-      for (int i = lane + r0 * kCh; i < S::kKeys * kCh; i += 32) {
+      for (int i = lane + r0 * kCh; i < kKeys * kCh; i += 32) {
         const int row = i / kCh, ch = i % kCh;
         uint4 *v = reinterpret_cast<uint4 *>(base + (ch >> 3) * S::kHalf + row * 128 + (ch & 7) * 16);
         if (row >= r1) {
@@ -1032,7 +1014,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       if (w.first() && !wait_warp(S::kRaw ? &bars.q_ready[s] : &bars.q_full[rs], w.seg, err)) return false;
       if (!take(pos)) return false;
       const uint64_t kd = k_desc + (pos % S::kStages) * (S::kStageBytes >> 4);
-      const uint32_t buf = nk % S::kBufs;
+      const uint32_t buf = nk % kBufs;
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
@@ -1046,11 +1028,11 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       ++nk;
       return true;
     };
-    // O += P V; of 128 keys the upper half first: its P is ready first.
+    // O += P V.
     const auto pv = [&](const Tile &w, int pos) {
-      const int st = pos % S::kStages, k0 = w.t * S::kKeys;
+      const int st = pos % S::kStages, k0 = w.t * kKeys;
       if (!take(pos)) return false;
-      if (!S::kRaw && k0 + S::kKeys > w.new0) {
+      if (!S::kRaw && k0 + kKeys > w.new0) {
         if (!kPair || s == 0) {
           repair(w, k0, st);
           if (kPair && lane == 0) sv::mbar_arrive(sv::smem_addr(&rb.fixed[st]));
@@ -1059,25 +1041,19 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           fix ^= 1u << st;
         }
       }
-      const uint32_t buf = nv % S::kBufs;
-#pragma unroll 1
-      for (int half = S::kKeys / 64 - 1; half >= 0; --half) {
-        if (!wait_warp(half ? &bars.p_half[s] : &bars.p_ready[s][buf], half ? nv : nv / S::kBufs, err)) return false;
-        tc_fence_after();
-        const uint64_t vd = v_desc + st * (S::kStageBytes >> 4) + half * (64 * 128 >> 4);
-        const uint32_t first = w.first() && half == S::kKeys / 64 - 1;
-        if (elect_one()) {
+      const uint32_t buf = nv % kBufs;
+      if (!wait_warp(&bars.p_ready[s][buf], nv / kBufs, err)) return false;
+      tc_fence_after();
+      const uint64_t vd = v_desc + st * (S::kStageBytes >> 4);
+      const uint32_t first = w.first();
+      if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_ts(to, ts + 64u * buf + S::kPOff + 32u * half + 8u * k, vd + k * (2048 >> 4), kPV,
-                      !(first && k == 0));
-          if (half == 0) {
-            tc_commit(sv::smem_addr(&rb.empty[st]));
-            tc_commit(sv::smem_addr(&bars.o_done[s][buf]));
-          }
-        }
-        __syncwarp();
+        for (int k = 0; k < 4; ++k)
+          tc_mma_ts(to, ts + 64u * buf + kPOff + 8u * k, vd + k * (2048 >> 4), kPV, !(first && k == 0));
+        tc_commit(sv::smem_addr(&rb.empty[st]));
+        tc_commit(sv::smem_addr(&bars.o_done[s][buf]));
       }
+      __syncwarp();
       ++nv;
       return true;
     };
@@ -1085,12 +1061,11 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     Tile w = tile_of(walk), behind = w;
     const int n = count_of(walk);
 #pragma unroll 1
-    for (int i = 0, pos = 0; ok && i < n + S::kBufs - 1; ++i) {
+    for (int i = 0, pos = 0; ok && i <= n && n > 0; ++i) {
       if (i < n) ok = qk(w, pos++);
-      if (kPair) behind = w;
-      if (ok && (kPair || i > 0)) ok = pv(behind, pos++);
+      if (ok && i > 0) ok = pv(behind, pos++);
       behind = w;
-      if (i < n) next_tile<S::kKeys>(a, upt, walk, w);
+      if (i < n) next_tile(a, upt, walk, w);
     }
     if (!ok) {  // issued products end before TMEM is freed
       if (elect_one()) tc_commit(sv::smem_addr(&bars.drain[s]));
@@ -1113,7 +1088,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // more is recomputed.  Groups at the smallest scale (2^-120, which the cache
     // writes for zeros) do not count and become 0 in V and beside larger ones.
     //
-    // The wideners of a ring are two groups, for its even and its odd positions:
+    // The wideners of a ring are two groups, of its even and its odd positions:
     // what a stage costs besides its conversions (two waits, the scales, a
     // fence) is latency, and two stages at a time hide each other's.  A group
     // waits for a stage to be empty before it waits for the raw one: by then the
@@ -1124,15 +1099,15 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     constexpr int kGW = S::kRaw ? S::kRingWideners / 2 : 1, kRS = S::kRaw ? S::kRawStages : 1;
     const int rs = kPair ? 0 : (warp - 12) / (2 * kGW), grp = warp & 1;
     const int ht = ((warp - 12 - rs * 2 * kGW) >> 1) * 32 + lane;
-    RingBars &rb = rings[rs];
+    Ring &rb = rings[rs];
     uint8_t *const ring = ring0 + rs * (S::kStages * S::kStageBytes);
     uint8_t *const raw = raw0 + rs * (S::kRawStages * S::kRawBytes);
     int v_ref = 0;
     // This thread's chunks: 16 codes (column group ch) of every kRowStep-th row.
     // Eight lanes write 4 chunks of one row and 4 of the next, whose swizzles
     // differ in the lowest bit: eight different 16-byte columns of the banks.
-    constexpr int kCh = D / 16, kRowStep = kGW * 32 / kCh, kRows = S::kKeys / kRowStep, kTurn = 4;
-    static_assert((kRowStep % 8 == 0 && kRows % kTurn == 0) || !S::kRaw, "one swizzle per thread, whole turns");
+    constexpr int kCh = D / 16, kRowStep = kGW * 32 / kCh, kRows = kKeys / kRowStep, kTurn = kRows < 4 ? kRows : 4;
+    static_assert(kRowStep % 8 == 0 || !S::kRaw, "one swizzle per thread");
     const int ch = (ht & 3) + (kCh == 8 ? (ht >> 3 & 1) * 4 : 0);
     const int row0 = (kCh == 8 ? ht >> 4 : ht >> 3) * 2 + (ht >> 2 & 1);
     const int from = row0 * D + ch * 16;
@@ -1141,19 +1116,19 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // A tile's K (the range's k-th) or V, at the group's next position.
     int st = grp, round = 0, rst = grp, rround = 0;
     const auto widen = [&](const Tile &w, bool is_v, int k) {
-      const int k0 = w.t * S::kKeys;
+      const int k0 = w.t * kKeys;
       if (round > 0 && !wait_warp(&rb.empty[st], round - 1, err)) return false;
       if (!wait_warp(&rb.rfull[rst], rround, err)) return false;
       const uint8_t *src = raw + rst * S::kRawBytes;
       const uint8_t *sc = src + S::kRawData;
       uint8_t *dst = ring + st * S::kStageBytes;
       constexpr int kSc = D / SV_KV_GROUP;            // scale bytes of a row
-      const int live = min(w.kv_end - k0, S::kKeys);  // rows that hold tokens
+      const int live = min(w.kv_end - k0, kKeys);  // rows that hold tokens
       int *const vs = &v_scale[rs][w.seg % kSegRing];
       if (is_v) {
         if (w.first()) {
           v_ref = 0;
-        } else if (!kPair && grp) {                   // a range's last V: the other group had the one before
+        } else if (grp) {                             // a range's last V: the other group had the one before
           const int pos = round * S::kStages + st - 1;
           if (!wait_warp(&rb.full[pos % S::kStages], pos / S::kStages, err)) return false;
           const int x = *vs;
@@ -1165,10 +1140,10 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         // The stage's largest scale, over the rows that hold tokens: each warp
         // reads them all.
         int hi = 0;
-        if (live == S::kKeys) {
+        if (live == kKeys) {
           uint32_t m = 0;
 #pragma unroll
-          for (int k = 0; k < S::kKeys * kSc / 128; ++k) {
+          for (int k = 0; k < kKeys * kSc / 128; ++k) {
             const uint32_t u = *reinterpret_cast<const uint32_t *>(sc + (k * 32 + lane) * 4);
             m = __vmaxu2(m, __vmaxu2(u & 0x00ff00ffu, (u >> 8) & 0x00ff00ffu));
           }
@@ -1238,7 +1213,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           *reinterpret_cast<uint4 *>(to + to_hi) = make_uint4(o[4], o[5], o[6], o[7]);
         }
       }
-      if (is_v && k0 + S::kKeys > w.new0) {  // the last tiles of a unit: the thread's own rows once more
+      if (is_v && k0 + kKeys > w.new0) {  // the last tiles of a unit: the thread's own rows once more
         const int r0 = max(w.new0 - k0, 0), r1 = w.kv_end - k0;
 #pragma unroll 1
         for (int t = 0; t < 2 * kRows; ++t) {
@@ -1272,15 +1247,12 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     Walk walk = sh_walk[rs];
     Tile w = tile_of(walk);
     const int n = count_of(walk);
-    // kPair: one group has K, the other V.  Else group 0 has K0 V0 V1 .., group
-    // 1 K1 K2 .. and the last V.
-    bool step = !kPair && grp && n > 1;      // to the next tile
+    bool step = grp && n > 1;                // to the next tile
 #pragma unroll 1
     for (int i = 0; ok && i < n; ++i) {
-      if (step) next_tile<S::kKeys>(a, upt, walk, w);
-      const bool is_v = kPair ? grp : grp ? i == n - 1 : i > 0;
-      ok = widen(w, is_v, kPair || !grp ? i : i + 1);
-      step = kPair || (grp ? i + 2 < n : i > 0);
+      if (step) next_tile(a, upt, walk, w);
+      ok = widen(w, grp ? i == n - 1 : i > 0, i + grp);
+      step = grp ? i + 2 < n : i > 0;
     }
   }
 

@@ -294,8 +294,8 @@ TcLayout tc_layout(int64_t T, int64_t G, int64_t D) {
 }
 
 // Key tiles of a request whose table is full.
-int64_t tc_tiles(const Cache &c, int keys) {
-  return std::max<int64_t>((static_cast<int64_t>(c.max_blocks) * c.bs + keys - 1) / keys, 1);
+int64_t tc_tiles(const Cache &c) {
+  return std::max<int64_t>((static_cast<int64_t>(c.max_blocks) * c.bs + kKeys - 1) / kKeys, 1);
 }
 
 // What the tensor-core kernel takes: whole 8-row swizzle atoms per page,
@@ -310,7 +310,7 @@ bool tc_takes(const sv_tree_attention_args *a, const AttnParams &p, const TcLayo
       static_cast<int64_t>(p.c.heads) * p.c.bs * (p.c.D / SV_KV_GROUP) > INT_MAX)
     return false;
   const int64_t units = static_cast<int64_t>(p.bt.B) * p.c.heads * w.MP;
-  return units <= INT_MAX / tc_tiles(p.c, 64);
+  return units <= INT_MAX / tc_tiles(p.c);
 }
 
 template <typename Q, typename C, int D, bool kPair>
@@ -362,7 +362,7 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
   p.slot_floats = w.slot_floats;
   const bool pair = ap.bt.T > w.TT;
   p.box = 8;  // a power of two that divides the block size, at most a stage
-  while (p.box < (pair ? 128 : 64) && ap.c.bs % (2 * p.box) == 0) p.box *= 2;
+  while (p.box < kKeys && ap.c.bs % (2 * p.box) == 0) p.box *= 2;
   p.c = std::max(std::fabs(ap.scale_log2), 1.2e-38f);  // not 0: -inf times it stays -inf
   p.negate = ap.scale_log2 < 0.f;
   p.TT = w.TT;
@@ -373,7 +373,7 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
   if (!*taken) return SV_OK;  // strides that no tensor map describes
   // At most one range per tile that the table has room for.
   const int64_t units = static_cast<int64_t>(ap.bt.B) * ap.c.heads * w.MP;
-  const int64_t tiles = units * tc_tiles(ap.c, pair ? 128 : 64);
+  const int64_t tiles = units * tc_tiles(ap.c);
   p.grid = std::min(nsm, kMaxGrid);
   p.ranges = static_cast<int>(std::min<int64_t>(p.grid * (pair ? 1 : 2), tiles));
   p.mvec = ap.mask && ap.bt.T % 4 == 0 && aligned(ap.mask, 4) && ap.msb % 4 == 0;
