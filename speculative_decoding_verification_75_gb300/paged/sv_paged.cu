@@ -187,7 +187,12 @@ sv_status kv_compact(const sv_kv_compact_args *a, sv_stream_t stream) {
   p.esz = elem_bytes(a->cache.dtype);
   p.status = a->status;
   const int64_t units = 2ll * p.c.heads * (p.c.D * p.esz / 16 + (p.esz == 1 ? p.c.D / SV_KV_GROUP : 0));
-  const int64_t blocks = a->B * p.c.num_layers, gy = (units + kMoveThreads - 1) / kMoveThreads;
+  // As many layers to a block as make all blocks run at once, four to an SM.
+  const int64_t gy = (units + kMoveThreads - 1) / kMoveThreads;
+  p.layers = static_cast<int>(std::max<int64_t>(
+      std::min<int64_t>((a->B * p.c.num_layers * gy + 4 * kMaxGrid - 1) / (4 * kMaxGrid), p.c.num_layers), 1));
+  p.groups = (p.c.num_layers + p.layers - 1) / p.layers;
+  const int64_t blocks = a->B * p.groups;
   if (blocks > INT_MAX || gy > 65535) return SV_ERR_INVALID_ARG;
   return launch(sv_kv_compact_kernel,
                 dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(gy)), kMoveThreads, 0,

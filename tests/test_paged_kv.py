@@ -429,7 +429,9 @@ def compact_reference(arrays, tables, bs, path, k, L):
 @gpu
 @pytest.mark.parametrize("layers,B,H,D,bs,P,cdt", [
     (None, 1, 2, 64, 16, 1, "bf16"), (1, 3, 8, 128, 16, 6, "bf16"), (3, 4, 8, 128, 16, 9, "e4m3"),
-    (2, 5, 1, 32, 5, 7, "e4m3"), (2, 2, 33, 256, 1, 20, "fp16"), (1, 2, 3, 8, 64, 150, "bf16")])
+    (2, 5, 1, 32, 5, 7, "e4m3"), (2, 2, 33, 256, 1, 20, "fp16"), (1, 2, 3, 8, 64, 150, "bf16"),
+    # More layers than run at once: several to a thread block, one left over.
+    (21, 40, 2, 32, 8, 5, "e4m3"), (71, 10, 1, 8, 4, 70, "bf16")])
 def test_compact(layers, B, H, D, bs, P, cdt):
     sv, _, _ = _pkg()
     rng = np.random.default_rng(P)
