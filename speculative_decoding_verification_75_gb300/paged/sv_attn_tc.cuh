@@ -23,9 +23,10 @@
 // host never waits.
 //
 // Softmax.  One pass: a row keeps a reference m and sums 2^(x - m) in fp32.
-// O is rescaled only when a tile's maximum exceeds m by more than 2^8 (bf16
-// and fp16 hold 2^8 as exactly as 1, fp32 sums lose nothing), which after
-// the first tiles is rare.
+// O is rescaled only when a tile's maximum exceeds the one that set m by more
+// than 2^8 (bf16 and fp16 hold 2^8 as exactly as 1, fp32 sums lose nothing),
+// which after the first tiles is rare.  fp16 probabilities begin at 2^7, so that
+// small ones keep their bits: what is lost is 2^-32 of the largest, at most.
 //
 // Data.  TMA boxes of one page's rows (a power of two of them that divides the
 // block size) fill 128-byte swizzled tiles through an mbarrier ring; e4m3 tiles
@@ -684,10 +685,12 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           }
           // Raise the reference where the tile's maximum is more than 2^8
           // above it (or nothing was seen before).
-          const bool up = mt > m_ref && !(mt - m_ref <= 8.f);
+          constexpr float kHead = S::M::kIsBf16 ? 0.f : 7.f;   // 2^(7 + 8) is below fp16's largest
+          const bool up = mt - kHead > m_ref && !(mt - m_ref <= kHead + 8.f);
           if (__any_sync(kFull, up)) {
             float f = 1.f;
             if (up) {
+              mt -= kHead;
               f = sv::ex2(m_ref - mt);
               m_ref = mc = mt;
               l *= f;

@@ -64,6 +64,7 @@ class Cache:
     """A cache's values in float64 and its look-up."""
 
     def __init__(self, k, v, tables, ks=None, vs=None):
+        self.e4m3 = ks is not None
         self.k, self.v = self._vals(k, ks), self._vals(v, vs)
         self.tables = tables.cpu().numpy()
         self.bs = k.shape[-2]
@@ -100,7 +101,10 @@ def attention(q, cache, seq_lens, new_lens, mask, scale, unit):
                   factor of exp(ds); 2^-20 more for exp2 itself;
       rounding p  unit * sum_j p_j |v_j|; for fp16 also 2^-25 absolute per
                   probability below its normal range, relative to the largest
-                  probability, which is at least 1 before normalising;
+                  probability, which is at least 1 before normalising; over an
+                  e4m3 cache probabilities are fp16 too, the largest at least
+                  2^7 before normalising: half a subnormal step, 2^-25, is
+                  2^-32 of it (bf16 has no such term, its range is fp32's);
       sums        (number of keys + 8) 2^-24 relative to sum_j p_j |v_j|, for
                   numerator and denominator;
       result      unit * |out|.
@@ -157,6 +161,8 @@ def attention(q, cache, seq_lens, new_lens, mask, scale, unit):
                 S = len(s)
                 rel = 2 * ds.max() + 2.0 ** -19 + 2 * (S + 8) * 2.0 ** -24
                 t = (unit + rel) * a + unit * np.abs(o)
+                if cache.e4m3:
+                    t = t + S * 2.0 ** -32 * np.abs(v).max(0) / l
                 if unit < 2.0 ** -10:
                     t = t + S * 2.0 ** -25 * np.abs(v).max(0) / l + 2.0 ** -25
                 tol[b, i, h] = t * 1.01 + 1e-37

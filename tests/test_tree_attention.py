@@ -146,6 +146,35 @@ def test_scales_of_an_e4m3_cache_that_differ_widely():
                 check(s)
 
 
+@pytest.mark.parametrize("D,T,bs,H", [(128, 3, 16, 24), (64, 2, 32, 32), (128, 40, 64, 12), (64, 70, 16, 12)])
+def test_values_of_an_e4m3_cache_that_begin_with_zeros(D, T, bs, H):
+    """Sequences whose first tokens' values are zeros at the smallest scale: the
+    scale that a range's values refer to is found in a later tile, its first,
+    its last or none, in ranges of many tiles."""
+    rng = np.random.default_rng(D + T)
+    zeros = [0, 30, 64, 100, 128, 200, 449, 2000, 320, 640]
+    L = [700, 400, 900, 130, 700, 1300, 1000, 800, 321, 641]
+    s = build(rng, len(L), T, 4 * H, H, D, bs, L, None, "chain", "bf16", "e4m3")
+    for b, m in enumerate(zeros):
+        for pos in range(min(m, L[b] + T)):
+            blk = int(s["tables"][b, pos // bs])
+            s["v"].view(torch.uint8)[blk, :, pos % bs] = 0
+            s["vs"][blk, :, pos % bs] = 7
+    check(s)
+
+
+def test_the_largest_scales_of_an_e4m3_cache():
+    rng = np.random.default_rng(34)
+    for nan in (False, True):
+        s = build(rng, 2, 3, 8, 2, 128, 16, [900, 70], None, "chain", "bf16", "e4m3")
+        s["vs"][:] = 248
+        s["v"].view(torch.uint8)[:] &= 0x8F          # codes of 2^-5 at most
+        if nan:
+            s["vs"][int(s["tables"][0, 3]), 1, 5, 1] = 255
+        out = check(s)
+        assert np.isnan(out).any() == nan
+
+
 @pytest.mark.parametrize("where", ["ks", "vs", "k", "v"])
 def test_not_a_number_among_the_committed_tokens_of_an_e4m3_cache(where):
     for T, D in ((3, 128), (70, 64)):
