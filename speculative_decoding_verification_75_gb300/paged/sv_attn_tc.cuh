@@ -666,11 +666,10 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             for (int k = 0; k < W; k += 32) tc_ld32(col_s + ch * W + k, x + k);
             tc_wait_ld(x);
           };
-          // (kRaw: loops over chunks, for the instruction cache's sake.)
-          constexpr int kChunks = kKeys / W, kUnroll = S::kRaw ? 1 : kChunks;
+          constexpr int kChunks = kKeys / W;
           float mt = -INFINITY, cf = c_row;
           if constexpr (S::kRaw) cf = fmaxf(c_row * scale_value(k_scale[rs][tiles % kScaleRing]), 1.2e-38f);
-#pragma unroll kUnroll
+#pragma unroll
           for (int ch = 0; ch < kChunks; ++ch) {
             load_s(ch);
             float q0 = -INFINITY, q1 = -INFINITY, q2 = -INFINITY, q3 = -INFINITY;
@@ -715,9 +714,9 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           uint64_t l2a = 0, l2b = 0;
           // The last chunk first: it is in registers, and P's columns are the
           // upper half of S, where a chunk's P covers only S already taken.
-#pragma unroll kUnroll
+#pragma unroll
           for (int ch = kChunks - 1; ch >= 0; --ch) {
-            if (S::kRaw || ch < kChunks - 1) load_s(ch);
+            if (ch < kChunks - 1) load_s(ch);
             uint32_t pk[W / 2];
 #pragma unroll
             for (int k = 0; k < W; k += 2) {
@@ -984,10 +983,17 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const uint32_t ts = tmem + kColS + 128u * s, to = tmem + kColO + 128u * s;
     uint32_t fix = 0;              // parities of the repairs, per stage
     uint32_t nk = 0, nv = 0;       // tiles multiplied so far
-    const auto take = [&](int pos) {
-      const bool good = wait_warp(&rb.full[pos % S::kStages], pos / S::kStages, err);
+    int st = 0, round = 0;         // of the next position
+    const auto take = [&] {
+      const bool good = wait_warp(&rb.full[st], round, err);
       tc_fence_after();
       return good;
+    };
+    const auto next_stage = [&] {
+      if (++st == S::kStages) {
+        st = 0;
+        ++round;
+      }
     };
     // Not kRaw: rows of V behind the committed tokens, keys k0 .. of a stage.
     // What lies behind the last token becomes 0, a value that is not finite
@@ -1012,29 +1018,30 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       fence_async_smem();
       __syncwarp();
     };
-    // S of the tile whose K is at `pos`.
-    const auto qk = [&](const Tile &w, int pos) {
+    // S of a tile.
+    const auto qk = [&](const Tile &w) {
       if (w.first() && !wait_warp(S::kRaw ? &bars.q_ready[s] : &bars.q_full[rs], w.seg, err)) return false;
-      if (!take(pos)) return false;
-      const uint64_t kd = k_desc + (pos % S::kStages) * (S::kStageBytes >> 4);
+      if (!take()) return false;
+      const uint64_t kd = k_desc + st * (S::kStageBytes >> 4);
       const uint32_t buf = nk % kBufs;
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           tc_mma_ss(ts + 64u * buf, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
                     kd + (((k >> 2) * S::kHalf + (k & 3) * 32) >> 4), kQK, k > 0);
-        tc_commit(sv::smem_addr(&rb.empty[pos % S::kStages]));
+        tc_commit(sv::smem_addr(&rb.empty[st]));
         tc_commit(sv::smem_addr(&bars.s_full[s][buf]));
         if (w.last()) tc_commit(sv::smem_addr(&bars.q_empty[s]));
       }
       __syncwarp();
+      next_stage();
       ++nk;
       return true;
     };
     // O += P V.
-    const auto pv = [&](const Tile &w, int pos) {
-      const int st = pos % S::kStages, k0 = w.t * kKeys;
-      if (!take(pos)) return false;
+    const auto pv = [&](const Tile &w) {
+      const int k0 = w.t * kKeys;
+      if (!take()) return false;
       if (!S::kRaw && k0 + kKeys > w.new0) {
         if (!kPair || s == 0) {
           repair(w, k0, st);
@@ -1057,6 +1064,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         tc_commit(sv::smem_addr(&bars.o_done[s][buf]));
       }
       __syncwarp();
+      next_stage();
       ++nv;
       return true;
     };
@@ -1064,9 +1072,9 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     Tile w = tile_of(walk), behind = w;
     const int n = count_of(walk);
 #pragma unroll 1
-    for (int i = 0, pos = 0; ok && i <= n && n > 0; ++i) {
-      if (i < n) ok = qk(w, pos++);
-      if (ok && i > 0) ok = pv(behind, pos++);
+    for (int i = 0; ok && i <= n && n > 0; ++i) {
+      if (i < n) ok = qk(w);
+      if (ok && i > 0) ok = pv(behind);
       behind = w;
       if (i < n) next_tile(a, upt, walk, w);
     }
@@ -1233,10 +1241,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       if (found) seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        sv::mbar_arrive(sv::smem_addr(&rb.full[st]));
-        sv::mbar_arrive(sv::smem_addr(&rb.rempty[rst]));
-      }
+      if (lane < 2) sv::mbar_arrive(sv::smem_addr(lane ? &rb.rempty[rst] : &rb.full[st]));
       if ((st += 2) >= S::kStages) {
         st -= S::kStages;
         ++round;
