@@ -164,9 +164,9 @@ SV_API sv_status sv_kv_compact(const sv_kv_compact_args *args, sv_stream_t strea
  *             initialisation needed; calls that share one are ordered on one
  *             stream.
  * head_dim is a multiple of 8 (of 32 for SV_E4M3), at most 256.  Statistics
- * and sums are fp32; probabilities are rounded to the 16-bit type before
- * their product with v.  A bounded wait that gives up sets SV_FAULT_TIMEOUT
- * in `status`.  Results are deterministic.
+ * and sums are fp32; probabilities may be rounded to the query's type, over an
+ * e4m3 cache to fp16, before their product with v.  A bounded wait that gives
+ * up sets SV_FAULT_TIMEOUT in `status`.  Results are deterministic.
  */
 typedef struct {
     uint64_t struct_bytes;

@@ -3,13 +3,15 @@
 //
 // Rows.  All n new tokens and the G query heads that share a KV head form one
 // matrix of n * G rows, row r = token r / G, head r % G, so that a key is read
-// once for all of them; a tile takes as many whole tokens as fit 128 rows.  S = Q K^T and O = P V run as M = 128 row tiles with
-// 128 keys a step; S and O live in tensor memory (TMEM: lane = row, one
-// thread per row), P overwrites half of its S as the 16-bit A operand.
+// once for all of them; a tile takes as many whole tokens as fit 128 rows.
+// S = Q K^T and O = P V run as M = 128 row tiles with 64 keys a step; S and O
+// live in tensor memory (TMEM: lane = row, one thread per row), P overwrites
+// half of its S as the 16-bit A operand.
 //
 // Two streams of such steps alternate in a thread block, each with a softmax
-// warpgroup of its own, so that the tensor cores work on one while the other
-// takes exponentials.  With at most 128 rows the streams are independent, each
+// warpgroup of its own and two S, so that the tensor cores work on one stream
+// while the other takes exponentials, and on the next scores of a stream while
+// it works on these.  With at most 128 rows the streams are independent, each
 // with a range of work of its own (kPair = false): one goes on while the other
 // stores its rows and begins the next unit.  With more rows each has 128 of
 // the unit's and both use every key tile (kPair = true).
@@ -30,11 +32,27 @@
 //
 // Data.  TMA boxes of one page's rows (a power of two of them that divides the
 // block size) fill 128-byte swizzled tiles through an mbarrier ring; e4m3 tiles
-// arrive raw with their scale bytes and are widened to fp16 by four warps.
+// arrive raw with their scale bytes and are widened to fp16 by eight warps.
 // Rows of V behind the last token are zeroed in shared memory, because
 // 0 * garbage may be NaN; a value that is not finite among the new tokens, or a
 // missing block, marks the unit, which is recomputed row by row
 // (sv_attn_general.cuh).
+//
+// Measured, both kernels together:
+//   131071 keys, 1 token, 64 heads on 8 of 128   92 us, 5.8 TB/s: HBM; 8 us are
+//                                                the join and the first tiles
+//   32 x 9 tokens, 32 heads on 32, 200-2000 keys 114 us, 5.1 TB/s: HBM, and the
+//                                                ends of units of few tiles
+//   8 x 6 tokens, 64 on 8, 1000-4000 keys        28 us, 2.9 TB/s: start, first
+//                                                data and join, 15 us together
+//   16 trees of 64, 32 on 8, 1000-8000 keys      101 us, 555 TFLOP/s: Q K^T at
+//                                                N = 64 is bound by its operands
+//                                                in shared memory; unit ends, join
+//   128 x 6 tokens, e4m3, 500-8000 keys          364 us, 3.2 TB/s: instructions
+//                                                of the wideners and the softmax
+// The kernel's code is fetched by five roles at once: with the loops unrolled
+// further they missed the instruction cache (90 % hits, 423 us for the last case
+// against 379 at 96 %), so each role's loop has one copy of its body.
 #pragma once
 
 #include <cuda.h>
@@ -48,8 +66,9 @@ namespace svp {
 constexpr int kMaxGrid = 152;   // thread blocks, one per SM
 constexpr int kTile = 128;      // rows of a tile
 // Keys of a step, and of a stage.  A stream has two S of 64 keys, so that Q K^T
-// is a step ahead of the softmax.  (One S of 128 keys made Q K^T, softmax and
-// P V a chain that set the pace: TREE_US.)
+// is a step ahead of the softmax.  (With one S of 128 keys Q K^T, softmax and P V
+// were a chain: 413 us for 128 e4m3 requests, 393 with two.  Pairs of row tiles,
+// bound by the tensor cores, take the same time with either.)
 constexpr int kKeys = 64, kBufs = 2;
 constexpr int kScaleRing = 16;  // K tiles that are widened and not yet used, at most 7
 constexpr int kSegRing = 32;    // more segments than any role is ahead of another
@@ -548,14 +567,14 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const uint32_t col_s0 = lanes + kColS + 128u * s, col_o = lanes + kColO + 128u * s;
     const int my = wq * 32 + lane;           // row of the 128-row tile
     const int rs = kPair ? 0 : s;            // range of the block
-    // kRaw: Q as fp16, each row times a power of two that brings its largest
+    // kRaw: bf16 Q as fp16, each row times a power of two that brings its largest
     // magnitude to 2^14 .. 2^15 (exact for elements down to 2^-31 of it, and
     // what is lost below is 2^-39 of it); c_next takes the power back.
     float c_next = p.c;
     const auto prepare_q = [&](const Walk &w) {
       const int rows = min(max(w.r.n - (w.mp * upt + (kPair ? s * p.TT : 0)), 0), p.TT) * a.G;
       if (!wait_warp(&bars.q_full[rs], w.seg, err)) return false;
-      if (my < rows) {
+      if (Q::kIsBf16 && my < rows) {
         uint8_t *q = sq + s * S::kQTile + my * 128;
         uint32_t big = 0;
 #pragma unroll 4
@@ -1089,15 +1108,14 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // becomes code * 2^(e - E), one conversion and one product for two codes
     // (as bf16 numbers they took six, and the widening bound the kernel).  E is
     // the largest e of the stage for K, that of a segment's first stage for V;
-    // S and O are scaled back in fp32.  The product is exact where it is at least
-    // 2^-14 (a code has 4 significant bits: down to 2^-21 it still is), and off
-    // by 2^-25 at most below.  A group's largest code is at least 224, so for
-    // e >= E - 16 that is 2^-16 of its largest value; V is held to this, for its
-    // elements are results.  For K, where only the sum counts, 2^-25 is 2^-33 of
-    // the stage's largest value; it is held to e >= E - 24, so that a row that
-    // is not seen cannot wipe out those that are.  A unit whose scales differ by
-    // more is recomputed.  Groups at the smallest scale (2^-120, which the cache
-    // writes for zeros) do not count and become 0 in V and beside larger ones.
+    // S and O are scaled back in fp32.  A code is a multiple of 2^-9, the product
+    // exact down to e = E - 15, and off by 2^-25 at most below.  V is held to the
+    // former, for its elements are results.  For K, where only the sum counts,
+    // 2^-25 is 2^-33 of the stage's largest value; it is held to e >= E - 24, so
+    // that a row that is not seen cannot wipe out those that are.  A unit whose
+    // scales differ by more is recomputed.  Groups at the smallest scale (2^-120,
+    // which the cache writes for zeros) do not count and become 0 in V and beside
+    // larger ones.
     //
     // The wideners of a ring are two groups, of its even and its odd positions:
     // what a stage costs besides its conversions (two waits, the scales, a
@@ -1199,7 +1217,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         if (__any_sync(kFull, far > span)) {
           // Scales that the products cannot hold (448 * 2^7 is below fp16's
           // largest), and NaN: the unit is recomputed.
-          const int below = ref - (is_v ? 16 : 24), above = min(is_v ? ref + 7 : ref, 254);
+          const int below = ref - (is_v ? 15 : 24), above = min(is_v ? ref + 7 : ref, 254);
 #pragma unroll
           for (int t = 0; t < kTurn; ++t) {
             found = found || (row0 + (t0 + t) * kRowStep < live && x[t] > 7 && (x[t] < below || x[t] > above));

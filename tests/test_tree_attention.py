@@ -107,6 +107,8 @@ CASES = [
     (1, 2, 8, 1, 128, 256, [700], None, "chain", "fp16", "fp16"),
     (1, 3, 8, 1, 64, 160, [700], None, "chain", "bf16", "e4m3"),
     (40, 2, 2, 1, 64, 8, list(range(40)), None, "chain", "bf16", "bf16"),
+    (3, 6, 64, 8, 128, 16, [5, 129, 777], [1, 6, 3], "tree", "fp16", "e4m3"),
+    (1, 65, 8, 2, 64, 32, [200], None, "chain", "fp16", "e4m3"),
 ]
 
 
@@ -219,6 +221,8 @@ MANY = [
     (4, 40, 16, 4, 128, 128, [9000, 20, 5000, 7000], [40, 7, 40, 36], "chain", "bf16", "e4m3"),
     (4, 70, 8, 4, 64, 32, [6000, 120, 4000, 5000], None, "any", "fp16", "fp16"),
     (4, 70, 8, 4, 64, 64, [6000, 120, 4000, 5000], None, "tree", "bf16", "e4m3"),
+    (5, 2, 32, 32, 128, 16, [2000, 1000, 1, 127, 1500], None, "any", "fp16", "e4m3"),
+    (4, 70, 8, 4, 128, 64, [6000, 120, 4000, 5000], None, "tree", "fp16", "e4m3"),
 ]
 
 
