@@ -1113,9 +1113,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // former, for its elements are results.  For K, where only the sum counts,
     // 2^-25 is 2^-33 of the stage's largest value; it is held to e >= E - 24, so
     // that a row that is not seen cannot wipe out those that are.  A unit whose
-    // scales differ by more is recomputed.  Groups at the smallest scale (2^-120,
-    // which the cache writes for zeros) do not count and become 0 in V and beside
-    // larger ones.
+    // scales differ by more is recomputed.  Zeros at the smallest scale (2^-120,
+    // which the cache writes for them) do not count.
     //
     // The wideners of a ring are two groups, of its even and its odd positions:
     // what a stage costs besides its conversions (two waits, the scales, a
@@ -1220,7 +1219,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
           const int below = ref - (is_v ? 15 : 24), above = min(is_v ? ref + 7 : ref, 254);
 #pragma unroll
           for (int t = 0; t < kTurn; ++t) {
-            found = found || (row0 + (t0 + t) * kRowStep < live && x[t] > 7 && (x[t] < below || x[t] > above));
+            const uint32_t any = (c[t].x | c[t].y | c[t].z | c[t].w) & 0x7f7f7f7fu;
+            found = found || (row0 + (t0 + t) * kRowStep < live && (x[t] > 7 || any) && (x[t] < below || x[t] > above));
             const float mf = __uint_as_float(static_cast<uint32_t>(min(max(x[t] - ref + 127, 0), 254)) << 23);
             m[t] = pack2<F16>(mf, mf);
           }

@@ -165,6 +165,17 @@ def test_values_of_an_e4m3_cache_that_begin_with_zeros(D, T, bs, H):
     check(s)
 
 
+@pytest.mark.parametrize("D,T", [(128, 3), (64, 70)])
+def test_the_smallest_scales_of_an_e4m3_cache(D, T):
+    """Values of 2^-112 and less: at the smallest scale, alone and beside zeros."""
+    s = build(np.random.default_rng(35), 2, T, 8, 2, D, 16, [300, 70], None, "chain", "bf16", "e4m3")
+    s["vs"][:] = 7
+    check(s)
+    assert ref.to64(call(s)).any()
+    s["vs"][int(s["tables"][0, 3])] = 90
+    check(s)
+
+
 def test_the_largest_scales_of_an_e4m3_cache():
     rng = np.random.default_rng(34)
     for nan in (False, True):
