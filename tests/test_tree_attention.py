@@ -109,6 +109,7 @@ CASES = [
     (40, 2, 2, 1, 64, 8, list(range(40)), None, "chain", "bf16", "bf16"),
     (3, 6, 64, 8, 128, 16, [5, 129, 777], [1, 6, 3], "tree", "fp16", "e4m3"),
     (1, 65, 8, 2, 64, 32, [200], None, "chain", "fp16", "e4m3"),
+    (2, 513, 4, 2, 64, 32, [0, 300], [513, 400], "chain", "fp16", "e4m3"),   # long prompts
 ]
 
 
