@@ -72,6 +72,7 @@ constexpr int kTile = 128;      // rows of a tile
 constexpr int kKeys = 64, kBufs = 2;
 constexpr int kScaleRing = 16;  // K tiles that are widened and not yet used, at most 7
 constexpr int kSegRing = 32;    // more segments than any role is ahead of another
+constexpr int kMarkBits = 1024; // of a range's marked segments, by number modulo this
 
 // The first segment of a range: its unit, the tile of the unit it begins at,
 // and the unit's tiles; `total` tiles of all ranges.
@@ -470,6 +471,24 @@ __device__ __forceinline__ bool wait_warp(const uint64_t *bar, uint32_t parity, 
   return __any_sync(kFull, sv::mbar_try_wait(at, parity)) || wait_long(at, parity, err);
 }
 
+// The marked units of a range that its ends do not cut, by all warps of the
+// block, when no role waits for another any more: the 128 rows of a tile take
+// 4 us a key (e4m3: 8.6), seconds over a long context, and bounded waits would
+// run out.  Segments whose number is a marked one's modulo kMarkBits are done
+// again as well.
+template <typename Q, typename C, int D>
+__device__ __noinline__ void recompute_marked(const AttnParams &p, int upt, const Walk &begin, const uint32_t *marks,
+                                              int warp, int warps) {
+#pragma unroll 1
+  for (Walk w = begin; w.on; next_segment(p, upt, w)) {
+    if (w.t0 > 0 || w.t1 < w.r.kt || !(marks[w.seg / 32 % (kMarkBits / 32)] >> (w.seg % 32) & 1u)) continue;
+    const int rows = min(w.r.n - w.mp * upt, upt) * p.G;
+#pragma unroll 1
+    for (int row = warp; row < rows; row += warps)
+      recompute_row<Q, C, D>(p, w.b, w.mp * upt + row / p.G, w.h * p.G + row % p.G);
+  }
+}
+
 // ------------------------------------------------------------ main kernel ----
 
 template <typename Q, typename C, int D, bool kPair>
@@ -483,6 +502,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ Walk sh_walk[S::kStreams];
   __shared__ int seg_bad[S::kStreams][kSegRing];  // holds 1 + a marked segment's number
+  __shared__ uint32_t marks[S::kStreams][kMarkBits / 32];  // whole units to recompute
+  __shared__ int marked[S::kStreams];                      // whether there are any
   // kRaw: scale bytes that a K tile, and (plus 256) a segment's V, refer to.
   __shared__ int k_scale[S::kStreams][kScaleRing], v_scale[S::kStreams][kSegRing];
 
@@ -522,6 +543,12 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     for (int s = 0; s < S::kStreams; ++s)
       for (int i = 0; i < kSegRing; ++i) seg_bad[s][i] = 0;
     sv::fence_mbar_init();
+  }
+  if (warp == 3) {
+    for (int s = 0; s < S::kStreams; ++s) {
+      for (int i = lane; i < kMarkBits / 32; i += 32) marks[s][i] = 0;
+      if (lane == 0) marked[s] = 0;
+    }
   }
   if (tid == 32) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.kmap) : "memory");
@@ -793,11 +820,11 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         }
         if (boss) reinterpret_cast<int *>(slot)[(D + 2) * p.slot_rows] = bad ? 1 : 0;
       }
-      __syncwarp();
-      if (bad && whole) {
-        for (int row = wq; row < tile_rows; row += 4)
-          recompute_row<Q, C, D>(a, sg.b, tok0 + row / a.G, sg.h * a.G + row % a.G);
+      if (bad && whole && boss) {
+        marks[rs][seg / 32 % (kMarkBits / 32)] |= 1u << (seg % 32);
+        marked[rs] = 1;
       }
+      __syncwarp();
       if (active && !bad) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -1286,6 +1313,10 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 11) tc_dealloc(tmem, 512);
+
+#pragma unroll 1
+  for (int rs = 0; rs < S::kStreams; ++rs)
+    if (marked[rs]) recompute_marked<Q, C, D>(a, upt, sh_walk[rs], marks[rs], warp, S::kWarps);
 }
 
 // ---------------------------------------------------------- second kernel ----

@@ -1,0 +1,138 @@
+"""Calls of the paged-cache operators at the edges of what they take: marked
+units with other requests behind them, rows without a finite score, powers of
+two at the ends of their range, lengths far behind the table, and one workspace
+for all sizes."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as ref
+from test_paged_kv import DEV, F8, TD, i32
+from test_tree_attention import UNIT, build, call, check
+
+gpu = pytest.mark.gpu
+
+
+def raw(t):
+    return t.view(torch.uint8) if t.dtype == F8 else t
+
+
+# ---------------------------------------------------------- marked units ----
+
+MARKED = [
+    (330, 2, 2, 2, 64, "bf16", "bf16"), (330, 2, 2, 2, 128, "bf16", "e4m3"),
+    # 136 rows of a KV head: two row tiles.
+    (80, 17, 32, 4, 64, "fp16", "fp16"), (80, 17, 32, 4, 128, "bf16", "e4m3")]
+
+
+@gpu
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,dt,cdt,why", [
+    (*c, why) for c in MARKED for why in ("value", "block", "scale") if why != "scale" or c[-1] == "e4m3"])
+def test_marked_units_among_others_of_a_range(B, T, Hq, Hkv, D, dt, cdt, why):
+    """Units of one or two tiles, several to a range, some of them to be
+    recomputed: a new token's value that is not finite, a missing block, scales
+    too far apart for the products."""
+    rng = np.random.default_rng(B + T)
+    L = [int(x) for x in rng.integers(0, 60, B)]
+    s = build(rng, B, T, Hq, Hkv, D, 16, L, None, "chain", dt, cdt)
+    status = 0
+    for b in (0, 3, 4, 5, 40, B - 1):
+        if why == "value":
+            j = L[b] + T - 1
+            raw(s["v"])[int(s["tables"][b, j // 16]), :, j % 16] = 0x7F if cdt == "e4m3" else float("inf")
+        elif why == "block":
+            s["tables"][b, 0] = -1
+            status = ref.MISSING
+        else:
+            s["vs"][int(s["tables"][b, 0]), :, :, 0] = 90
+    check(s, want_status=status)
+
+
+@gpu
+def test_more_units_in_a_range_than_marks_are_kept_for():
+    """Over a thousand units of one tile in each range; some requests' only
+    block is missing, and their rows are 0."""
+    import speculative_decoding_verification_75_gb300 as sv
+    B, H, D, bs, L = 10400, 32, 64, 16, 9
+    g = torch.Generator(device=DEV).manual_seed(3)
+    k, v = (torch.randn(64, H, bs, D, generator=g, device=DEV).bfloat16() for _ in range(2))
+    q = torch.randn(B, 1, H, D, generator=g, device=DEV).bfloat16()
+    tab = torch.randint(64, (B, 1), generator=g, device=DEV).int()
+    gone = torch.randperm(B, generator=g, device=DEV)[:40]
+    tab[gone] = -1
+    out = torch.full_like(q, -7.0)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    sv.tree_attention(q, k, v, tab, i32([L] * B), out=out, status=status)
+    assert status.item() == ref.MISSING
+    assert not out[gone].any()
+    live = torch.ones(B, dtype=torch.bool, device=DEV)
+    live[gone] = False
+    at = tab[live, 0].long()
+    for i in range(0, at.numel(), 2000):
+        kk, vv = (x[at[i:i + 2000], :, :L + 1].double() for x in (k, v))
+        p = torch.einsum("bhd,bhsd->bhs", q[live][i:i + 2000, 0].double(), kk).mul(D ** -0.5).softmax(-1)
+        o, a = (torch.einsum("bhs,bhsd->bhd", p, x) for x in (vv, vv.abs()))
+        # Probabilities and results rounded to bf16; fp32 scores and sums are
+        # off by far less than the tenth of that allowed for them.
+        assert ((out[live][i:i + 2000, 0].double() - o).abs() <= UNIT["bf16"] * (1.1 * a + o.abs())).all()
+
+
+@gpu
+def test_a_marked_unit_of_a_long_context_holds_up_nobody():
+    """Two requests over 98304 keys with a value that is not finite at their
+    last token, and healthy ones behind them in the same ranges.  (One warp
+    recomputes a row at about 1 us a key; 32 rows to a warp took 3.2 s, longer
+    than the kernel's other warps wait.)
+
+    Every request has the same 64 blocks over and over, so that a softmax over
+    its keys is one over 8192 keys, each counted 12 times, and its new tokens."""
+    import speculative_decoding_verification_75_gb300 as sv
+    B, T, G, D, bs, pool, times = 640, 16, 8, 128, 128, 64, 12
+    L = pool * bs * times
+    g = torch.Generator(device=DEV).manual_seed(5)
+    k, v = (torch.randn(pool + B, 1, bs, D, generator=g, device=DEV).mul(100).clamp(-448, 448).to(F8)
+            for _ in range(2))
+    ks, vs = (torch.full((pool + B, 1, bs, D // 32), 120, dtype=torch.uint8, device=DEV) for _ in range(2))
+    tab = torch.empty(B, pool * times + 1, dtype=torch.int32, device=DEV)
+    tab[:, :-1] = (torch.arange(pool * times, device=DEV) % pool).int()
+    tab[:, -1] = torch.arange(B, device=DEV).int() + pool
+    q = torch.randn(B, T, G, D, generator=g, device=DEV).bfloat16()
+    # Range i of 304 begins with unit 640 i / 304: 99 and 300 lie within one,
+    # with others behind them.
+    for b in (99, 300):
+        raw(v)[pool + b, 0, T - 1] = 0x7F
+    out = torch.full_like(q, -7.0)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    sv.tree_attention(q, k, v, tab, i32([L] * B), k_scale=ks, v_scale=vs, out=out, status=status)
+    assert status.item() == 0
+    K, V = ((x.double() / 128).squeeze(1) for x in (k, v))
+    K0, V0 = K[:pool].flatten(0, 1), V[:pool].flatten(0, 1)
+    see = torch.ones(T, T, dtype=torch.bool, device=DEV).tril()
+    for b in (98, 99, 100, 101, 300, 301):
+        x0 = torch.einsum("tgd,sd->tgs", q[b].double(), K0) * D ** -0.5
+        x1 = torch.einsum("tgd,sd->tgs", q[b].double(), K[pool + b, :T]) * D ** -0.5
+        x1 = x1.masked_fill(~see[:, None], -math.inf)
+        m = torch.maximum(x0.amax(-1), x1.amax(-1))[..., None]
+        p0, p1 = times * (x0 - m).exp(), (x1 - m).exp()
+        l = (p0.sum(-1) + p1.sum(-1))[..., None]
+        o = torch.einsum("tgs,sd->tgd", p0 / l, V0)
+        a = torch.einsum("tgs,sd->tgd", p0 / l, V0.abs()) + torch.einsum("tgs,sd->tgd", p1 / l, V[pool + b, :T].nan_to_num().abs())
+        for t in range(T):                    # a row's own values only: 0 * NaN
+            o[t] += torch.einsum("gs,sd->gd", p1[t, :, :t + 1] / l[t], V[pool + b, :t + 1])
+        assert bool(o.isnan().any()) == (b in (99, 300))
+        assert torch.equal(out[b].isnan(), o.isnan())
+        # Tolerance: probabilities to fp16 (2^-11, below its normal numbers
+        # 2^-32 of the largest), the result to bf16, scores and exponentials as
+        # in paged_ref, fp32 sums: a chain of 1536 tiles of 4 products each,
+        # doubled where additions truncate, and of 1536 tiles and 64 terms for
+        # the denominator; a recomputed row's is one term per key.
+        S = L + T
+        ds = (D + 8) * 2.0 ** -23 * D ** -0.5 * max(
+            torch.einsum("tgd,sd->tgs", q[b].double().abs(), x.abs()).max().item() for x in (K0, K[pool + b, :T]))
+        chain = 2 * (S + 8) if b in (99, 300) else 2 * 1536 * 4 + 1536 + 64
+        t = (2.0 ** -11 + 2 * ds + 2.0 ** -19 + chain * 2.0 ** -24) * a + 2.0 ** -8 * o.abs()
+        t = 1.01 * (t + S * 2.0 ** -32 * V0.abs().max() / l)
+        fine = ~o.isnan()
+        assert ((out[b].double() - o).abs()[fine] <= t[fine]).all()
