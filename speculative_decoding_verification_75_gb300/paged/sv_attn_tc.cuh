@@ -1135,13 +1135,12 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     // becomes code * 2^(e - E), one conversion and one product for two codes
     // (as bf16 numbers they took six, and the widening bound the kernel).  E is
     // the largest e of the stage for K, that of a segment's first stage for V;
-    // S and O are scaled back in fp32.  A code is a multiple of 2^-9, the product
-    // exact down to e = E - 15, and off by 2^-25 at most below.  V is held to the
-    // former, for its elements are results.  For K, where only the sum counts,
-    // 2^-25 is 2^-33 of the stage's largest value; it is held to e >= E - 24, so
-    // that a row that is not seen cannot wipe out those that are.  A unit whose
-    // scales differ by more is recomputed.  Zeros at the smallest scale (2^-120,
-    // which the cache writes for them) do not count.
+    // S and O are scaled back in fp32.  A code is a multiple of 2^-9, so that the
+    // product is exact down to e = E - 15.  A unit whose scales differ by more is
+    // recomputed: the key that sets a stage's E may be one that a row does not
+    // see, or sees without weight, and must not round those that count (at
+    // E - 24 a code is rounded to a whole number).  Zeros at the smallest scale
+    // (2^-120, which the cache writes for them) do not count.
     //
     // The wideners of a ring are two groups, of its even and its odd positions:
     // what a stage costs besides its conversions (two waits, the scales, a
@@ -1243,7 +1242,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         if (__any_sync(kFull, far > span)) {
           // Scales that the products cannot hold (448 * 2^7 is below fp16's
           // largest), and NaN: the unit is recomputed.
-          const int below = ref - (is_v ? 15 : 24), above = min(is_v ? ref + 7 : ref, 254);
+          const int below = ref - 15, above = min(is_v ? ref + 7 : ref, 254);
 #pragma unroll
           for (int t = 0; t < kTurn; ++t) {
             const uint32_t any = (c[t].x | c[t].y | c[t].z | c[t].w) & 0x7f7f7f7fu;

@@ -136,3 +136,61 @@ def test_a_marked_unit_of_a_long_context_holds_up_nobody():
         t = 1.01 * (t + S * 2.0 ** -32 * V0.abs().max() / l)
         fine = ~o.isnan()
         assert ((out[b].double() - o).abs()[fine] <= t[fine]).all()
+
+
+# ---------------------------------------------------------------- scales ----
+
+def lse_within_fp32(s, scale):
+    """The log-sum-exp against 64 bits, to what fp32 scores and sums lose: each
+    score's error counts by its probability (the log's derivative), so that a
+    key without weight allows none."""
+    B, T, Hq, D = s["q"].shape
+    lse = torch.zeros(B, T, Hq, device=DEV)
+    call(s, lse=lse, scale=scale)
+    cache = ref.Cache(s["k"], s["v"], torch.from_numpy(s["tables"]), s["ks"], s["vs"])
+    q, lse = ref.to64(s["q"]), ref.to64(lse)
+    for b in range(B):
+        L, n = s["L"][b], s["n"][b]
+        at = [cache.place(b, j)[:2] for j in range(L + n)]
+        K = np.stack([cache.k[blk, :, row] for blk, row in at])
+        for i in range(n):
+            see = np.ones(L + n, dtype=bool)
+            see[L:] = np.arange(n) <= i if s["mask"] is None else s["mask"][b, i, :n]
+            for h in range(Hq):
+                k = K[see, h // (Hq // K.shape[1])]
+                x = k @ q[b, i, h] * scale
+                # Products of two 16-bit values are exact in fp32, one rounding
+                # per addition, doubled where an addition truncates.
+                dx = (D + 8) * 2.0 ** -23 * (np.abs(k) @ np.abs(q[b, i, h])) * scale
+                p = np.exp(x - x.max())
+                want = x.max() + np.log(p.sum())
+                p /= p.sum()
+                tol = (p @ dx) * 1.01 + abs(x.max()) * 2.0 ** -22 + (len(x) + 8) * 2.0 ** -24 + 2.0 ** -19
+                assert abs(lse[b, i, h] - want) <= tol, (b, i, h, lse[b, i, h] - want, tol)
+
+
+@gpu
+@pytest.mark.parametrize("above", [15, 16, 18, 20, 22, 24, 25, 40])
+@pytest.mark.parametrize("T", [4, 20])
+def test_a_large_key_without_weight_does_not_round_the_others(above, T):
+    """A draft that no row sees, and a committed key whose scores are far below
+    the rest, 2^above times as large as the other keys."""
+    rng = np.random.default_rng(above)
+    s = build(rng, 1, T, 8, 1, 128, 16, [12], None, "tree", "bf16", "e4m3")
+    sign = torch.from_numpy(np.where(rng.random(128) < 0.5, -1.0, 1.0)).to(DEV)
+    s["q"] = (s["q"].abs() * sign).to(torch.bfloat16)
+    s["ks"][:] = 120
+    place = lambda j: (int(s["tables"][0, j // 16]), j % 16)  # noqa: E731
+    plain = s["k"].view(torch.uint8).clone()
+    for what in ("hidden", "unlikely"):
+        s["k"].view(torch.uint8).copy_(plain)
+        s["ks"][:] = 120
+        if what == "hidden":
+            s["mask"][0, :, T - 2] = False
+            blk, row = place(12 + T - 2)
+        else:
+            blk, row = place(5)
+            s["k"][blk, 0, row] = (-448 * sign).to(F8)
+        s["ks"][blk, :, row] = 120 + above
+        check(s)
+        lse_within_fp32(s, 128 ** -0.5)
