@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         const int t = tok0 + my / a.G, g = my % a.G;
         const int64_t row = (static_cast<int64_t>(sg.b) * a.bt.T + t) * a.Hq + sg.h * a.G + g;
         orow = a.out + row * (D * 2);
-        inv = l == 0.f ? 0.f : vs / l;
+        inv = vs / l;
         if (mine && a.lse && !bad) a.lse[row] = l == 0.f ? -INFINITY : mx * kLn2 + logf(l);
       } else {
         // Slot 0 of the range where the segment starts it, else slot 1.
@@ -838,7 +838,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
                 uint32_t u[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  u[e] = pack2<Q>(__uint_as_float(o[k + 2 * e]) * inv, __uint_as_float(o[k + 2 * e + 1]) * inv);
+                  u[e] = l == 0.f ? 0u   // not 0 * O: it may be NaN
+                                  : pack2<Q>(__uint_as_float(o[k + 2 * e]) * inv, __uint_as_float(o[k + 2 * e + 1]) * inv);
                 *reinterpret_cast<uint4 *>(orow + (c + k) * 2) = make_uint4(u[0], u[1], u[2], u[3]);
               }
             } else {
@@ -1414,13 +1415,14 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
     }
   }
   if (!in) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = 1.f / l;
   const int t = tok0 + row / a.G, g = row % a.G;
   const int64_t orow = (static_cast<int64_t>(b) * a.bt.T + t) * a.Hq + h * a.G + g;
 #pragma unroll
   for (int e = 0; e < E; ++e)
     *reinterpret_cast<uint2 *>(a.out + orow * (D * 2) + (e * kCols + d4) * 8) =
-        make_uint2(pack2<Q>(v[e].x * inv, v[e].y * inv), pack2<Q>(v[e].z * inv, v[e].w * inv));
+        l == 0.f ? make_uint2(0u, 0u)   // not 0 * v: it may be NaN
+                 : make_uint2(pack2<Q>(v[e].x * inv, v[e].y * inv), pack2<Q>(v[e].z * inv, v[e].w * inv));
   if (a.lse && d4 == 0) a.lse[orow] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 

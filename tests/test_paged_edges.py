@@ -194,3 +194,29 @@ def test_a_large_key_without_weight_does_not_round_the_others(above, T):
         s["ks"][blk, :, row] = 120 + above
         check(s)
         lse_within_fp32(s, 128 ** -0.5)
+
+
+# --------------------------------------------------------- rows and keys ----
+
+@gpu
+@pytest.mark.parametrize("D,dt,cdt", [(128, "bf16", "bf16"), (64, "fp16", "fp16"), (128, "bf16", "e4m3"),
+                                      (40, "bf16", "bf16"), (32, "bf16", "e4m3")])
+@pytest.mark.parametrize("T,L", [(2, [9, 0]), (2, [5000, 700]), (20, [3000, 33])])
+def test_a_row_with_no_score_above_minus_infinity_is_zero(D, dt, cdt, T, L):
+    """Whatever its values hold, infinities and NaN among them, in a unit of
+    one range and in one that ranges cut."""
+    s = build(np.random.default_rng(T), 2, T, 8, 1, D, 16, L, None, "chain", dt, cdt)
+    if cdt == "e4m3":
+        s["k"].view(torch.uint8).bitwise_and_(0x7F).bitwise_or_(0x08).clamp_(max=0x7E)
+        s["q"][:] = -math.inf
+    else:
+        s["q"] = s["q"].abs() + 0.5
+        s["k"][:] = -math.inf
+    for b in range(2):
+        for j in range(3, L[b], 5):         # committed tokens' values
+            raw(s["v"])[int(s["tables"][b, j // 16]), :, j % 16] = (
+                0x7F if cdt == "e4m3" else math.inf if j % 2 else math.nan)
+    lse = torch.zeros(2, T, 8, device=DEV)
+    out = call(s, lse=lse)
+    assert (out == 0).all()
+    assert (lse == -math.inf).all()
