@@ -294,6 +294,13 @@ struct Shape {
   static constexpr int kSmem = kQBytes + kStreams * (kStages * kStageBytes + kRawStages * kRawBytes);
 };
 
+// Least factor of a score: with 0, -inf would become NaN.  Nothing that a finite
+// product of it reaches 2^-20.
+constexpr float kLeast = 1.4e-45f;
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // TMEM columns.
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream (S: + 64 * buffer)
 constexpr uint32_t kPOff = kKeys / 2;       // P in the upper half of its S
@@ -596,8 +603,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     const int rs = kPair ? 0 : s;            // range of the block
     // kRaw: bf16 Q as fp16, each row times a power of two that brings its largest
     // magnitude to 2^14 .. 2^15 (exact for elements down to 2^-31 of it, and
-    // what is lost below is 2^-39 of it); c_next takes the power back.
-    float c_next = p.c;
+    // what is lost below is 2^-39 of it); a tile's factor takes 2^q_next back.
+    int q_next = 0;
     const auto prepare_q = [&](const Walk &w) {
       const int rows = min(max(w.r.n - (w.mp * upt + (kPair ? s * p.TT : 0)), 0), p.TT) * a.G;
       if (!wait_warp(&bars.q_full[rs], w.seg, err)) return false;
@@ -612,7 +619,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         }
         const int e = max(static_cast<int>(max(big & 0xffffu, big >> 16) >> 7), 14);   // 127 + exponent
         const float m = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);         // 2^(141 - e)
-        c_next = fmaxf(p.c * __uint_as_float(static_cast<uint32_t>(max(e - 14, 1)) << 23), 1.2e-38f);
+        q_next = e - 141;
 #pragma unroll 4
         for (int ch = 0; ch < D / 8; ++ch) {
           uint4 *at = reinterpret_cast<uint4 *>(q + (ch >> 3) * (kTile * 128) + (((ch & 7) ^ (my & 7)) << 4));
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
 #pragma unroll 1
     while (ok && walk.on) {
       const Walk sg = walk;
-      const float c_row = c_next;
+      const int q_exp = q_next;
       const Req &r = sg.r;
       const int nt = sg.t1 - sg.t0, seg = sg.seg;
       // Tokens and rows of this stream's tile.
@@ -713,8 +720,13 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
             tc_wait_ld(x);
           };
           constexpr int kChunks = kKeys / W;
-          float mt = -INFINITY, cf = c_row;
-          if constexpr (S::kRaw) cf = fmaxf(c_row * scale_value(k_scale[rs][tiles % kScaleRing]), 1.2e-38f);
+          float mt = -INFINITY, cf = p.c;
+          if constexpr (S::kRaw) {
+            // The powers of the row's queries and of the tile's keys together, for
+            // they may cancel; in two steps, for the sum may not be an exponent.
+            const int e = max(q_exp + k_scale[rs][tiles % kScaleRing] - 127, -252), e0 = e >> 1;
+            cf = fmaxf(p.c * pow2(e0) * pow2(e - e0), kLeast);
+          }
 #pragma unroll
           for (int ch = 0; ch < kChunks; ++ch) {
             load_s(ch);

@@ -369,7 +369,7 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
   const bool pair = ap.bt.T > w.TT;
   p.box = 8;  // a power of two that divides the block size, at most a stage
   while (p.box < kKeys && ap.c.bs % (2 * p.box) == 0) p.box *= 2;
-  p.c = std::max(std::fabs(ap.scale_log2), 1.2e-38f);  // not 0: -inf times it stays -inf
+  p.c = std::max(std::fabs(ap.scale_log2), kLeast);
   p.negate = ap.scale_log2 < 0.f;
   p.TT = w.TT;
   p.qbox = std::min(w.TT, ap.bt.T);

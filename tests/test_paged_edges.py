@@ -220,3 +220,26 @@ def test_a_row_with_no_score_above_minus_infinity_is_zero(D, dt, cdt, T, L):
     out = call(s, lse=lse)
     assert (out == 0).all()
     assert (lse == -math.inf).all()
+
+
+@gpu
+@pytest.mark.parametrize("q_exp,k_byte", [(-120, 240), (-126, 246), (-112, 232), (100, 20), (-60, 60)])
+def test_powers_of_queries_and_keys_that_cancel(q_exp, k_byte):
+    """Tiny queries over keys with enormous scales, and the reverse: scores of
+    a few units."""
+    for T in (3, 20):
+        rng = np.random.default_rng(T)
+        s = build(rng, 2, T, 8, 1, 64, 16, [100, 7], None, "chain", "bf16", "e4m3")
+        s["q"] = (s["q"].double() * 2.0 ** q_exp).to(torch.bfloat16)
+        s["ks"][:] = torch.from_numpy(rng.integers(k_byte - 1, k_byte + 2, tuple(s["ks"].shape)).astype(np.uint8)).to(DEV)
+        check(s)
+
+
+@gpu
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -140, -(2.0 ** -140)])
+def test_a_scale_that_leaves_nothing_of_large_products(scale):
+    """q . k of 2^120 and more, and a scale that makes every score next to 0."""
+    s = build(np.random.default_rng(2), 2, 3, 8, 1, 64, 16, [100, 7], None, "chain", "bf16", "bf16")
+    s["q"] *= 2.0 ** 58
+    s["k"] *= 2.0 ** 58
+    check(s, scale=scale)
