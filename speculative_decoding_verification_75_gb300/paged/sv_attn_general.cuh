@@ -45,15 +45,15 @@ __device__ __forceinline__ void attend(const AttnParams &p, int b, int i, int h,
       p.mask ? p.mask + b * p.msb + static_cast<int64_t>(i) * p.bt.T : nullptr;
   for (int64_t jj = j0; jj < total; jj += step) {
     const int j = static_cast<int>(jj) + lane;
-    bool see = jj + lane < total;
+    const bool in = jj + lane < total;
+    const int id = in ? block_of(p.c, b, j, st) : -1;  // hidden positions too: their problems are reported
+    bool see = id >= 0;
     if (see && j >= L) see = mrow ? ld8(mrow + (j - L)) != 0 : j - L <= i;
     int64_t at = 0, sat = 0;
     if (see) {
-      const int id = block_of(p.c, b, j, st);
-      see = id >= 0;
       const int row = j % p.c.bs;
-      at = (see ? id : 0) * p.c.block_bytes + head_bytes + static_cast<int64_t>(row) * row_bytes;
-      sat = (see ? id : 0) * p.c.sblock_bytes + shead + static_cast<int64_t>(row) * srow;
+      at = id * p.c.block_bytes + head_bytes + static_cast<int64_t>(row) * row_bytes;
+      sat = id * p.c.sblock_bytes + shead + static_cast<int64_t>(row) * srow;
     }
     float x = -INFINITY;
     if (see) {

@@ -243,3 +243,19 @@ def test_a_scale_that_leaves_nothing_of_large_products(scale):
     s["q"] *= 2.0 ** 58
     s["k"] *= 2.0 ** 58
     check(s, scale=scale)
+
+
+@gpu
+@pytest.mark.parametrize("D", [40, 128])
+def test_problems_of_hidden_positions_are_reported_too(D):
+    """Drafts that no row sees, in a missing block, one behind the pool or
+    behind the table: the status word is the same for every head dimension."""
+    from speculative_decoding_verification_75_gb300 import api, kv
+    for entry, want in ((-1, api.SV_KV_MISSING_BLOCK), (99, kv.SV_KV_BAD_BLOCK), (None, api.SV_KV_TABLE_SHORT)):
+        s = build(np.random.default_rng(D), 1, 20, 4, 2, D, 16, [16], None, "tree", "bf16", "bf16")
+        s["mask"][0, :, 16:] = False            # drafts 16 .. 19: positions 32 .. 35
+        if entry is None:
+            s["tables"] = s["tables"][:, :2].copy()
+        else:
+            s["tables"][0, 2] = entry
+        check(s, want_status=want)
