@@ -32,6 +32,14 @@ struct RowState {
   float o[kMaxD / 32];
 };
 
+// Positions of request b that the table holds.  A length far behind it costs no
+// look-ups: 2^31 positions of a row would take seconds.
+__device__ __forceinline__ int held(const Cache &c, int L, int n, uint32_t &st) {
+  const int total = min(L + n, c.max_blocks * c.bs);  // both below 2^31
+  if (total < L + n) st |= SV_KV_TABLE_SHORT;
+  return total;
+}
+
 // Positions j0 + lane, j0 + step + lane, ... below `total` of row (b, i) and
 // KV head h, by one warp.  load_q(d, f): elements d .. d + 7 of the row.
 template <typename C, int kMaxD, typename LoadQ>
@@ -145,7 +153,7 @@ __device__ __noinline__ void recompute_row(const AttnParams &p, int b, int i, in
   r.l = 0.f;
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) r.o[e] = 0.f;
-  attend<C, D>(p, b, i, hq / p.G, L, n, L + n, load_q, 0, 32, lane, r, st);
+  attend<C, D>(p, b, i, hq / p.G, L, n, held(p.c, L, n, st), load_q, 0, 32, lane, r, st);
   store_row<Q, D>(p, (static_cast<int64_t>(b) * p.bt.T + i) * p.Hq + hq, lane, r);
 }
 
@@ -187,7 +195,7 @@ __global__ void __launch_bounds__(32 * kGenWarps) sv_attn_general_kernel(const A
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = qs[d + e];
   };
-  attend<C, kMaxD>(p, b, i, h / p.G, L, n, L + n, load_q, warp * 32, 32 * kGenWarps, lane, r, st);
+  attend<C, kMaxD>(p, b, i, h / p.G, L, n, held(p.c, L, n, st), load_q, warp * 32, 32 * kGenWarps, lane, r, st);
 #pragma unroll
   for (int e = 0; e < kMaxD / 32; ++e) part[warp][lane + 32 * e] = r.o[e];
   if (lane == 0) {

@@ -259,3 +259,28 @@ def test_problems_of_hidden_positions_are_reported_too(D):
         else:
             s["tables"][0, 2] = entry
         check(s, want_status=want)
+
+
+@gpu
+@pytest.mark.parametrize("D,hole", [(40, False), (40, True), (128, False), (128, True)])
+def test_a_length_far_behind_the_table(D, hole):
+    """Every row sees what the table holds; nothing walks the 2^31 positions
+    behind it, which would take seconds (a hole has rows recomputed)."""
+    from speculative_decoding_verification_75_gb300 import api
+    s = build(np.random.default_rng(D), 2, 3, 8, 2, D, 16, [61, 61], None, "chain", "bf16", "bf16")
+    s["tables"] = s["tables"][:, :4].copy()
+    want = api.SV_KV_TABLE_SHORT
+    if hole:
+        s["tables"][0, 1] = -1
+        want |= api.SV_KV_MISSING_BLOCK
+    s["L"] = [64, 64]
+    check(s, want_status=want)
+    near = call(s)
+    s["L"] = [2 ** 31 - 100, 2 ** 31 - 4]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    far = call(s, status=status)
+    end.record()
+    assert torch.equal(far, near) and status.item() == want
+    assert begin.elapsed_time(end) < 100
