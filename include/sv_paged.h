@@ -186,8 +186,9 @@ typedef struct {
 } sv_tree_attention_args;
 SV_API sv_status sv_tree_attention(const sv_tree_attention_args *args, sv_stream_t stream);
 
-/* Workspace of sv_tree_attention for batches up to these sizes (the cache's
- * type and block size do not matter); 0 for invalid sizes. */
+/* Workspace of sv_tree_attention: what it returns serves every smaller B, T,
+ * num_heads and head_dim, and more KV heads (the cache's type and block size do
+ * not matter); 0 for invalid sizes. */
 SV_API size_t sv_tree_attention_workspace_bytes(int64_t B, int64_t T, int64_t num_heads,
                                                 int64_t num_kv_heads, int64_t head_dim);
 

@@ -134,7 +134,8 @@ def kv_compact(path: torch.Tensor, num_accepted: torch.Tensor, seq_lens: torch.T
 
 def tree_attention_workspace_bytes(B: int, T: int, num_heads: int, num_kv_heads: int,
                                    head_dim: int) -> int:
-    """Bytes of workspace ``tree_attention`` needs for batches of these sizes."""
+    """Bytes of workspace ``tree_attention`` needs for batches of up to B
+    requests and T new tokens."""
     return int(_api.load_library().sv_tree_attention_workspace_bytes(
         B, T, num_heads, num_kv_heads, head_dim))
 

@@ -290,7 +290,10 @@ TcLayout tc_layout(int64_t T, int64_t G, int64_t D) {
   w.MP = static_cast<int>(std::max<int64_t>((T + unit - 1) / unit, 1));
   w.slot_rows = pair ? 2 * kTile
                      : static_cast<int>(up(std::min<int64_t>(std::max<int64_t>(T * G, 1), kTile), 32));
-  w.slot_floats = static_cast<int>(up((D + 2) * w.slot_rows + 1, 32));
+  // A pair's slot is two of a full single tile: a workspace for many tokens
+  // serves few ones too.
+  const auto slot = [&](int rows) { return static_cast<int>(up((D + 2) * rows + 1, 32)); };
+  w.slot_floats = pair ? 2 * slot(kTile) : slot(w.slot_rows);
   w.cuts = 0;
   w.err = up(2 * kMaxGrid * sizeof(Cut), 256);
   w.slots = w.err + 256;

@@ -284,3 +284,34 @@ def test_a_length_far_behind_the_table(D, hole):
     end.record()
     assert torch.equal(far, near) and status.item() == want
     assert begin.elapsed_time(end) < 100
+
+
+# ------------------------------------------------------------- workspace ----
+
+def test_a_workspace_serves_every_smaller_batch():
+    from speculative_decoding_verification_75_gb300 import kv
+    n = kv.tree_attention_workspace_bytes
+    for Hkv in (1, 2, 7, 8):
+        for G in (1, 2, 3, 4, 7, 8, 16, 100, 128, 130):
+            for D in (8, 64, 128, 256):
+                by_T = [n(4, T, G * Hkv, Hkv, D) for T in (*range(1, 140), 1000)]
+                assert by_T == sorted(by_T)
+    for T in (1, 2, 3, 16, 17, 64, 65, 128, 129):
+        by_heads = [n(4, T, 8 * G, 8, 128) for G in range(1, 140)]
+        assert by_heads == sorted(by_heads)
+        by_kv_heads = [n(4, T, 64, Hkv, 128) for Hkv in (64, 32, 16, 8, 4, 2, 1)]
+        assert by_kv_heads == sorted(by_kv_heads)
+        by_D = [n(4, T, 32, 8, D) for D in range(8, 257, 8)]
+        assert by_D == sorted(by_D)
+        assert len({n(B, T, 32, 8, 128) for B in (1, 2, 100, 5000)}) == 1
+
+
+@gpu
+@pytest.mark.parametrize("cdt", ["bf16", "e4m3"])
+def test_one_workspace_for_steps_of_all_sizes(cdt):
+    from speculative_decoding_verification_75_gb300 import kv
+    ws = torch.empty(kv.tree_attention_workspace_bytes(2, 64, 16, 2, 128), dtype=torch.uint8, device=DEV)
+    for T in (64, 16, 17, 15, 1, 33):            # 16 tokens are one tile, 17 a pair
+        ws.fill_(0xA5)
+        check(build(np.random.default_rng(T), 2, T, 16, 2, 128, 16, [3000, 10], None, "chain", "bf16", cdt),
+              workspace=ws)
