@@ -919,6 +919,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
         seg_bad[rs][w.seg % kSegRing] = w.seg + 1;
         x.id = 0;
       }
+      __syncwarp();  // the mark before the elected lane's arrival on the stage's barrier
     };
     // A tile's K or V into the next stage.
     int st = grp, round = 0;                 // of the next position

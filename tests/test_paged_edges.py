@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import paged_ref as ref
-from test_paged_kv import DEV, F8, TD, i32
+from test_paged_kv import DEV, F8, i32
 from test_tree_attention import UNIT, build, call, check
 
 gpu = pytest.mark.gpu
@@ -136,6 +136,18 @@ def test_a_marked_unit_of_a_long_context_holds_up_nobody():
         t = 1.01 * (t + S * 2.0 ** -32 * V0.abs().max() / l)
         fine = ~o.isnan()
         assert ((out[b].double() - o).abs()[fine] <= t[fine]).all()
+
+
+@gpu
+@pytest.mark.parametrize("T", [2, 20])
+@pytest.mark.parametrize("cdt", ["bf16", "e4m3"])
+def test_a_missing_block_at_any_place_of_a_tile(T, cdt):
+    """Eight blocks to a tile, each looked up by another lane: the mark of one
+    that is missing reaches the warps that store the rows."""
+    for j in range((140 + T + 7) // 8):
+        s = build(np.random.default_rng(j), 1, T, 8, 1, 64, 8, [140], None, "chain", "bf16", cdt)
+        s["tables"][0, j] = -1
+        check(s, want_status=ref.MISSING)
 
 
 # ---------------------------------------------------------------- scales ----
