@@ -70,6 +70,7 @@ enum { SV_F16 = 2, SV_E4M3 = 3 };
 
 #define SV_KV_GROUP 32        /* elements that share a scale byte */
 #define SV_KV_MAX_HEAD_DIM 256
+#define SV_ATTN_MAX_KEYS 0x7ffff000  /* positions of a table, for attention */
 
 /* Every field is 8 bytes wide. */
 typedef struct {
@@ -163,8 +164,8 @@ SV_API sv_status sv_kv_compact(const sv_kv_compact_args *args, sv_stream_t strea
  *   workspace sv_tree_attention_workspace_bytes() bytes, 256-byte aligned, no
  *             initialisation needed; calls that share one are ordered on one
  *             stream.
- * head_dim is a multiple of 8 (of 32 for SV_E4M3), at most 256.  Statistics
- * and sums are fp32; probabilities may be rounded to the query's type, over an
+ * head_dim is a multiple of 8 (of 32 for SV_E4M3), at most 256, and max_blocks *
+ * block_size at most SV_ATTN_MAX_KEYS.  Statistics and sums are fp32; probabilities may be rounded to the query's type, over an
  * e4m3 cache to fp16, before their product with v.  A bounded wait that gives
  * up sets SV_FAULT_TIMEOUT in `status`.  Results are deterministic.
  */

@@ -404,7 +404,8 @@ sv_status tree_attention(const sv_tree_attention_args *a, sv_stream_t stream) {
   AttnParams p = {};
   if (const sv_status s = take_cache(a->cache, a->B, false, p.c)) return s;
   if (a->cache.dtype != SV_E4M3 && a->cache.dtype != a->dtype) return SV_ERR_UNSUPPORTED_DTYPE;
-  if (!attn_sizes_ok(a->B, a->T, a->num_heads, p.c.heads, p.c.D) || !std::isfinite(a->scale))
+  if (!attn_sizes_ok(a->B, a->T, a->num_heads, p.c.heads, p.c.D) || !std::isfinite(a->scale) ||
+      a->cache.max_blocks * a->cache.block_size > SV_ATTN_MAX_KEYS)  // a tile of keys ends below 2^31
     return SV_ERR_INVALID_ARG;
   const double sl2 = a->scale * 1.4426950408889634;
   if (std::fabs(sl2) > 3.4e38) return SV_ERR_INVALID_ARG;

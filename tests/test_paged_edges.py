@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import paged_ref as ref
-from test_paged_kv import DEV, F8, i32
+from test_paged_kv import _attn, _cache_words, _write, DEV, F8, i32
 from test_tree_attention import UNIT, build, call, check
 
 gpu = pytest.mark.gpu
@@ -327,3 +327,18 @@ def test_one_workspace_for_steps_of_all_sizes(cdt):
         ws.fill_(0xA5)
         check(build(np.random.default_rng(T), 2, T, 16, 2, 128, 16, [3000, 10], None, "chain", "bf16", cdt),
               workspace=ws)
+
+
+# -------------------------------------------------------------- refusals ----
+
+def test_a_table_of_2_31_positions_is_refused_by_attention():
+    """Within the last tile below 2^31 the kernel's positions would overflow."""
+    from speculative_decoding_verification_75_gb300 import api, kv
+    lib = api.load_library()
+    for bs, blocks in ((65528, 32772), (1 << 20, 2047), (1, 2 ** 31 - 1), (1, 2 ** 31 - 4095)):
+        cache = _cache_words(bs=bs, max_blocks=blocks, block=2 * bs * 64)
+        assert (bs * blocks > 0x7ffff000) == (bs != 1 << 20)
+        # Nothing is launched for an empty batch; its sizes are checked.
+        want = api.SV_ERR_INVALID_ARG if bs * blocks > 0x7ffff000 else api.SV_OK
+        assert _attn(lib, kv, cache, B=0) == want
+        assert _write(lib, kv, cache, B=0) == api.SV_OK
