@@ -510,7 +510,6 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   __shared__ Walk sh_walk[S::kStreams];
   __shared__ int seg_bad[S::kStreams][kSegRing];  // holds 1 + a marked segment's number
   __shared__ uint32_t marks[S::kStreams][kMarkBits / 32];  // whole units to recompute
-  __shared__ int marked[S::kStreams];                      // whether there are any
   // kRaw: scale bytes that a K tile, and (plus 256) a segment's V, refer to.
   __shared__ int k_scale[S::kStreams][kScaleRing], v_scale[S::kStreams][kSegRing];
 
@@ -552,10 +551,8 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
     sv::fence_mbar_init();
   }
   if (warp == 3) {
-    for (int s = 0; s < S::kStreams; ++s) {
+    for (int s = 0; s < S::kStreams; ++s)
       for (int i = lane; i < kMarkBits / 32; i += 32) marks[s][i] = 0;
-      if (lane == 0) marked[s] = 0;
-    }
   }
   if (tid == 32) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.kmap) : "memory");
@@ -579,7 +576,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   // Where this block's ranges begin: one warp each finds out, all start there.
   const int upt = p.TT * S::kTilesPerUnit;
   uint32_t *const err = p.err;
-  bool ok = true;
+  bool ok = true, marked = false;
   if (warp >= 8 && warp - 8 < S::kStreams) {
     const int i = static_cast<int>(blockIdx.x + (warp - 8) * gridDim.x);
     Walk w;
@@ -834,7 +831,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       }
       if (bad && whole && boss) {
         marks[rs][seg / 32 % (kMarkBits / 32)] |= 1u << (seg % 32);
-        marked[rs] = 1;
+        marked = true;
       }
       __syncwarp();
       if (active && !bad) {
@@ -1323,13 +1320,14 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
   }
 
   tc_fence_before();
-  __syncthreads();
+  const bool some = __syncthreads_or(marked);
   tc_fence_after();
   if (warp == 11) tc_dealloc(tmem, 512);
-
+  if (some) {
 #pragma unroll 1
-  for (int rs = 0; rs < S::kStreams; ++rs)
-    if (marked[rs]) recompute_marked<Q, C, D>(a, upt, sh_walk[rs], marks[rs], warp, S::kWarps);
+    for (int rs = 0; rs < S::kStreams; ++rs)
+      recompute_marked<Q, C, D>(a, upt, sh_walk[rs], marks[rs], warp, S::kWarps);
+  }
 }
 
 // ---------------------------------------------------------- second kernel ----
