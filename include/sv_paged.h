@@ -25,6 +25,7 @@
  * SV_BF16, SV_F16, or SV_E4M3 with one scale byte s per 32 elements of
  * head_dim (k_scale, v_scale: [num_layers][num_blocks][num_kv_heads]
  * [block_size][head_dim / 32], E8M0: value = code * 2^(s - 127), 255 is NaN).
+ * k and v do not overlap, or are one array for both, as are then the scales.
  * k, v and the scales start on 16-byte boundaries; block_stride and
  * layer_stride in bytes, scale_block_stride and scale_layer_stride are
  * multiples of 16 where they are used.
@@ -92,7 +93,8 @@ typedef struct {
  *   other strides free (in elements: a view of a fused projection).
  * head_dim is a multiple of 8 (of 32 for SV_E4M3), at most 256.  No two
  * positions written by one call may share a cache row (two requests that
- * share a block hold it below both of their L).
+ * share a block hold it below both of their L).  Where k and v are one array,
+ * so are key and value.
  */
 typedef struct {
     uint64_t struct_bytes;        /* sizeof(sv_kv_write_args) */
@@ -108,7 +110,8 @@ SV_API sv_status sv_kv_write(const sv_kv_write_args *args, sv_stream_t stream);
 /*
  * Cached tokens as dense tensors: positions starts[b] + i (NULL: i) for
  * i < lens[b] go to key[b, i], value[b, i] ([B, T, num_kv_heads, head_dim] of
- * `dtype`: SV_BF16, SV_F16 or SV_F32, strides as in sv_kv_write).  Values of
+ * `dtype`: SV_BF16, SV_F16 or SV_F32, strides as in sv_kv_write; two tensors
+ * that do not overlap).  Values of
  * an e4m3 cache are code * 2^(s-127) rounded to `dtype`, to nearest.
  */
 typedef struct {

@@ -87,6 +87,12 @@ bool take_strides(const int64_t (&s)[3], int esz, int64_t &b, int64_t &t, int64_
   return true;
 }
 
+// Whether k and v are one array; false where their scales say otherwise.
+bool one_array(const Cache &c, bool &same) {
+  same = c.num_blocks > 0 && c.k == c.v;
+  return !c.ks || c.num_blocks == 0 || (c.ks == c.vs) == same;
+}
+
 bool batch_ok(int64_t B, int64_t T) {
   return B >= 0 && T >= 0 && B <= INT_MAX && T <= INT_MAX && (B == 0 || T <= INT_MAX / B);
 }
@@ -140,6 +146,10 @@ sv_status kv_write(const sv_kv_write_args *a, sv_stream_t stream) {
   if (const sv_status s = take_move(p, a->key, a->value, a->key_stride, a->value_stride, a->B,
                                     a->T, 2, grid))
     return s;
+  bool same;
+  if (!one_array(p.c, same) ||
+      (same && (p.key != p.value || p.ksb != p.vsb || p.kst != p.vst || p.ksh != p.vsh)))
+    return SV_ERR_INVALID_ARG;
   if (a->cache.dtype != SV_E4M3)  // a copy: the two 16-bit types are one
     return launch(sv_kv_write_kernel<BF16, BF16>, grid, kMoveThreads, 0, stream, p);
   return a->dtype == SV_BF16
@@ -168,6 +178,7 @@ sv_status kv_read(const sv_kv_read_args *a, sv_stream_t stream) {
   if (const sv_status s = take_move(p, a->key, a->value, a->key_stride, a->value_stride, a->B,
                                     a->T, elem_bytes(a->dtype), grid))
     return s;
+  if (p.key == p.value) return SV_ERR_INVALID_ARG;
   if (a->cache.dtype == SV_BF16) return read_as<BF16>(a->dtype, grid, stream, p);
   if (a->cache.dtype == SV_F16) return read_as<F16>(a->dtype, grid, stream, p);
   return read_as<E4M3>(a->dtype, grid, stream, p);
@@ -186,7 +197,10 @@ sv_status kv_compact(const sv_kv_compact_args *a, sv_stream_t stream) {
   p.P = static_cast<int>(a->P);
   p.esz = elem_bytes(a->cache.dtype);
   p.status = a->status;
-  const int64_t units = 2ll * p.c.heads * (p.c.D * p.esz / 16 + (p.esz == 1 ? p.c.D / SV_KV_GROUP : 0));
+  bool same;
+  if (!one_array(p.c, same)) return SV_ERR_INVALID_ARG;
+  p.sides = same ? 1 : 2;
+  const int64_t units = static_cast<int64_t>(p.sides) * p.c.heads * (p.c.D * p.esz / 16 + (p.esz == 1 ? p.c.D / SV_KV_GROUP : 0));
   // As many layers to a block as make all blocks run at once, four to an SM.
   const int64_t gy = (units + kMoveThreads - 1) / kMoveThreads;
   p.layers = static_cast<int>(std::max<int64_t>(

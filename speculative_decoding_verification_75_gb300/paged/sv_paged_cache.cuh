@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_read_kernel(const MovePara
 struct CompactParams {
   Cache c;
   const int32_t *path, *num_accepted, *seq_lens;
-  int B, P, esz;
+  int B, P, esz, sides;  // sides: 1 where k and v are one array
   int layers, groups;  // layers of a thread block, groups of them
   uint32_t *status;
 };
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) sv_kv_compact_kernel(const Co
   const int row_bytes = p.c.D * p.esz, per_head = row_bytes / 16, per_side = p.c.heads * per_head;
   const int srow = p.esz == 1 ? p.c.D / SV_KV_GROUP : 0, sper_side = p.c.heads * srow;
   const int u = blockIdx.y * kMoveThreads + threadIdx.x;
-  const bool data = u < 2 * per_side, scales = !data && u - 2 * per_side < 2 * sper_side;
+  const bool data = u < p.sides * per_side, scales = !data && u - p.sides * per_side < p.sides * sper_side;
   uint8_t *base = nullptr;
   if (data) {
     const bool is_v = u >= per_side;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) sv_kv_compact_kernel(const Co
     base = (is_v ? p.c.v : p.c.k) +
            static_cast<int64_t>(h) * p.c.bs * row_bytes + (cc - h * per_head) * 16;
   } else if (scales) {
-    const int s = u - 2 * per_side;
+    const int s = u - p.sides * per_side;
     const bool is_v = s >= sper_side;
     const int cc = s - (is_v ? sper_side : 0), h = cc / srow;
     base = (is_v ? p.c.vs : p.c.ks) +

@@ -9,7 +9,8 @@ import pytest
 import torch
 
 import paged_ref as ref
-from test_paged_kv import _attn, _cache_words, _write, DEV, F8, i32
+from test_paged_kv import (DEV, F8, TD, PTR, _attn, _cache_words, _compact, _read, _write, bits,
+                           compact_reference, i32, make_cache, make_tables)
 from test_tree_attention import UNIT, build, call, check
 
 gpu = pytest.mark.gpu
@@ -342,3 +343,33 @@ def test_a_table_of_2_31_positions_is_refused_by_attention():
         want = api.SV_ERR_INVALID_ARG if bs * blocks > 0x7ffff000 else api.SV_OK
         assert _attn(lib, kv, cache, B=0) == want
         assert _write(lib, kv, cache, B=0) == api.SV_OK
+
+
+def test_two_results_in_one_place_are_refused():
+    from speculative_decoding_verification_75_gb300 import api, kv
+    lib, bad = api.load_library(), api.SV_ERR_INVALID_ARG
+    assert _read(lib, kv, _cache_words(v=2 * PTR)) == bad               # key and value in one tensor
+    assert _write(lib, kv, _cache_words(), value=2 * PTR) == bad        # k and v in one cache
+    assert _write(lib, kv, _cache_words(), vt=256) == bad
+    f8 = dict(dtype=3, block=2048, sblock=64)
+    for call in (_write, _compact):
+        assert call(lib, kv, _cache_words(v=2 * PTR, ks=PTR, vs=PTR, **f8)) == bad
+        assert call(lib, kv, _cache_words(ks=PTR, vs=2 * PTR, **f8)) == bad
+
+
+@gpu
+@pytest.mark.parametrize("B,H,D,bs,P,cdt", [(3, 8, 128, 16, 9, "bf16"), (2, 33, 256, 4, 70, "e4m3"), (1, 1, 32, 5, 200, "e4m3")])
+def test_compact_where_keys_and_values_are_one_array(B, H, D, bs, P, cdt):
+    import speculative_decoding_verification_75_gb300 as sv
+    rng = np.random.default_rng(P)
+    L = rng.integers(0, 3 * bs, B)
+    path = np.stack([np.sort(rng.permutation(2 * P)[:P]) for _ in range(B)])
+    need = [-(-(int(x) + 2 * P) // bs) for x in L]
+    tables = make_tables(rng, need, sum(need) + 1, max(need))
+    c, _, s, _ = make_cache(rng, sum(need) + 1, H, bs, D, TD[cdt], layers=2)
+    want = compact_reference([bits(x).copy() for x in (c, s) if x is not None], tables, bs, path, [P] * B, L)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    sv.kv_compact(i32(path), i32([P] * B), i32(L), i32(tables), c, c, k_scale=s, v_scale=s, status=status)
+    assert status.item() == 0
+    for x, w in zip((c, s), want):
+        assert np.array_equal(bits(x), w)
