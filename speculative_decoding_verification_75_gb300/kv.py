@@ -1,6 +1,6 @@
 """Python binding of the paged-cache operators (``include/sv_paged.h``).
 
-Argument marshalling only, in a small native module (``lib/_svkv``): shapes
+Argument marshalling only, in a small native module (``lib/_svkv.*.so``): shapes
 and types are checked there, sizes and alignments by the library, and the work
 is done by its CUDA kernels on the current (or given) stream.
 
@@ -41,10 +41,10 @@ def load_binding():
     global _native
     if _native is None:
         lib = _api.load_library()
-        path = _build.BINDING
+        path = _build.binding_path()
         if not path.exists():
             raise RuntimeError(
-                f"{path} is not built: run `python -m "
+                f"{path} is not built (for this Python and PyTorch): run `python -m "
                 "speculative_decoding_verification_75_gb300.build`")
         loader = importlib.machinery.ExtensionFileLoader("_svkv", str(path))
         mod = importlib.util.module_from_spec(
