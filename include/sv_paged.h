@@ -16,6 +16,10 @@
  *   sv_kv_compact      the entries of an accepted tree path move together;
  *   sv_kv_rollback     cuts the sequence behind them (spec_verify.h);
  *   sv_kv_read         reads a sequence back as dense tensors.
+ * The entries to keep are those of the last emitted token and of the accepted
+ * drafts: where both were written in the step, sv_kv_compact and sv_kv_rollback
+ * take spec_verify's num_accepted + 1 (0 for a request that it marked invalid),
+ * and sv_kv_rollback's draft_lens are the new tokens, n.
  *
  * The cache.  k and v are arrays [num_layers][num_blocks][num_kv_heads]
  * [block_size][head_dim]; the innermost three dimensions are dense, blocks
@@ -128,10 +132,11 @@ SV_API sv_status sv_kv_read(const sv_kv_read_args *args, sv_stream_t stream);
 /*
  * The accepted path of a tree, moved together in every layer: for i < k =
  * num_accepted[b] the entry at position seq_lens[b] + path[b, i] moves to
- * seq_lens[b] + i.  path [B, P] holds strictly increasing node numbers (a
- * parent is numbered before its children), so path[b, i] >= i; entries at
- * i >= k are not read.  k < 0 (a request that spec_verify marked invalid)
- * moves nothing, k > P is SV_KV_BAD_LENGTH.  seq_lens is not changed:
+ * seq_lens[b] + i.  k counts entries: the accepted drafts and, where it is the
+ * tree's node 0, the last emitted token.  path [B, P] holds strictly increasing
+ * node numbers (a parent is numbered before its children), so path[b, i] >= i;
+ * entries at i >= k are not read.  k <= 0 moves nothing, k > P is
+ * SV_KV_BAD_LENGTH.  seq_lens is not changed:
  * sv_kv_rollback does that.  Rows that are read or written must belong to one
  * request alone.
  */

@@ -121,10 +121,12 @@ def kv_compact(path: torch.Tensor, num_accepted: torch.Tensor, seq_lens: torch.T
     ``sv_kv_compact``: position seq_lens[b] + path[b, i] goes to seq_lens[b] +
     i for i < num_accepted[b].
 
-    path [B, P] int32, strictly increasing per request.  The caches (and
+    path [B, P] int32, strictly increasing per request.  num_accepted [B] int32
+    counts the entries to keep: where the last emitted token was written with the
+    drafts, as node 0, that is ``verify``'s num_accepted + 1.  The caches (and
     scales) may have a layers dimension in front: one call then moves every
-    layer.  ``kv_rollback`` with the same num_accepted cuts the sequence
-    afterwards."""
+    layer.  ``kv_rollback`` with the same count cuts the sequence afterwards
+    (its draft_lens: the new tokens, the emitted one among them)."""
     rc = (_native or load_binding()).kv_compact(
         path, num_accepted, seq_lens, block_tables, k_cache, v_cache, k_scale, v_scale, status,
         None if stream is None else stream.cuda_stream)

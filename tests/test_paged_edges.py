@@ -3,6 +3,7 @@ units with other requests behind them, rows without a finite score, powers of
 two at the ends of their range, lengths far behind the table, and one workspace
 for all sizes."""
 import math
+from pathlib import Path
 
 import numpy as np
 import pytest
@@ -373,3 +374,34 @@ def test_compact_where_keys_and_values_are_one_array(B, H, D, bs, P, cdt):
     assert status.item() == 0
     for x, w in zip((c, s), want):
         assert np.array_equal(bits(x), w)
+
+
+# --------------------------------------------------------------- a step ----
+
+@gpu
+def test_the_step_of_the_readme_keeps_every_token():
+    """The step as README.md spells it out, on ragged batches: the sequences
+    read back are the committed tokens, the emitted one and the accepted drafts."""
+    readme = (Path(__file__).resolve().parents[1] / "README.md").read_text()
+    code = next(b for b in readme.split("```python")[1:] if "kv_compact" in b).split("```")[0]
+    rng = np.random.default_rng(17)
+    B, T, H, D, block_size, n = 4, 6, 2, 64, 4, 30
+    L, new, accepted = [0, 7, 20, 3], [6, 1, 4, 6], [3, 0, -1, 5]
+    nodes = [[0, 2, 3, 5, -1, -1], [0, -1, -1, -1, -1, -1], [-1] * 6, [0, 1, 2, 3, 4, 5]]
+    k, v = (torch.from_numpy(rng.standard_normal((B, 30, H, D))).bfloat16().to(DEV) for _ in range(2))
+    k_cache, v_cache = (torch.zeros(40, H, block_size, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    tables = make_tables(rng, [-(-(a + b) // block_size) for a, b in zip(L, new)], 40, 8)
+    space = dict(k_cache=k_cache, v_cache=v_cache, block_tables=i32(tables), seq_lens=i32(L), new_lens=i32(new),
+                 block_size=block_size, T=T, n=n, tree_mask=None, path=i32(nodes), num_accepted=i32(accepted),
+                 query=torch.zeros(B, T, 2 * H, D, dtype=torch.bfloat16, device=DEV),
+                 free_list=i32([-1] * 40), free_count=i32([0]))
+    import speculative_decoding_verification_75_gb300 as sv
+    sv.kv_write(k, v, k_cache, v_cache, space["block_tables"], i32([0] * B), i32(L))   # committed tokens
+    space["key"], space["value"] = (torch.stack([x[b, l:l + T] for b, l in enumerate(L)]) for x in (k, v))
+    exec(code, space)
+    kept = [a + 1 for a in accepted]
+    assert space["seq_lens"].tolist() == [l + m for l, m in zip(L, kept)]
+    for got, x in ((space["keys"], k), (space["values"], v)):
+        for b, l in enumerate(L):
+            want = torch.cat([x[b, :l], x[b, [l + j for j in nodes[b][:kept[b]]]]])
+            assert torch.equal(got[b, :l + kept[b]], want) and not got[b, l + kept[b]:].any()
