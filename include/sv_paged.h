@@ -136,8 +136,7 @@ SV_API sv_status sv_kv_read(const sv_kv_read_args *args, sv_stream_t stream);
  * tree's node 0, the last emitted token.  path [B, P] holds strictly increasing
  * node numbers (a parent is numbered before its children), so path[b, i] >= i;
  * entries at i >= k are not read.  k <= 0 moves nothing, k > P is
- * SV_KV_BAD_LENGTH.  seq_lens is not changed:
- * sv_kv_rollback does that.  Rows that are read or written must belong to one
+ * SV_KV_BAD_LENGTH.  seq_lens is not changed: sv_kv_rollback does that.  Rows that are read or written must belong to one
  * request alone.
  */
 typedef struct {
@@ -173,9 +172,18 @@ SV_API sv_status sv_kv_compact(const sv_kv_compact_args *args, sv_stream_t strea
  *             initialisation needed; calls that share one are ordered on one
  *             stream.
  * head_dim is a multiple of 8 (of 32 for SV_E4M3), at most 256, and max_blocks *
- * block_size at most SV_ATTN_MAX_KEYS.  Statistics and sums are fp32; probabilities may be rounded to the query's type, over an
- * e4m3 cache to fp16, before their product with v.  A bounded wait that gives
- * up sets SV_FAULT_TIMEOUT in `status`.  Results are deterministic.
+ * block_size at most SV_ATTN_MAX_KEYS.  Statistics and sums are fp32;
+ * probabilities may be rounded to the query's type, over an e4m3 cache to fp16,
+ * before their product with v; over an e4m3 cache elements of a bf16 query row
+ * below 2^-31 of its largest may lose bits.  A bounded wait that gives up sets
+ * SV_FAULT_TIMEOUT in `status`.  Results are deterministic.
+ *
+ * Fast for head_dim 64 and 128, block_size a multiple of 8 and query rows on
+ * 16-byte boundaries; other batches take 25 to 200 times as long.  Rows of one
+ * KV head and request (128 or 256 at a time) are computed at that rate too where
+ * one of their blocks is missing, a new token's value is not finite, or, e4m3,
+ * scales lie further apart than 2^15 (k: of 64 keys, v: below the first ones',
+ * or 2^7 above); zeros with s = 7, as sv_kv_write leaves them, do not count.
  */
 typedef struct {
     uint64_t struct_bytes;

@@ -168,7 +168,11 @@ def tree_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     new ``out`` is not initialised).  ``lse`` [B, T, heads] fp32 receives the
     log of the softmax denominators.  ``workspace``: a uint8 tensor of
     ``tree_attention_workspace_bytes`` on a 256-byte boundary, allocated per
-    call if None; calls that share one must be ordered on one stream."""
+    call if None; calls that share one must be ordered on one stream.
+
+    Fast for head dims 64 and 128, block sizes that are a multiple of 8 and
+    query rows on 16-byte boundaries.  Like the other operators here it is not
+    differentiable."""
     rc, out = (_native or load_binding()).tree_attention(
         query, k_cache, v_cache, block_tables, seq_lens, tree_mask, new_lens, scale, k_scale,
         v_scale, out, lse, workspace, status, None if stream is None else stream.cuda_stream)

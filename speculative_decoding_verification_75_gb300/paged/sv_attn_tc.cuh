@@ -36,19 +36,21 @@
 // Rows of V behind the last token are zeroed in shared memory, because
 // 0 * garbage may be NaN; a value that is not finite among the new tokens, or a
 // missing block, marks the unit, which is recomputed row by row
-// (sv_attn_general.cuh).
+// (sv_attn_general.cuh): by the second kernel if it is cut, else when the
+// block's ranges are done.
 //
 // Measured, both kernels together:
-//   131071 keys, 1 token, 64 heads on 8 of 128   93 us, 5.8 TB/s: HBM; 8 us are
+//   131071 keys, 1 token, 64 heads on 8 of 128   92 us, 5.8 TB/s: HBM; 8 us are
 //                                                the join and the first tiles
-//   32 x 9 tokens, 32 heads on 32, 200-2000 keys 115 us, 5.1 TB/s: HBM, and the
+//   32 x 9 tokens, 32 heads on 32, 200-2000 keys 114 us, 5.1 TB/s: HBM, and the
 //                                                ends of units of few tiles
 //   8 x 6 tokens, 64 on 8, 1000-4000 keys        29 us, 2.9 TB/s: start, first
 //                                                data and join, 15 us together
-//   16 trees of 64, 32 on 8, 1000-8000 keys      102 us, 549 TFLOP/s: Q K^T at
-//                                                N = 64 is bound by its operands
-//                                                in shared memory; unit ends, join
-//   128 x 6 tokens, e4m3, 500-8000 keys          366 us, 3.2 TB/s: instructions
+//   16 trees of 64, 32 on 8, 1000-8000 keys      102 us, 547 TFLOP/s: unit ends,
+//                                                join; a step takes twice its
+//                                                products' time, with 64 keys a
+//                                                step and with 128
+//   128 x 6 tokens, e4m3, 500-8000 keys          363 us, 3.2 TB/s: instructions
 //                                                of the wideners and the softmax
 // The kernel's code is fetched by five roles at once: with the loops unrolled
 // further they missed the instruction cache (90 % hits, 423 us for the last case
