@@ -40,7 +40,7 @@ EXPORTS = ("sv_workspace_bytes", "spec_verify", "spec_verify_diag",
            "sv_last_error", "sv_status_string", "spec_verify_noalloc", "sv_kv_rollback",
            "sv_selftest_wait_timeout", "sv_set_small_batch_path",
            "sv_kv_write", "sv_kv_read", "sv_kv_compact", "sv_tree_attention",
-           "sv_tree_attention_workspace_bytes")
+           "sv_tree_attention_workspace_bytes", "sv_kv_reserve", "sv_qk_norm_rope")
 
 # Bits of the status word of sv_kv_rollback (include/spec_verify.h).
 SV_KV_FREE_LIST_FULL = 0x1
@@ -101,7 +101,8 @@ def load_library():
     lib.sv_selftest_wait_timeout.argtypes = [_P, _P, ctypes.c_uint, _P]
     lib.sv_kv_rollback.restype = _I
     lib.sv_kv_rollback.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _P, _P]
-    for name in ("sv_kv_write", "sv_kv_read", "sv_kv_compact", "sv_tree_attention"):
+    for name in ("sv_kv_write", "sv_kv_read", "sv_kv_compact", "sv_tree_attention",
+                 "sv_kv_reserve", "sv_qk_norm_rope"):
         fn = getattr(lib, name)
         fn.restype = _I
         fn.argtypes = [ctypes.c_char_p, _P]  # a packed argument struct, the stream

@@ -1,7 +1,7 @@
 """Build ``lib/libspecverify.so`` (the CUDA verification library) in-tree.
 
-Two translation units (the verification step, the paged KV cache), compiled
-in parallel for sm_103a only and linked, and beside them ``lib/_svkv.*.so``,
+Three translation units (the verification step, the paged KV cache, what a step
+does before its attention), compiled in parallel for sm_103a only and linked, and beside them ``lib/_svkv.*.so``,
 the native module of ``kv.py`` (plain C++ against the installed PyTorch).  The
 results are git-ignored; every machine that runs the library builds them from
 source.  The library needs nvcc alone: where the module cannot be built (no g++,
@@ -23,7 +23,7 @@ ROOT = PKG.parent
 SRC_DIR = PKG / "csrc"
 MAIN = SRC_DIR / "spec_verify.cu"
 PAGED_DIR = PKG / "paged"
-UNITS = [MAIN, PAGED_DIR / "sv_paged.cu"]
+UNITS = [MAIN, PAGED_DIR / "sv_paged.cu", PAGED_DIR / "sv_step.cu"]
 INCLUDE = ROOT / "include"
 LIB = PKG / "lib" / "libspecverify.so"
 BINDING_SRC = PAGED_DIR / "sv_paged_binding.cpp"

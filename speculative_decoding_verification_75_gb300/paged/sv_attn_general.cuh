@@ -46,7 +46,7 @@ template <typename C, int kMaxD, typename LoadQ>
 __device__ __forceinline__ void attend(const AttnParams &p, int b, int i, int h, int L, int n,
                                        int total, const LoadQ &load_q, int j0, int step, int lane,
                                        RowState<kMaxD> &r, uint32_t &st) {
-  const int D = p.c.D, row_bytes = D * C::kBytes, srow = D / SV_KV_GROUP;
+  const int D = p.c.D, row_bytes = D / 8 * C::kBits, srow = D / SV_KV_GROUP;
   const int64_t head_bytes = static_cast<int64_t>(h) * p.c.bs * row_bytes;
   const int64_t shead = static_cast<int64_t>(h) * p.c.bs * srow;
   const uint8_t *mrow =
@@ -67,20 +67,14 @@ __device__ __forceinline__ void attend(const AttnParams &p, int b, int i, int h,
     if (see) {
       x = 0.f;
       for (int d = 0; d < D; d += 8) {
-        uint4 raw;
-        if constexpr (C::kBytes == 1) {
-          const uint2 w = ld64(p.c.k + at + d);
-          raw = make_uint4(w.x, w.y, 0, 0);
-        } else {
-          raw = ld128(p.c.k + at + d * C::kBytes);
-        }
+        const uint4 raw = load8<C>(p.c.k + at + d / 8 * C::kBits);
         float f[8], q[8];
         unpack8<C>(&raw, f);
         load_q(d, q);
         float s8 = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) s8 = fmaf(q[e], f[e], s8);
-        if constexpr (C::kBytes == 1) s8 *= scale_value(ld8(p.c.ks + sat + d / SV_KV_GROUP));
+        if constexpr (C::kScaled) s8 *= scale_value<C>(ld8(p.c.ks + sat + d / SV_KV_GROUP));
         x += s8;
       }
     }
@@ -106,10 +100,13 @@ __device__ __forceinline__ void attend(const AttnParams &p, int b, int i, int h,
         const int d = lane + 32 * e;
         if (d < D) {
           float v;
-          if constexpr (C::kBytes == 1) {
+          if constexpr (C::kBits == 8) {
             const __half_raw hr = __nv_cvt_fp8_to_halfraw(
                 static_cast<__nv_fp8_storage_t>(ld8(p.c.v + vs + d)), __NV_E4M3);
-            v = __half2float(__half(hr)) * scale_value(ld8(p.c.vs + ss + d / SV_KV_GROUP));
+            v = __half2float(__half(hr)) * scale_value<C>(ld8(p.c.vs + ss + d / SV_KV_GROUP));
+          } else if constexpr (C::kBits == 4) {
+            const uint32_t code = ld8(p.c.v + vs + d / 2) >> (4 * (d & 1)) & 15u;
+            v = static_cast<float>(static_cast<int>(code) - 8) * scale_value<C>(ld8(p.c.vs + ss + d / SV_KV_GROUP));
           } else if constexpr (sizeof(typename C::raw) == 2) {
             const uint16_t w16 = static_cast<uint16_t>(ld16(p.c.v + vs + d * 2));
             v = load1<C>(&w16);

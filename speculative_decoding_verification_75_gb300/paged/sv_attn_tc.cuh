@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(Shape<Q, C, D, kPair>::kThreads, 1)
       if (S::kRaw && walk.on && !(ok = prepare_q(walk))) break;   // while the last products run
       if (!(ok = wait_warp(&bars.o_done[s][(tiles - 1) % kBufs], (tiles - 1) / kBufs, err))) break;
       tc_fence_after();
-      const float vs = S::kRaw ? scale_value(v_scale[rs][seg % kSegRing] & 255) : 1.f;
+      const float vs = S::kRaw ? scale_value<E4M3>(v_scale[rs][seg % kSegRing] & 255) : 1.f;
       const bool bad = seg_bad[rs][seg % kSegRing] == seg + 1;
       const bool whole = sg.t0 == 0 && sg.t1 == r.kt;
       const int base_row = kPair ? s * kTile : 0;            // of the slot

@@ -1,116 +1,13 @@
 // sv_paged.cu -- C ABI of the paged-cache operators (include/sv_paged.h):
 // argument checks, the choice of a kernel and the launches.
-#include <cuda_runtime.h>
-
-#include <algorithm>
-#include <atomic>
-#include <climits>
-#include <cmath>
-#include <cstdint>
-
 #include "sv_paged.h"
-#include "sv_paged_common.cuh"
+#include "sv_paged_host.cuh"
 #include "sv_paged_cache.cuh"
 #include "sv_attn_general.cuh"
 #include "sv_attn_tc.cuh"
 
 namespace svp {
 namespace {
-
-bool aligned(const void *p, uintptr_t a) {
-  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
-
-int elem_bytes(int64_t dtype) {
-  return dtype == SV_F32 ? 4 : dtype == SV_BF16 || dtype == SV_F16 ? 2 : dtype == SV_E4M3 ? 1 : 0;
-}
-
-constexpr int64_t kMaxStride = int64_t{1} << 46;  // elements; far past any memory
-
-// Checks a cache and its block tables (B rows) and lays it out in bytes.
-sv_status take_cache(const sv_kv_cache &c, int64_t B, bool layered, Cache &o) {
-  if (c.dtype != SV_BF16 && c.dtype != SV_F16 && c.dtype != SV_E4M3)
-    return SV_ERR_UNSUPPORTED_DTYPE;
-  const bool f8 = c.dtype == SV_E4M3;
-  const int64_t esz = elem_bytes(c.dtype);
-  if (c.num_blocks < 0 || c.num_blocks > INT_MAX || c.num_kv_heads < 1 ||
-      c.num_kv_heads > 65536 || c.block_size < 1 || c.block_size > (1 << 20) ||
-      c.head_dim < 8 || c.head_dim > SV_KV_MAX_HEAD_DIM || c.head_dim % (f8 ? 32 : 8) ||
-      c.num_layers < 1 || c.num_layers > (layered ? 65536 : 1) || c.max_blocks < 0 ||
-      c.max_blocks > INT_MAX)
-    return SV_ERR_INVALID_ARG;
-  const int64_t rows = c.num_kv_heads * c.block_size;
-  if (rows * c.head_dim > INT_MAX || c.max_blocks * c.block_size > INT_MAX) return SV_ERR_INVALID_ARG;
-  // A pool or a table may be empty (then every position is reported missing).
-  if ((c.num_blocks > 0 && (!c.k || !c.v || (f8 && (!c.k_scale || !c.v_scale)))) ||
-      (c.max_blocks > 0 && B > 0 && !c.block_tables))
-    return SV_ERR_INVALID_ARG;
-  if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.block_tables, 4)) return SV_ERR_INVALID_ARG;
-  const auto stride_ok = [](int64_t s, int64_t least, int64_t unit, bool used) {
-    return !used || (s >= least && s <= kMaxStride && s % unit == 0);
-  };
-  const bool many = c.num_blocks > 1, deep = c.num_layers > 1;
-  if (!stride_ok(c.block_stride, rows * c.head_dim, 16 / esz, many) ||
-      !stride_ok(c.layer_stride, rows * c.head_dim, 16 / esz, deep))
-    return SV_ERR_INVALID_ARG;
-  if (f8) {
-    if (!aligned(c.k_scale, 16) || !aligned(c.v_scale, 16) ||
-        !stride_ok(c.scale_block_stride, rows * c.head_dim / SV_KV_GROUP, 1, many) ||
-        !stride_ok(c.scale_layer_stride, rows * c.head_dim / SV_KV_GROUP, 1, deep))
-      return SV_ERR_INVALID_ARG;
-  }
-  o.k = static_cast<uint8_t *>(c.k);
-  o.v = static_cast<uint8_t *>(c.v);
-  o.ks = f8 ? c.k_scale : nullptr;
-  o.vs = f8 ? c.v_scale : nullptr;
-  o.block_bytes = many ? c.block_stride * esz : 0;
-  o.layer_bytes = deep ? c.layer_stride * esz : 0;
-  o.sblock_bytes = f8 && many ? c.scale_block_stride : 0;
-  o.slayer_bytes = f8 && deep ? c.scale_layer_stride : 0;
-  o.tables = c.block_tables;
-  o.num_layers = static_cast<int>(c.num_layers);
-  o.num_blocks = static_cast<int>(c.num_blocks);
-  o.heads = static_cast<int>(c.num_kv_heads);
-  o.bs = static_cast<int>(c.block_size);
-  o.D = static_cast<int>(c.head_dim);
-  o.max_blocks = static_cast<int>(c.max_blocks);
-  return SV_OK;
-}
-
-// Strides of a dense side [B, T, heads, D] with dense rows, in bytes.
-bool take_strides(const int64_t (&s)[3], int esz, int64_t &b, int64_t &t, int64_t &h) {
-  for (int64_t x : s)
-    if (x < 0 || x > kMaxStride) return false;
-  b = s[0] * esz;
-  t = s[1] * esz;
-  h = s[2] * esz;
-  return true;
-}
-
-// Whether k and v are one array; false where their scales say otherwise.
-bool one_array(const Cache &c, bool &same) {
-  same = c.num_blocks > 0 && c.k == c.v;
-  return !c.ks || c.num_blocks == 0 || (c.ks == c.vs) == same;
-}
-
-bool batch_ok(int64_t B, int64_t T) {
-  return B >= 0 && T >= 0 && B <= INT_MAX && T <= INT_MAX && (B == 0 || T <= INT_MAX / B);
-}
-
-template <typename K, typename... P>
-sv_status launch(K kernel, dim3 grid, int threads, size_t smem, sv_stream_t stream, const P &...p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p...) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
-}
 
 // The dense side of kv_write and kv_read and their grid.
 sv_status take_move(MoveParams &p, const void *key, const void *value, const int64_t (&ks)[3],
@@ -138,7 +35,7 @@ sv_status kv_write(const sv_kv_write_args *a, sv_stream_t stream) {
   if (a->dtype != SV_BF16 && a->dtype != SV_F16) return SV_ERR_UNSUPPORTED_DTYPE;
   MoveParams p = {};
   if (const sv_status s = take_cache(a->cache, a->B, false, p.c)) return s;
-  if (a->cache.dtype != SV_E4M3 && a->cache.dtype != a->dtype) return SV_ERR_UNSUPPORTED_DTYPE;
+  if (!scaled(a->cache.dtype) && a->cache.dtype != a->dtype) return SV_ERR_UNSUPPORTED_DTYPE;
   if (a->B == 0 || a->T == 0) return SV_OK;
   if (!a->seq_lens) return SV_ERR_INVALID_ARG;
   p.bt = Batch{a->seq_lens, a->new_lens, static_cast<int>(a->B), static_cast<int>(a->T), a->status};
@@ -150,8 +47,12 @@ sv_status kv_write(const sv_kv_write_args *a, sv_stream_t stream) {
   if (!one_array(p.c, same) ||
       (same && (p.key != p.value || p.ksb != p.vsb || p.kst != p.vst || p.ksh != p.vsh)))
     return SV_ERR_INVALID_ARG;
-  if (a->cache.dtype != SV_E4M3)  // a copy: the two 16-bit types are one
+  if (!scaled(a->cache.dtype))  // a copy: the two 16-bit types are one
     return launch(sv_kv_write_kernel<BF16, BF16>, grid, kMoveThreads, 0, stream, p);
+  if (a->cache.dtype == SV_I4)
+    return a->dtype == SV_BF16
+               ? launch(sv_kv_write_kernel<BF16, I4>, grid, kMoveThreads, 0, stream, p)
+               : launch(sv_kv_write_kernel<F16, I4>, grid, kMoveThreads, 0, stream, p);
   return a->dtype == SV_BF16
              ? launch(sv_kv_write_kernel<BF16, E4M3>, grid, kMoveThreads, 0, stream, p)
              : launch(sv_kv_write_kernel<F16, E4M3>, grid, kMoveThreads, 0, stream, p);
@@ -181,6 +82,7 @@ sv_status kv_read(const sv_kv_read_args *a, sv_stream_t stream) {
   if (p.key == p.value) return SV_ERR_INVALID_ARG;
   if (a->cache.dtype == SV_BF16) return read_as<BF16>(a->dtype, grid, stream, p);
   if (a->cache.dtype == SV_F16) return read_as<F16>(a->dtype, grid, stream, p);
+  if (a->cache.dtype == SV_I4) return read_as<I4>(a->dtype, grid, stream, p);
   return read_as<E4M3>(a->dtype, grid, stream, p);
 }
 
@@ -195,12 +97,12 @@ sv_status kv_compact(const sv_kv_compact_args *a, sv_stream_t stream) {
   p.seq_lens = a->seq_lens;
   p.B = static_cast<int>(a->B);
   p.P = static_cast<int>(a->P);
-  p.esz = elem_bytes(a->cache.dtype);
+  p.bits = cache_bits(a->cache.dtype);
   p.status = a->status;
   bool same;
   if (!one_array(p.c, same)) return SV_ERR_INVALID_ARG;
   p.sides = same ? 1 : 2;
-  const int64_t units = static_cast<int64_t>(p.sides) * p.c.heads * (p.c.D * p.esz / 16 + (p.esz == 1 ? p.c.D / SV_KV_GROUP : 0));
+  const int64_t units = static_cast<int64_t>(p.sides) * p.c.heads * (p.c.D * p.bits / 128 + (p.bits < 16 ? p.c.D / SV_KV_GROUP : 0));
   // As many layers to a block as make all blocks run at once, four to an SM.
   const int64_t gy = (units + kMoveThreads - 1) / kMoveThreads;
   p.layers = static_cast<int>(std::max<int64_t>(
@@ -218,57 +120,14 @@ sv_status attn_general(int64_t cache_dtype, const AttnParams &p, sv_stream_t str
   const int64_t rows = static_cast<int64_t>(p.bt.B) * p.bt.T * p.Hq;
   if (rows > INT_MAX) return SV_ERR_INVALID_ARG;
   const dim3 grid(static_cast<unsigned>(rows));
-  return cache_dtype == SV_E4M3
+  return cache_dtype == SV_I4
+             ? launch(sv_attn_general_kernel<Q, I4>, grid, 32 * kGenWarps, 0, stream, p)
+         : cache_dtype == SV_E4M3
              ? launch(sv_attn_general_kernel<Q, E4M3>, grid, 32 * kGenWarps, 0, stream, p)
              : launch(sv_attn_general_kernel<Q, Q>, grid, 32 * kGenWarps, 0, stream, p);
 }
 
 // ------------------------------------------- tensor-core attention ----
-
-constexpr int kMaxDevices = 64;
-
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder, looked up once per process.
-EncodeTiled encode_tiled() {
-  static std::atomic<void *> fn{nullptr};
-  void *f = fn.load(std::memory_order_acquire);
-  if (!f) {
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn.store(f, std::memory_order_release);
-  }
-  return reinterpret_cast<EncodeTiled>(f);
-}
-
-// A cache side as [block][head][row][element]; boxes of `box` rows, 128
-// bytes wide for 16-bit types (swizzled, as the tensor cores read them), a
-// whole row for e4m3.
-bool make_map(CUtensorMap &m, const Cache &c, const void *base, int64_t dtype, int box) {
-  const EncodeTiled enc = encode_tiled();
-  if (!enc) return false;
-  const bool f8 = dtype == SV_E4M3;
-  const cuuint64_t esz = f8 ? 1 : 2;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.bs),
-                              static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.num_blocks)};
-  const cuuint64_t row = c.D * esz, head = row * c.bs;
-  const cuuint64_t strides[3] = {row, head,
-                                 c.block_bytes ? static_cast<cuuint64_t>(c.block_bytes) : head * c.heads};
-  const cuuint32_t boxes[4] = {f8 ? static_cast<cuuint32_t>(c.D) : 64u, static_cast<cuuint32_t>(box), 1, 1};
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
-  return enc(&m,
-             f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                : dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-             4, const_cast<void *>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // The queries as [request][token][head][element]; boxes of `tokens` tokens of
 // the G heads that share a KV head, 64 elements wide.
@@ -328,6 +187,7 @@ int64_t tc_tiles(const Cache &c) {
 bool tc_takes(const sv_tree_attention_args *a, const AttnParams &p, const TcLayout &w) {
   if (p.c.D != 64 && p.c.D != 128) return false;
   if (p.c.bs % 8 || p.c.num_blocks < 1 || p.G > kTile || !p.qvec) return false;
+  if (a->cache.dtype == SV_I4) return false;
   if (a->cache.dtype == SV_E4M3 && p.c.sblock_bytes % 16) return false;
   if (p.c.block_bytes >= (int64_t{1} << 40) || p.c.sblock_bytes > INT_MAX ||
       static_cast<int64_t>(p.c.heads) * p.c.bs * (p.c.D / SV_KV_GROUP) > INT_MAX)
@@ -417,7 +277,7 @@ sv_status tree_attention(const sv_tree_attention_args *a, sv_stream_t stream) {
   if (a->dtype != SV_BF16 && a->dtype != SV_F16) return SV_ERR_UNSUPPORTED_DTYPE;
   AttnParams p = {};
   if (const sv_status s = take_cache(a->cache, a->B, false, p.c)) return s;
-  if (a->cache.dtype != SV_E4M3 && a->cache.dtype != a->dtype) return SV_ERR_UNSUPPORTED_DTYPE;
+  if (!scaled(a->cache.dtype) && a->cache.dtype != a->dtype) return SV_ERR_UNSUPPORTED_DTYPE;
   if (!attn_sizes_ok(a->B, a->T, a->num_heads, p.c.heads, p.c.D) || !std::isfinite(a->scale) ||
       a->cache.max_blocks * a->cache.block_size > SV_ATTN_MAX_KEYS)  // a tile of keys ends below 2^31
     return SV_ERR_INVALID_ARG;

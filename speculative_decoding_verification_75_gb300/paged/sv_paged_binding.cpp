@@ -36,6 +36,8 @@ decltype(&sv_kv_read) fn_read;
 decltype(&sv_kv_compact) fn_compact;
 decltype(&sv_tree_attention) fn_attn;
 decltype(&sv_tree_attention_workspace_bytes) fn_ws;
+decltype(&sv_kv_reserve) fn_reserve;
+decltype(&sv_qk_norm_rope) fn_rope;
 
 std::string str(at::IntArrayRef s) {
   std::ostringstream o;
@@ -98,8 +100,11 @@ uint32_t *status_word(PyObject *o, int dev) {
 
 int code_of(at::ScalarType t) {
   return t == at::kBFloat16 ? SV_BF16 : t == at::kHalf ? SV_F16 : t == at::kFloat8_e4m3fn ? SV_E4M3
-         : t == at::kFloat ? SV_F32 : -1;
+         : t == at::kByte ? SV_I4 : t == at::kFloat ? SV_F32 : -1;
 }
+
+// Caches of codes with scales, which take and are read by both 16-bit types.
+bool scaled(int64_t code) { return code == SV_E4M3 || code == SV_I4; }
 
 // Strides (layer, block) of a k / v pair whose last three dimensions are
 // dense.  Dimensions of one element may have any stride.
@@ -117,6 +122,7 @@ void pool(const at::Tensor &k, const at::Tensor &v, const char *what, bool lead,
   block = s[lead ? 1 : 0];
 }
 
+// otab NULL: a call without block tables.
 void take_cache(sv_kv_cache &c, PyObject *ok, PyObject *ov, PyObject *oks, PyObject *ovs, PyObject *otab, int dev,
                 bool lead) {
   const at::Tensor &k = tensor(ok, "k_cache"), &v = tensor(ov, "v_cache");
@@ -132,30 +138,36 @@ void take_cache(sv_kv_cache &c, PyObject *ok, PyObject *ov, PyObject *oks, PyObj
   if (n[l + 1] == 0 || n[l + 2] == 0 || n[l + 3] == 0) value_error("k_cache has an empty dimension");
   pool(k, v, "k_cache and v_cache", lead, c.layer_stride, c.block_stride);
   const at::Tensor *ks = tensor_or_null(oks, "k_scale"), *vs = tensor_or_null(ovs, "v_scale");
-  if (code == SV_E4M3) {
-    if (!ks || !vs) value_error("an e4m3 cache needs k_scale and v_scale");
-    if (n[l + 3] % SV_KV_GROUP) value_error("the head dim of an e4m3 cache is a multiple of 32");
+  const int64_t per = code == SV_I4 ? 2 : 1;   // elements of an element of the tensor
+  if (scaled(code)) {
+    const std::string what = code == SV_I4 ? "a 4-bit" : "an e4m3";
+    if (!ks || !vs) value_error(what + " cache needs k_scale and v_scale");
+    if (n[l + 3] * per % SV_KV_GROUP) value_error("the head dim of " + what + " cache is a multiple of 32");
     c10::SmallVector<int64_t, 5> sn(n.begin(), n.end());
-    sn.back() /= SV_KV_GROUP;
+    sn.back() = sn.back() * per / SV_KV_GROUP;
     same(*ks, "k_scale", sn, at::kByte, dev);
     same(*vs, "v_scale", sn, at::kByte, dev);
     pool(*ks, *vs, "k_scale and v_scale", lead, c.scale_layer_stride, c.scale_block_stride);
     c.k_scale = static_cast<uint8_t *>(ks->data_ptr());
     c.v_scale = static_cast<uint8_t *>(vs->data_ptr());
   } else {
-    if (ks || vs) value_error("k_scale and v_scale belong to an e4m3 cache");
+    if (ks || vs) value_error("k_scale and v_scale belong to a cache of codes (e4m3, 4 bits)");
   }
-  const at::Tensor &tab = tensor(otab, "block_tables");
-  if (tab.dim() != 2) value_error("block_tables must be [B, max_blocks]");
-  c.block_tables = ids(otab, "block_tables", tab.sizes(), dev);
-  c.max_blocks = tab.size(1);
+  if (otab) {
+    const at::Tensor &tab = tensor(otab, "block_tables");
+    if (tab.dim() != 2) value_error("block_tables must be [B, max_blocks]");
+    c.block_tables = ids(otab, "block_tables", tab.sizes(), dev);
+    c.max_blocks = tab.size(1);
+  }
   c.k = k.data_ptr();
   c.v = v.data_ptr();
   c.num_layers = lead ? n[0] : 1;
   c.num_blocks = n[l];
   c.num_kv_heads = n[l + 1];
   c.block_size = n[l + 2];
-  c.head_dim = n[l + 3];
+  c.head_dim = n[l + 3] * per;
+  c.layer_stride *= per;
+  c.block_stride *= per;
   c.dtype = code;
 }
 
@@ -172,6 +184,23 @@ void *dense(const at::Tensor &t, const char *name, at::IntArrayRef shape, at::Sc
 void no_overlap(const at::Tensor &t, const char *name) {
   for (int64_t i = 0; i < t.dim(); ++i)
     if (t.size(i) > 1 && t.stride(i) == 0) value_error(std::string(name) + " must not be an expanded tensor");
+}
+
+// A tree mask [B, T, T] or [T, T], or None.
+template <typename A>
+void take_mask(A &a, PyObject *o, int dev) {
+  const at::Tensor *m = tensor_or_null(o, "tree_mask");
+  if (!m) return;
+  if (m->scalar_type() != at::kBool) type_error("tree_mask must be a bool tensor");
+  const int64_t d = m->dim();
+  if ((d != 2 && d != 3) || m->size(d - 1) != a.T || m->size(d - 2) != a.T || (d == 3 && m->size(0) != a.B))
+    value_error("tree_mask has shape " + str(m->sizes()) + ", expected " + str({a.T, a.T}) + " or " +
+                str({a.B, a.T, a.T}));
+  on_device(*m, "tree_mask", dev);
+  if (a.T > 1 && (m->stride(d - 1) != 1 || m->stride(d - 2) != a.T))
+    value_error("tree_mask: the last two dimensions must be dense");
+  a.tree_mask = static_cast<const uint8_t *>(m->data_ptr());
+  a.mask_batch_stride = d == 3 && a.B > 1 ? m->stride(0) : 0;
 }
 
 [[noreturn]] void not_together(const char *a, const at::Tensor &x, const at::Tensor &k, const at::Tensor &tab) {
@@ -235,7 +264,7 @@ PyObject *kv_write(PyObject *, PyObject *const *o, Py_ssize_t n) {
     if (key.dim() != 4) value_error("key must be [B, T, kv heads, head dim]");
     a.dtype = code_of(key.scalar_type());
     if (a.dtype != SV_BF16 && a.dtype != SV_F16) type_error("unsupported key dtype " + dtype_name(key.scalar_type()));
-    if (a.cache.dtype != SV_E4M3 && a.cache.dtype != a.dtype)
+    if (!scaled(a.cache.dtype) && a.cache.dtype != a.dtype)
       type_error("a " + dtype_name(k.scalar_type()) + " cache takes no " + dtype_name(key.scalar_type()) + " keys");
     a.B = key.size(0);
     a.T = key.size(1);
@@ -262,7 +291,7 @@ PyObject *kv_read(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const at::Tensor &key = tensor(o[5], "out[0]"), &value = tensor(o[6], "out[1]");
     if (key.dim() != 4) value_error("out must be two [B, T, kv heads, head dim] tensors");
     a.dtype = code_of(key.scalar_type());
-    if (a.dtype < 0 || a.dtype == SV_E4M3) type_error("unsupported output dtype " + dtype_name(key.scalar_type()));
+    if (a.dtype < 0 || scaled(a.dtype)) type_error("unsupported output dtype " + dtype_name(key.scalar_type()));
     a.B = tab.size(0);
     a.T = key.size(1);
     if (key.size(0) != a.B || key.size(2) != a.cache.num_kv_heads || key.size(3) != a.cache.head_dim)
@@ -300,6 +329,26 @@ PyObject *kv_compact(PyObject *, PyObject *const *o, Py_ssize_t n) {
   });
 }
 
+// A tuple of new references; NULL where one of them is.
+PyObject *tuple_of(std::initializer_list<PyObject *> items) {
+  PyObject *t = PyTuple_New(static_cast<Py_ssize_t>(items.size()));
+  Py_ssize_t i = 0;
+  bool whole = t != nullptr;
+  for (PyObject *x : items) whole = whole && x;
+  for (PyObject *x : items) {
+    if (whole) PyTuple_SET_ITEM(t, i++, x);
+    else Py_XDECREF(x);
+  }
+  if (!whole) Py_CLEAR(t);
+  return t;
+}
+
+PyObject *given_or(PyObject *given, const at::Tensor &made) {
+  if (given == Py_None) return THPVariable_Wrap(made);
+  Py_INCREF(given);
+  return given;
+}
+
 // (query, k_cache, v_cache, block_tables, seq_lens, tree_mask, new_lens, scale, k_scale, v_scale, out, lse,
 //  workspace, status, stream) -> (status, out)
 PyObject *tree_attention(PyObject *, PyObject *const *o, Py_ssize_t n) {
@@ -313,7 +362,7 @@ PyObject *tree_attention(PyObject *, PyObject *const *o, Py_ssize_t n) {
     if (q.dim() != 4) value_error("query must be [B, T, heads, head dim]");
     a.dtype = code_of(q.scalar_type());
     if (a.dtype != SV_BF16 && a.dtype != SV_F16) type_error("unsupported query dtype " + dtype_name(q.scalar_type()));
-    if (a.cache.dtype != SV_E4M3 && a.cache.dtype != a.dtype)
+    if (!scaled(a.cache.dtype) && a.cache.dtype != a.dtype)
       type_error(dtype_name(q.scalar_type()) + " queries do not read a " + dtype_name(k.scalar_type()) + " cache");
     a.B = q.size(0);
     a.T = q.size(1);
@@ -323,18 +372,7 @@ PyObject *tree_attention(PyObject *, PyObject *const *o, Py_ssize_t n) {
     a.query = dense(q, "query", q.sizes(), q.scalar_type(), dev, a.query_stride);
     a.seq_lens = ids(o[4], "seq_lens", {a.B}, dev);
     a.new_lens = ids(o[6], "new_lens", {a.B}, dev, true);
-    if (const at::Tensor *m = tensor_or_null(o[5], "tree_mask")) {
-      if (m->scalar_type() != at::kBool) type_error("tree_mask must be a bool tensor");
-      const int64_t d = m->dim();
-      if ((d != 2 && d != 3) || m->size(d - 1) != a.T || m->size(d - 2) != a.T || (d == 3 && m->size(0) != a.B))
-        value_error("tree_mask has shape " + str(m->sizes()) + ", expected " + str({a.T, a.T}) + " or " +
-                    str({a.B, a.T, a.T}));
-      on_device(*m, "tree_mask", dev);
-      if (a.T > 1 && (m->stride(d - 1) != 1 || m->stride(d - 2) != a.T))
-        value_error("tree_mask: the last two dimensions must be dense");
-      a.tree_mask = static_cast<const uint8_t *>(m->data_ptr());
-      a.mask_batch_stride = d == 3 && a.B > 1 ? m->stride(0) : 0;
-    }
+    take_mask(a, o[5], dev);
     if (o[7] == Py_None) {
       a.scale = 1.0 / std::sqrt(static_cast<double>(a.cache.head_dim));
     } else {
@@ -373,22 +411,160 @@ PyObject *tree_attention(PyObject *, PyObject *const *o, Py_ssize_t n) {
     a.workspace_bytes = static_cast<uint64_t>(ws->numel());
     PyObject *rc = call(fn_attn, a, w.stream);
     if (!rc) return nullptr;
-    PyObject *res = o[10];
-    if (res == Py_None) res = THPVariable_Wrap(new_out);
-    else Py_INCREF(res);
-    if (!res) {
-      Py_DECREF(rc);
-      return nullptr;
+    return tuple_of({rc, given_or(o[10], new_out)});
+  });
+}
+
+// A result of this shape: the given tensor, contiguous, or a new one.
+template <typename E>
+E *result(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType dtype, const at::TensorOptions &like,
+          int dev, at::Tensor &made) {
+  const at::Tensor *t = tensor_or_null(o, name);
+  if (t) {
+    same(*t, name, shape, dtype, dev);
+    if (!t->is_contiguous()) value_error(std::string(name) + " must be contiguous");
+  } else {
+    made = at::empty(shape, like.dtype(dtype));
+    t = &made;
+  }
+  return static_cast<E *>(t->data_ptr());
+}
+
+// (seq_lens, new_lens, block_tables, block_size, free_list, free_count, tree_mask, max_new, slots, positions,
+//  reserved, status, stream) -> (status, slots, positions, reserved)
+PyObject *kv_reserve(PyObject *, PyObject *const *o, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject * {
+    sv_kv_reserve_args a = {};
+    a.struct_bytes = sizeof a;
+    const at::Tensor &seq = tensor(o[0], "seq_lens"), &tab = tensor(o[2], "block_tables");
+    const int dev = device_of(seq, "seq_lens");
+    if (tab.dim() != 2) value_error("block_tables must be [B, max_blocks]");
+    a.B = tab.size(0);
+    a.max_blocks = tab.size(1);
+    a.seq_lens = ids(o[0], "seq_lens", {a.B}, dev);
+    a.new_lens = ids(o[1], "new_lens", {a.B}, dev, true);
+    a.block_tables = const_cast<int32_t *>(ids(o[2], "block_tables", tab.sizes(), dev));
+    a.block_size = PyLong_AsLongLong(o[3]);
+    if (PyErr_Occurred()) throw Refused{nullptr, ""};
+    const at::Tensor &list = tensor(o[4], "free_list");
+    if (list.dim() != 1) value_error("free_list must have 1 dimension");
+    a.free_list = ids(o[4], "free_list", list.sizes(), dev);
+    a.free_capacity = list.numel();
+    const at::Tensor &cnt = tensor(o[5], "free_count");
+    if (cnt.numel() != 1) value_error("free_count must have 1 element");
+    a.free_count = const_cast<int32_t *>(ids(o[5], "free_count", cnt.sizes(), dev));
+    // T: said, or that of the first tensor which has it.
+    if (o[7] != Py_None) {
+      a.T = PyLong_AsLongLong(o[7]);
+      if (PyErr_Occurred()) throw Refused{nullptr, ""};
+      if (a.T < 0) value_error("max_new is negative");
+    } else {
+      const at::Tensor *m = tensor_or_null(o[6], "tree_mask");
+      const at::Tensor *s = tensor_or_null(o[8], "slots");
+      if (s && s->dim() == 2) a.T = s->size(1);
+      else if (m && m->dim() >= 2) a.T = m->size(m->dim() - 1);
+      else value_error("max_new is needed when neither slots nor tree_mask says how many new tokens there are");
     }
-    PyObject *both = PyTuple_New(2);
-    if (!both) {
-      Py_DECREF(rc);
-      Py_DECREF(res);
-      return nullptr;
+    take_mask(a, o[6], dev);
+    a.status = status_word(o[11], dev);
+    const Where w(o[12], dev);
+    at::Tensor slots, positions, reserved;
+    const auto like = seq.options();
+    a.slots = result<int64_t>(o[8], "slots", {a.B, a.T}, at::kLong, like, dev, slots);
+    a.positions = result<int32_t>(o[9], "positions", {a.B, a.T}, at::kInt, like, dev, positions);
+    a.reserved = result<int32_t>(o[10], "reserved", {a.B}, at::kInt, like, dev, reserved);
+    PyObject *rc = call(fn_reserve, a, w.stream);
+    if (!rc) return nullptr;
+    return tuple_of({rc, given_or(o[8], slots), given_or(o[9], positions), given_or(o[10], reserved)});
+  });
+}
+
+// (query, key, cos_sin, positions, q_weight, k_weight, eps, interleaved, out, key_out, value, k_cache, v_cache, slots,
+//  k_scale, v_scale, status, stream) -> (status, out, key_out or None)
+PyObject *qk_norm_rope(PyObject *, PyObject *const *o, Py_ssize_t n) {
+  return guarded(n, 18, [&]() -> PyObject * {
+    sv_qk_norm_rope_args a = {};
+    a.struct_bytes = sizeof a;
+    const at::Tensor &q = tensor(o[0], "query"), &k = tensor(o[1], "key");
+    const int dev = device_of(q, "query");
+    if (q.dim() != 4) value_error("query must be [B, T, heads, head dim]");
+    if (k.dim() != 4 || k.size(0) != q.size(0) || k.size(1) != q.size(1) || k.size(3) != q.size(3))
+      value_error("query " + str(q.sizes()) + " and key " + str(k.sizes()) + " do not belong together");
+    a.dtype = code_of(q.scalar_type());
+    if (a.dtype != SV_BF16 && a.dtype != SV_F16) type_error("unsupported query dtype " + dtype_name(q.scalar_type()));
+    a.B = q.size(0);
+    a.T = q.size(1);
+    a.num_heads = q.size(2);
+    a.num_kv_heads = k.size(2);
+    a.head_dim = q.size(3);
+    a.query = dense(q, "query", q.sizes(), q.scalar_type(), dev, a.query_stride);
+    a.key = dense(k, "key", k.sizes(), q.scalar_type(), dev, a.key_stride);
+    const at::Tensor &cs = tensor(o[2], "cos_sin");
+    if (cs.dim() != 2) value_error("cos_sin must be [positions, rotary dim]");
+    same(cs, "cos_sin", cs.sizes(), at::kFloat, dev);
+    if (!cs.is_contiguous()) value_error("cos_sin must be contiguous");
+    a.cos_sin = static_cast<const float *>(cs.data_ptr());
+    a.num_positions = cs.size(0);
+    a.rotary_dim = cs.size(1);
+    a.positions = ids(o[3], "positions", {a.B, a.T}, dev);
+    const auto weight = [&](PyObject *x, const char *name) -> const void * {
+      const at::Tensor *t = tensor_or_null(x, name);
+      if (!t) return nullptr;
+      same(*t, name, {a.head_dim}, q.scalar_type(), dev);
+      if (!t->is_contiguous()) value_error(std::string(name) + " must be contiguous");
+      return t->data_ptr();
+    };
+    a.q_weight = weight(o[4], "q_weight");
+    a.k_weight = weight(o[5], "k_weight");
+    a.eps = PyFloat_AsDouble(o[6]);
+    if (PyErr_Occurred()) throw Refused{nullptr, ""};
+    const int pairs = PyObject_IsTrue(o[7]);
+    if (pairs < 0) throw Refused{nullptr, ""};
+    a.interleaved = pairs;
+    const bool cached = o[11] != Py_None || o[12] != Py_None;
+    if (cached) {
+      take_cache(a.cache, o[11], o[12], o[14], o[15], nullptr, dev, false);
+      const at::Tensor &kc = tensor(o[11], "k_cache");
+      if (!scaled(a.cache.dtype) && a.cache.dtype != a.dtype)
+        type_error("a " + dtype_name(kc.scalar_type()) + " cache takes no " + dtype_name(k.scalar_type()) + " keys");
+      if (a.cache.num_kv_heads != a.num_kv_heads || a.cache.head_dim != a.head_dim)
+        value_error("key " + str(k.sizes()) + " and k_cache " + str(kc.sizes()) + " do not belong together");
+      const at::Tensor &v = tensor(o[10], "value"), &s = tensor(o[13], "slots");
+      a.value = dense(v, "value", k.sizes(), q.scalar_type(), dev, a.value_stride);
+      same(s, "slots", {a.B, a.T}, at::kLong, dev);
+      if (!s.is_contiguous()) value_error("slots must be contiguous");
+      a.slots = static_cast<const int64_t *>(s.data_ptr());
+    } else {
+      if (o[10] != Py_None || o[13] != Py_None || o[14] != Py_None || o[15] != Py_None)
+        value_error("value, slots and scales belong to k_cache and v_cache");
     }
-    PyTuple_SET_ITEM(both, 0, rc);
-    PyTuple_SET_ITEM(both, 1, res);
-    return both;
+    a.status = status_word(o[16], dev);
+    const at::Tensor *out = tensor_or_null(o[8], "out"), *ko = tensor_or_null(o[9], "key_out");
+    if (out) {
+      a.out = dense(*out, "out", q.sizes(), q.scalar_type(), dev, a.out_stride);
+      no_overlap(*out, "out");
+    }
+    if (ko) {
+      a.key_out = dense(*ko, "key_out", k.sizes(), q.scalar_type(), dev, a.key_out_stride);
+      no_overlap(*ko, "key_out");
+    }
+    const Where w(o[17], dev);
+    at::Tensor new_out, new_ko;
+    const auto like = q.options().memory_format(at::MemoryFormat::Contiguous);
+    if (!out) {
+      new_out = at::empty(q.sizes(), like);
+      a.out = dense(new_out, "out", q.sizes(), q.scalar_type(), dev, a.out_stride);
+    }
+    if (!ko && !cached) {
+      new_ko = at::empty(k.sizes(), like);
+      a.key_out = dense(new_ko, "key_out", k.sizes(), q.scalar_type(), dev, a.key_out_stride);
+    }
+    // An empty slots tensor has no address; its call has nothing to do.
+    if (a.B == 0 || a.T == 0) return tuple_of({PyLong_FromLong(SV_OK), given_or(o[8], new_out),
+                                              !ko && cached ? Py_NewRef(Py_None) : given_or(o[9], new_ko)});
+    PyObject *rc = call(fn_rope, a, w.stream);
+    if (!rc) return nullptr;
+    return tuple_of({rc, given_or(o[8], new_out), !ko && cached ? Py_NewRef(Py_None) : given_or(o[9], new_ko)});
   });
 }
 
@@ -406,7 +582,9 @@ PyObject *bind_library(PyObject *, PyObject *arg) {
   fn_compact = reinterpret_cast<decltype(fn_compact)>(dlsym(lib, "sv_kv_compact"));
   fn_attn = reinterpret_cast<decltype(fn_attn)>(dlsym(lib, "sv_tree_attention"));
   fn_ws = reinterpret_cast<decltype(fn_ws)>(dlsym(lib, "sv_tree_attention_workspace_bytes"));
-  if (!fn_write || !fn_read || !fn_compact || !fn_attn || !fn_ws) {
+  fn_reserve = reinterpret_cast<decltype(fn_reserve)>(dlsym(lib, "sv_kv_reserve"));
+  fn_rope = reinterpret_cast<decltype(fn_rope)>(dlsym(lib, "sv_qk_norm_rope"));
+  if (!fn_write || !fn_read || !fn_compact || !fn_attn || !fn_ws || !fn_reserve || !fn_rope) {
     PyErr_SetString(PyExc_OSError, "the library lacks the paged-cache entry points");
     return nullptr;
   }
@@ -418,6 +596,8 @@ PyMethodDef methods[] = {
     {"kv_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv_read)), METH_FASTCALL, nullptr},
     {"kv_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv_compact)), METH_FASTCALL, nullptr},
     {"tree_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(tree_attention)), METH_FASTCALL, nullptr},
+    {"kv_reserve", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv_reserve)), METH_FASTCALL, nullptr},
+    {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(qk_norm_rope)), METH_FASTCALL, nullptr},
     {"bind_library", bind_library, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

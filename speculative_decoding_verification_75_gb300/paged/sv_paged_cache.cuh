@@ -5,7 +5,7 @@
 // by HBM, a step's few tokens by the chain lengths -> block table -> data.
 #pragma once
 
-#include "sv_paged_common.cuh"
+#include "sv_paged_quant.cuh"
 
 namespace svp {
 
@@ -81,64 +81,6 @@ __device__ __forceinline__ Column column_of(const Cache &c, int i) {
   return q;
 }
 
-// Quantises 32 elements that 4 adjacent lanes hold (8 each); returns the
-// scale byte.  Every lane of the warp takes part.  Magnitudes are compared as
-// 16-bit integers, two at a time, and only a warp that meets an infinity or NaN
-// looks at its elements one by one (8 prompts of up to 8192 tokens: 58 us, 5.3 TB/s;
-// 68 us with comparisons of single fp32 magnitudes).
-template <typename Q>
-__device__ __forceinline__ uint32_t quantise8(const uint4 &raw, uint2 &codes) {
-  const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-  constexpr uint32_t kInf = Q::kIsBf16 ? 0x7f80u : 0x7c00u;
-  uint32_t big = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) big = __vmaxu2(big, u[i] & 0x7fff7fffu);
-  big = max(big & 0xffffu, big >> 16);
-  const bool odd = __any_sync(kFull, big >= kInf);
-  if (odd) {                                       // the largest finite magnitude
-    big = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = u[i] & 0x7fffu, hi = (u[i] >> 16) & 0x7fffu;
-      big = max(big, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
-    }
-  }
-  big = max(big, __shfl_xor_sync(kFull, big, 1));
-  big = max(big, __shfl_xor_sync(kFull, big, 2));
-  float a[8];
-  const uint4 only = make_uint4(big, 0, 0, 0);
-  unpack8<Q>(&only, a);
-  // a = 1.f * 2^E <= 448 * 2^e = 1.75 * 2^(e + 8): e = E - 8, or E - 7 where
-  // 1.f is above 1.75.  (Subnormal a: E is too large, but e is -120 anyway.)
-  const uint32_t v = __float_as_uint(a[0]);
-  int e = static_cast<int>(v >> 23) - 127 - 8 + ((v & 0x7fffffu) > 0x600000u ? 1 : 0);
-  e = max(e, -120);
-  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  float f[8];
-  unpack8<Q>(&raw, f);
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 y = make_float2(f[2 * i] * inv, f[2 * i + 1] * inv);  // exact, or below every code
-    if (odd) {  // at most 448 where f is finite; an infinity becomes NaN, not 448
-      if (!(fabsf(y.x) <= 448.f)) y.x = __uint_as_float(0x7fc00000u);
-      if (!(fabsf(y.y) <= 448.f)) y.y = __uint_as_float(0x7fc00000u);
-    }
-    h[i] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-  }
-  codes = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-  return static_cast<uint32_t>(e + 127);
-}
-
-// 16 bytes from the dense side, whatever its alignment (2-byte elements).
-__device__ __forceinline__ uint4 load16(const uint8_t *s, bool vec) {
-  if (vec) return ld128(s);
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] = ld16(s + 4 * k) | (ld16(s + 4 * k + 2) << 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // kv_write.  Q: type of the new tokens, C: the cache's.  Grid: (requests x
 // token groups, column groups).
 template <typename Q, typename C>
@@ -147,7 +89,7 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_write_kernel(const MovePar
   sv::pdl_wait();
   sv::pdl_launch_dependents();
   const int b = blockIdx.x / p.groups, t0 = (blockIdx.x - b * p.groups) * kMoveTokens;
-  const int row_bytes = p.c.D * C::kBytes;
+  const int row_bytes = p.c.D / 8 * C::kBits;
   const int cnt = find_slots<false>(p, b, t0, row_bytes, slot);
   const Column q = column_of(p.c, blockIdx.y * kMoveThreads + threadIdx.x);
   const int64_t step = q.is_v ? p.vst : p.kst;
@@ -159,9 +101,9 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_write_kernel(const MovePar
     raw[i] = q.on && i < cnt ? load16(src + i * step, p.vec) : make_uint4(0, 0, 0, 0);
   __syncthreads();
   uint8_t *dst = (q.is_v ? p.c.v : p.c.k) + static_cast<int64_t>(q.h) * p.c.bs * row_bytes +
-                 q.d8 * 8 * C::kBytes;
+                 q.d8 * C::kBits;
   const int srow = p.c.D / SV_KV_GROUP;
-  uint8_t *dsc = C::kBytes == 1
+  uint8_t *dsc = C::kScaled
                      ? (q.is_v ? p.c.vs : p.c.ks) + static_cast<int64_t>(q.h) * p.c.bs * srow + q.d8 / 4
                      : nullptr;
 #pragma unroll
@@ -169,11 +111,11 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_write_kernel(const MovePar
     if (i >= cnt) break;  // the same for every thread
     const Slot s = slot[i];
     const bool put = q.on && s.data >= 0;
-    if constexpr (C::kBytes == 1) {
-      uint2 codes;
+    if constexpr (C::kScaled) {
+      typename Codes<C>::type codes;
       const uint32_t sc = quantise8<Q>(raw[i], codes);
       if (put) {
-        *reinterpret_cast<uint2 *>(dst + s.data) = codes;
+        *reinterpret_cast<typename Codes<C>::type *>(dst + s.data) = codes;
         if ((q.d8 & 3) == 0) dsc[s.scale] = static_cast<uint8_t>(sc);
       }
     } else {
@@ -189,15 +131,15 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_read_kernel(const MovePara
   sv::pdl_wait();
   sv::pdl_launch_dependents();
   const int b = blockIdx.x / p.groups, t0 = (blockIdx.x - b * p.groups) * kMoveTokens;
-  const int row_bytes = p.c.D * C::kBytes;
+  const int row_bytes = p.c.D / 8 * C::kBits;
   const int cnt = find_slots<true>(p, b, t0, row_bytes, slot);
   const Column q = column_of(p.c, blockIdx.y * kMoveThreads + threadIdx.x);
   __syncthreads();
   if (!q.on) return;
   const uint8_t *src = (q.is_v ? p.c.v : p.c.k) + static_cast<int64_t>(q.h) * p.c.bs * row_bytes +
-                       q.d8 * 8 * C::kBytes;
+                       q.d8 * C::kBits;
   const int srow = p.c.D / SV_KV_GROUP;
-  const uint8_t *ssc = C::kBytes == 1 ? (q.is_v ? p.c.vs : p.c.ks) +
+  const uint8_t *ssc = C::kScaled ? (q.is_v ? p.c.vs : p.c.ks) +
                                             static_cast<int64_t>(q.h) * p.c.bs * srow + q.d8 / 4
                                       : nullptr;
   uint4 raw[kMoveTokens];
@@ -205,13 +147,8 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_read_kernel(const MovePara
 #pragma unroll
   for (int i = 0; i < kMoveTokens; ++i) {
     if (i < cnt && slot[i].data >= 0) {
-      if constexpr (C::kBytes == 1) {
-        const uint2 w = ld64(src + slot[i].data);
-        raw[i] = make_uint4(w.x, w.y, 0, 0);
-        sc[i] = ld8(ssc + slot[i].scale);
-      } else {
-        raw[i] = ld128(src + slot[i].data);
-      }
+      raw[i] = load8<C>(src + slot[i].data);
+      if constexpr (C::kScaled) sc[i] = ld8(ssc + slot[i].scale);
     }
   }
   const int64_t step = q.is_v ? p.vst : p.kst;
@@ -223,8 +160,8 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_read_kernel(const MovePara
     if (slot[i].data < 0) continue;
     float f[8];
     unpack8<C>(&raw[i], f);
-    if constexpr (C::kBytes == 1) {
-      const float m = scale_value(sc[i]);
+    if constexpr (C::kScaled) {
+      const float m = scale_value<C>(sc[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] *= m;
     }
@@ -242,7 +179,7 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_read_kernel(const MovePara
 struct CompactParams {
   Cache c;
   const int32_t *path, *num_accepted, *seq_lens;
-  int B, P, esz, sides;  // sides: 1 where k and v are one array
+  int B, P, bits, sides;  // bits of an element; sides: 1 where k and v are one array
   int layers, groups;  // layers of a thread block, groups of them
   uint32_t *status;
 };
@@ -255,7 +192,8 @@ struct Move {
 };
 
 __device__ __forceinline__ Move move_of(const CompactParams &p, int from, int from_pos, int to, int to_pos) {
-  const Slot f = slot_at(p.c, from, from_pos, p.c.D * p.esz), t = slot_at(p.c, to, to_pos, p.c.D * p.esz);
+  const int row_bytes = p.c.D / 8 * p.bits;
+  const Slot f = slot_at(p.c, from, from_pos, row_bytes), t = slot_at(p.c, to, to_pos, row_bytes);
   return Move{f.data, t.data, f.scale, t.scale};
 }
 
@@ -312,8 +250,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) sv_kv_compact_kernel(const Co
   if (blockIdx.y == 0 && l0 == 0) report(p.status, st);
   if (__syncthreads_or(static_cast<int>(st))) return;
 
-  const int row_bytes = p.c.D * p.esz, per_head = row_bytes / 16, per_side = p.c.heads * per_head;
-  const int srow = p.esz == 1 ? p.c.D / SV_KV_GROUP : 0, sper_side = p.c.heads * srow;
+  const int row_bytes = p.c.D / 8 * p.bits, per_head = row_bytes / 16, per_side = p.c.heads * per_head;
+  const int srow = p.bits < 16 ? p.c.D / SV_KV_GROUP : 0, sper_side = p.c.heads * srow;
   const int u = blockIdx.y * kMoveThreads + threadIdx.x;
   const bool data = u < p.sides * per_side, scales = !data && u - p.sides * per_side < p.sides * sper_side;
   uint8_t *base = nullptr;

@@ -20,11 +20,13 @@ namespace svp {
 
 using sv::kFull;
 
-// Element tags.
-struct BF16 { using raw = __nv_bfloat16; static constexpr int kBytes = 2; static constexpr bool kIsBf16 = true; };
-struct F16 { using raw = __half; static constexpr int kBytes = 2; static constexpr bool kIsBf16 = false; };
-struct F32 { using raw = float; static constexpr int kBytes = 4; };
-struct E4M3 { using raw = uint8_t; static constexpr int kBytes = 1; };
+// Element tags.  kScaled: codes, with a scale byte for SV_KV_GROUP of them.
+// Eight elements take kBits bytes.
+struct BF16 { using raw = __nv_bfloat16; static constexpr int kBits = 16, kBytes = 2; static constexpr bool kIsBf16 = true, kScaled = false; };
+struct F16 { using raw = __half; static constexpr int kBits = 16, kBytes = 2; static constexpr bool kIsBf16 = false, kScaled = false; };
+struct F32 { using raw = float; static constexpr int kBits = 32, kBytes = 4; };
+struct E4M3 { using raw = uint8_t; static constexpr int kBits = 8, kBytes = 1; static constexpr bool kScaled = true; };
+struct I4 { using raw = uint8_t; static constexpr int kBits = 4; static constexpr bool kScaled = true; };
 
 struct Cache {
   uint8_t *k, *v;
@@ -71,6 +73,19 @@ __device__ __forceinline__ uint2 ld64(const void *p) {
   return v;
 }
 
+// Eight elements as they lie in the cache, in the vector's first kBits bytes.
+template <typename C>
+__device__ __forceinline__ uint4 load8(const void *p) {
+  if constexpr (C::kBits == 4) {
+    return make_uint4(static_cast<uint32_t>(ld32(static_cast<const int32_t *>(p))), 0, 0, 0);
+  } else if constexpr (C::kBits == 8) {
+    const uint2 w = ld64(p);
+    return make_uint4(w.x, w.y, 0, 0);
+  } else {
+    return ld128(p);
+  }
+}
+
 __device__ __forceinline__ void report(uint32_t *status, uint32_t bits) {
   if (status && bits) atomicOr(status, bits);
 }
@@ -101,9 +116,21 @@ __device__ __forceinline__ bool lengths(const Batch &bt, int b, int &L, int &n, 
   return true;
 }
 
+// A scale byte's value.
+template <typename C>
+__device__ __forceinline__ float scale_value(uint32_t s);
+
 // 2^(s - 127), with E8M0's NaN at 255.
-__device__ __forceinline__ float scale_value(uint32_t s) {
+template <>
+__device__ __forceinline__ float scale_value<E4M3>(uint32_t s) {
   return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : s << 23);
+}
+
+// 2^(s / 8 - 14) * (1 + s % 8 / 8): the byte is the exponent and three fraction
+// bits of a float, moved by 113.
+template <>
+__device__ __forceinline__ float scale_value<I4>(uint32_t s) {
+  return __uint_as_float(s > SV_KV_I4_MAX_SCALE ? 0x7fc00000u : (s << 20) + (113u << 23));
 }
 
 // Eight elements as fp32.
@@ -145,6 +172,13 @@ __device__ __forceinline__ void unpack8<E4M3>(const void *p, float (&f)[8]) {
     f[2 * i] = t.x;
     f[2 * i + 1] = t.y;
   }
+}
+
+template <>
+__device__ __forceinline__ void unpack8<I4>(const void *p, float (&f)[8]) {
+  const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(static_cast<int>(w >> (4 * i) & 15u) - 8);
 }
 
 template <typename E>
