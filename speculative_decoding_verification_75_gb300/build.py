@@ -23,7 +23,8 @@ ROOT = PKG.parent
 SRC_DIR = PKG / "csrc"
 MAIN = SRC_DIR / "spec_verify.cu"
 PAGED_DIR = PKG / "paged"
-UNITS = [MAIN, PAGED_DIR / "sv_paged.cu", PAGED_DIR / "sv_step.cu"]
+UNITS = [MAIN, PAGED_DIR / "sv_paged.cu", PAGED_DIR / "sv_step.cu",
+         PAGED_DIR / "sv_attn_i4.cu"]
 INCLUDE = ROOT / "include"
 LIB = PKG / "lib" / "libspecverify.so"
 BINDING_SRC = PAGED_DIR / "sv_paged_binding.cpp"

@@ -89,6 +89,7 @@ struct TcParams {
   Cut *cuts;           // [ranges] where each range begins
   float *slots;        // [ranges * 2] partial results
   int ranges, grid;    // of the tiles; thread blocks at most
+  int unit_rows;       // query rows of a unit at most
   int slot_rows;       // rows of a slot
   int slot_floats;
   int box;             // rows of a TMA box of the cache
@@ -323,19 +324,36 @@ struct Req {
   int L, n, mp, kv_end, kt, weight;
 };
 
-// Tiles of a request: its units (KV head, group of row tiles) times its key
-// tiles.  upt: new tokens of a unit.
-__device__ __forceinline__ Req request(const AttnParams &p, int upt, int b, uint32_t &st) {
+// What a unit has of a request's rows: whole tokens (an int: how many), tiles of
+// kKeys keys; or (sv_attn_i4.cuh) rows whatever tokens they belong to.
+struct RowUnits {
+  int rows;
+};
+template <typename U>
+constexpr int kUnitKeys = kKeys;
+template <>
+constexpr int kUnitKeys<RowUnits> = 128;
+__device__ __forceinline__ int units_of(int upt, int n, int) { return (n + upt - 1) / upt; }
+__device__ __forceinline__ int units_of(RowUnits u, int n, int G) { return (n * G + u.rows - 1) / u.rows; }
+__device__ __forceinline__ int rows_per(int upt, int G) { return upt * G; }
+__device__ __forceinline__ int rows_per(RowUnits u, int) { return u.rows; }
+
+// Tiles of a request: its units (KV head, group of rows) times its key tiles.
+// upt: new tokens of a unit, or its RowUnits.
+template <typename U>
+__device__ __forceinline__ Req request(const AttnParams &p, U upt, int b, uint32_t &st) {
+  constexpr int keys = kUnitKeys<U>;
   Req r;
   lengths(p.bt, b, r.L, r.n, st);
-  r.mp = (r.n + upt - 1) / upt;
+  r.mp = units_of(upt, r.n, p.G);
   r.kv_end = min(r.L + r.n, p.c.max_blocks * p.c.bs);
-  r.kt = max(1, (r.kv_end + kKeys - 1) / kKeys);
+  r.kt = max(1, (r.kv_end + keys - 1) / keys);
   r.weight = p.c.heads * r.mp * r.kt;
   return r;
 }
 
-__device__ __forceinline__ int weight_of(const AttnParams &p, int upt, int b, uint32_t &st) {
+template <typename U>
+__device__ __forceinline__ int weight_of(const AttnParams &p, U upt, int b, uint32_t &st) {
   return b < p.bt.B ? request(p, upt, b, st).weight : 0;
 }
 
@@ -368,7 +386,8 @@ struct Walk {
 
 // To the next segment.  Not inlined: every role of the kernel walks, and the
 // copies together would crowd the instruction cache.
-__device__ __noinline__ void next_segment(const AttnParams &p, int upt, Walk &w) {
+template <typename U>
+__device__ __noinline__ void next_segment(const AttnParams &p, U upt, Walk &w) {
   Walk v = w;
   v.on = v.left > 0;
   if (v.on) {
@@ -403,7 +422,8 @@ __device__ __forceinline__ Tile tile_of(const Walk &w) {
   return Tile{w.t0, w.t0, w.t1, w.b, w.h, w.mp, w.seg, w.r.kv_end, w.new0(), w.on, w.r.kv_end < w.r.L + w.r.n};
 }
 
-__device__ __forceinline__ void next_tile(const AttnParams &p, int upt, Walk &w, Tile &x) {
+template <typename U>
+__device__ __forceinline__ void next_tile(const AttnParams &p, U upt, Walk &w, Tile &x) {
   if (++x.t < x.t1) return;
   next_segment(p, upt, w);
   x = tile_of(w);
@@ -416,7 +436,8 @@ __device__ __forceinline__ int count_of(const Walk &w) { return w.on ? w.left + 
 
 // Range i's first tile, by a whole warp: the requests are spread over the
 // lanes, 32 at a time.
-__device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, int limit, Walk &w, int &total) {
+template <typename U>
+__device__ __forceinline__ void begin_walk(const AttnParams &p, U upt, int i, int limit, Walk &w, int &total) {
   const int lane = threadIdx.x & 31, B = p.bt.B;
   uint32_t st = 0;
   const int mine = weight_of(p, upt, lane, st);  // requests 0 .. 31
@@ -464,7 +485,7 @@ __device__ __forceinline__ void begin_walk(const AttnParams &p, int upt, int i, 
 // A converged warp's wait for an mbarrier phase; false when it gives up, after
 // about two seconds.  The warp is suspended meanwhile: polling warps took the
 // issue slots of those that widen and of the softmax.
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t *err) {
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t *err) {
   const uint64_t t0 = sv::global_timer_ns();
 #pragma unroll 1
   for (uint32_t i = 0; i < (1u << 30); ++i) {
@@ -485,16 +506,16 @@ __device__ __forceinline__ bool wait_warp(const uint64_t *bar, uint32_t parity, 
 // 4 us a key (e4m3: 8.6), seconds over a long context, and bounded waits would
 // run out.  Segments whose number is a marked one's modulo kMarkBits are done
 // again as well.
-template <typename Q, typename C, int D>
-__device__ __noinline__ void recompute_marked(const AttnParams &p, int upt, const Walk &begin, const uint32_t *marks,
+template <typename Q, typename C, int D, typename U>
+__device__ __noinline__ void recompute_marked(const AttnParams &p, U upt, const Walk &begin, const uint32_t *marks,
                                               int warp, int warps) {
 #pragma unroll 1
   for (Walk w = begin; w.on; next_segment(p, upt, w)) {
     if (w.t0 > 0 || w.t1 < w.r.kt || !(marks[w.seg / 32 % (kMarkBits / 32)] >> (w.seg % 32) & 1u)) continue;
-    const int rows = min(w.r.n - w.mp * upt, upt) * p.G;
+    const int per = rows_per(upt, p.G), end = min((w.mp + 1) * per, w.r.n * p.G);
 #pragma unroll 1
-    for (int row = warp; row < rows; row += warps)
-      recompute_row<Q, C, D>(p, w.b, w.mp * upt + row / p.G, w.h * p.G + row % p.G);
+    for (int row = w.mp * per + warp; row < end; row += warps)
+      recompute_row<Q, C, D>(p, w.b, row / p.G, w.h * p.G + row % p.G);
   }
 }
 
@@ -1368,7 +1389,7 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
   int c1 = min(N - 1, static_cast<int>(static_cast<float>(end) * N / static_cast<float>(total)));
   while (ranges.start(c1) > end) --c1;
   while (c1 + 1 < N && ranges.start(c1 + 1) <= end) ++c1;
-  const int upt = p.TT * (kPair ? 2 : 1), tok0 = mp * upt, rows = min(upt, n - tok0) * a.G;
+  const int row0 = mp * p.unit_rows, rows = min(p.unit_rows, n * a.G - row0);
   const auto slot_of = [&](int c) {
     return p.slots + (static_cast<size_t>(c) * 2 + (c == c0 ? late : 0)) * p.slot_floats;
   };
@@ -1380,7 +1401,7 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
   const bool in = o < rows * kCols;
   const int d4 = in ? o / rows : 0, row = in ? o - d4 * rows : 0;
   // Rows of the second tile start at row 128 of a slot.
-  const int tile_rows = p.TT * a.G, srow = row < tile_rows ? row : kTile + row - tile_rows;
+  const int tile_rows = kPair ? p.unit_rows / 2 : p.unit_rows, srow = row < tile_rows ? row : kTile + row - tile_rows;
   float m = -INFINITY, l = 0.f;
   float4 v[E];
 #pragma unroll
@@ -1410,7 +1431,7 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
   if (__any_sync(kFull, bad)) {                       // the same for every warp
     constexpr int warps = kJoinThreads / 32;
     for (int r = blockIdx.y * warps + tid / 32; r < rows; r += gridDim.y * warps)
-      recompute_row<Q, C, D>(a, b, tok0 + r / a.G, h * a.G + r % a.G);
+      recompute_row<Q, C, D>(a, b, (row0 + r) / a.G, h * a.G + (row0 + r) % a.G);
     return;
   }
   if (K > 1) {
@@ -1429,7 +1450,7 @@ __global__ void __launch_bounds__(kJoinThreads) sv_attn_join_kernel(const __grid
   }
   if (!in) return;
   const float inv = 1.f / l;
-  const int t = tok0 + row / a.G, g = row % a.G;
+  const int t = (row0 + row) / a.G, g = (row0 + row) % a.G;
   const int64_t orow = (static_cast<int64_t>(b) * a.bt.T + t) * a.Hq + h * a.G + g;
 #pragma unroll
   for (int e = 0; e < E; ++e)

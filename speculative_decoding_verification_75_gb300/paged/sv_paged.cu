@@ -4,7 +4,7 @@
 #include "sv_paged_host.cuh"
 #include "sv_paged_cache.cuh"
 #include "sv_attn_general.cuh"
-#include "sv_attn_tc.cuh"
+#include "sv_attn_host.cuh"
 
 namespace svp {
 namespace {
@@ -148,37 +148,6 @@ bool make_query_map(CUtensorMap &m, const AttnParams &p, int64_t dtype, int toke
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Workspace of the tensor-core path.
-struct TcLayout {
-  size_t cuts, err, slots, total;
-  int TT, MP, slot_rows, slot_floats;
-};
-
-TcLayout tc_layout(int64_t T, int64_t G, int64_t D) {
-  const auto up = [](size_t x, size_t a) { return (x + a - 1) / a * a; };
-  TcLayout w;
-  w.TT = static_cast<int>(std::max<int64_t>(kTile / G, 1));  // tokens of a row tile
-  const bool pair = T > w.TT;
-  const int64_t unit = pair ? 2 * w.TT : w.TT;
-  w.MP = static_cast<int>(std::max<int64_t>((T + unit - 1) / unit, 1));
-  w.slot_rows = pair ? 2 * kTile
-                     : static_cast<int>(up(std::min<int64_t>(std::max<int64_t>(T * G, 1), kTile), 32));
-  // A pair's slot is two of a full single tile: a workspace for many tokens
-  // serves few ones too.
-  const auto slot = [&](int rows) { return static_cast<int>(up((D + 2) * rows + 1, 32)); };
-  w.slot_floats = pair ? 2 * slot(kTile) : slot(w.slot_rows);
-  w.cuts = 0;
-  w.err = up(2 * kMaxGrid * sizeof(Cut), 256);
-  w.slots = w.err + 256;
-  w.total = w.slots + up(static_cast<size_t>(kMaxGrid) * (pair ? 1 : 2) * 2 * w.slot_floats * 4, 256);
-  return w;
-}
-
-// Key tiles of a request whose table is full.
-int64_t tc_tiles(const Cache &c) {
-  return std::max<int64_t>((static_cast<int64_t>(c.max_blocks) * c.bs + kKeys - 1) / kKeys, 1);
-}
-
 // What the tensor-core kernel takes: whole 8-row swizzle atoms per page,
 // query rows on 16-byte boundaries and a token's heads within a tile, sizes
 // within TMA's and int32's.  It is
@@ -187,7 +156,6 @@ int64_t tc_tiles(const Cache &c) {
 bool tc_takes(const sv_tree_attention_args *a, const AttnParams &p, const TcLayout &w) {
   if (p.c.D != 64 && p.c.D != 128) return false;
   if (p.c.bs % 8 || p.c.num_blocks < 1 || p.G > kTile || !p.qvec) return false;
-  if (a->cache.dtype == SV_I4) return false;
   if (a->cache.dtype == SV_E4M3 && p.c.sblock_bytes % 16) return false;
   if (p.c.block_bytes >= (int64_t{1} << 40) || p.c.sblock_bytes > INT_MAX ||
       static_cast<int64_t>(p.c.heads) * p.c.bs * (p.c.D / SV_KV_GROUP) > INT_MAX)
@@ -201,25 +169,11 @@ sv_status tc_launch(const TcParams &p, int64_t units, int dev, sv_stream_t strea
   using S = Shape<Q, C, D, kPair>;
   static std::atomic<uint64_t> done{0};
   auto *k = sv_attn_tc_kernel<Q, C, D, kPair>;
-  const uint64_t bit = 1ull << (dev % kMaxDevices);
-  if (!(done.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
-      return SV_ERR_CUDA;
-    done.fetch_or(bit, std::memory_order_acq_rel);
-  }
+  if (!shared_memory(k, S::kSmem, dev, done)) return SV_ERR_CUDA;
   if (const sv_status s = launch(k, dim3(static_cast<unsigned>(std::min(p.ranges, p.grid))), S::kThreads, S::kSmem,
                                  stream, p))
     return s;
-  if (p.ranges < 2) return SV_OK;  // nothing is cut
-  // Few units are cut into many parts: then more threads share an output, and
-  // so do those of a block that would have none.
-  const int outputs = std::min(p.a.bt.T, p.TT * S::kTilesPerUnit) * p.a.G * (D / 4 / kJoinCols);
-  int K = 1;
-  while (K < 8 && K * units <= p.ranges && (K * 4 * units <= p.ranges || outputs * 2 * K <= kJoinThreads)) K *= 2;
-  const int per = kJoinThreads / K;
-  return launch(sv_attn_join_kernel<Q, C, D, kPair>,
-                dim3(static_cast<unsigned>(p.ranges - 1), static_cast<unsigned>((outputs + per - 1) / per)), kJoinThreads,
-                0, stream, p, K);
+  return join_launch<Q, C, D, kPair>(p, std::min(p.a.bt.T, p.TT * S::kTilesPerUnit) * p.a.G, units, stream);
 }
 
 template <typename Q, typename C>
@@ -249,6 +203,7 @@ sv_status attn_tc(const sv_tree_attention_args *a, const AttnParams &ap, const T
   p.c = std::max(std::fabs(ap.scale_log2), kLeast);
   p.negate = ap.scale_log2 < 0.f;
   p.TT = w.TT;
+  p.unit_rows = w.TT * (pair ? 2 : 1) * ap.G;
   p.qbox = std::min(w.TT, ap.bt.T);
   *taken = make_map(p.kmap, ap.c, ap.c.k, a->cache.dtype, p.box) &&
            make_map(p.vmap, ap.c, ap.c.v, a->cache.dtype, p.box) &&
@@ -303,8 +258,11 @@ sv_status tree_attention(const sv_tree_attention_args *a, sv_stream_t stream) {
   p.Hq = static_cast<int>(a->num_heads);
   p.G = p.Hq / p.c.heads;
   const TcLayout w = tc_layout(a->T, p.G, p.c.D);
-  if (tc_takes(a, p, w)) {
-    bool taken = false;
+  bool taken = false;
+  if (a->cache.dtype == SV_I4) {
+    const sv_status s = attn_i4(a, p, stream, &taken);
+    if (taken || s != SV_OK) return s;
+  } else if (tc_takes(a, p, w)) {
     const sv_status s = attn_tc(a, p, w, stream, &taken);
     if (taken || s != SV_OK) return s;
   }
