@@ -48,9 +48,9 @@ sv_status attn_i4(const sv_tree_attention_args *a, const AttnParams &ap, sv_stre
   p.slot_floats = ((c.D + 2) * p.slot_rows + 1 + 31) / 32 * 32;
   p.box = 8;  // a power of two that divides the block size, at most a tile
   while (p.box < i4::kT && c.bs % (2 * p.box) == 0) p.box *= 2;
+  if (!make_map(p.kmap, c, c.k, SV_I4, p.box) || !make_map(p.vmap, c, c.v, SV_I4, p.box)) return SV_OK;
   p.c = std::max(std::fabs(ap.scale_log2), kLeast);
   p.negate = ap.scale_log2 < 0.f;
-  if (!make_map(p.kmap, c, c.k, SV_I4, p.box) || !make_map(p.vmap, c, c.v, SV_I4, p.box)) return SV_OK;
   *taken = true;
   p.grid = std::min(nsm, kMaxGrid);
   p.ranges = static_cast<int>(std::min<int64_t>(p.grid, units * most));

@@ -397,31 +397,41 @@ def test_bad_lengths_and_halves_and_strides():
 
 
 @gpu
-def test_long_context_in_many_ranges():
-    """One unit cut into as many ranges as there are thread blocks, against the dense form in 64 bits on the GPU."""
+@pytest.mark.parametrize("B,Hkv,D,G,T,L,dt", [(1, 2, 128, 8, 1, 50001, "fp16"), (1, 2, 64, 4, 3, 39997, "bf16"),
+                                              (2, 8, 128, 8, 6, 33333, "bf16"), (3, 8, 64, 7, 2, 30000, "fp16"),
+                                              (2, 8, 128, 2, 3, 45000, "fp16")])
+def test_long_contexts(B, Hkv, D, G, T, L, dt):
+    """Units cut into many ranges, and ranges of many tiles, against the dense form in 64 bits on the GPU."""
     sv, _, _ = _pkg()
-    rng = np.random.default_rng(10)
-    for D, G, T, L in ((128, 8, 1, 50001), (64, 4, 3, 39997)):
-        s = attn_setup(rng, 1, T, 2 * G, 2, D, 64, [L], [T], "fp16", False)
-        lse = torch.zeros(1, T, 2 * G, device=DEV)
-        out = run(s, lse=lse)
-        k, v = sv.kv_read(s["c"][0], s["c"][1], i32(s["tables"]), i32([L + T]), max_len=L + T, dtype=torch.float32,
-                          k_scale=s["c"][2], v_scale=s["c"][3])
-        q = s["q"].double().view(1, T, 2, G, D)
-        z = torch.einsum("bthgd,bshd->bhtgs", q, k.double()) / math.sqrt(D)
-        hide = torch.arange(L + T, device=DEV) > (L + torch.arange(T, device=DEV))[:, None]
-        z = z.masked_fill(hide[None, None, :, None], -math.inf)
+    rng = np.random.default_rng(L)
+    Ls = [L - 1111 * b for b in range(B)]
+    s = attn_setup(rng, B, T, Hkv * G, Hkv, D, 64, Ls, [T] * B, dt, False)
+    lse = torch.zeros(B, T, Hkv * G, device=DEV)
+    out = run(s, lse=lse)
+    S = max(Ls) + T
+    K, V = sv.kv_read(s["c"][0], s["c"][1], i32(s["tables"]), i32([x + T for x in Ls]), max_len=S, dtype=torch.float32,
+                      k_scale=s["c"][2], v_scale=s["c"][3])
+    for b in range(B):
+        k, v = K[b].double(), V[b].double()
+        q = s["q"][b].double().view(T, Hkv, G, D)
+        z = torch.einsum("thgd,shd->htgs", q, k) / math.sqrt(D)
+        hide = torch.arange(S, device=DEV) > (Ls[b] + torch.arange(T, device=DEV))[:, None]
+        z = z.masked_fill(hide[None, :, None], -math.inf)
         p = z.softmax(-1)
-        w = torch.einsum("bhtgs,bshd->bthgd", p, v.double()).reshape(1, T, 2 * G, D)
-        a = torch.einsum("bhtgs,bshd->bthgd", p, v.double().abs()).reshape(1, T, 2 * G, D)
-        # Scores off by (D + 8) 2^-23 sum |q k|; probabilities and result rounded to fp16, those below its normal
-        # range by 2^-25 of the largest, whose share of the sum is p.max(), and values are below 16; sums of L terms.
-        ds = (D + 8) * 2.0 ** -23 * torch.einsum("bthgd,bshd->bhtgs", q.abs(), k.double().abs()).max() / math.sqrt(D)
-        rel = 2 * ds + 2.0 ** -19 + 2 * L * 2.0 ** -24
-        pm = p.amax(-1).permute(0, 2, 1, 3).reshape(1, T, 2 * G, 1)
-        tol = (2.0 ** -11 + rel) * a + 2.0 ** -11 * w.abs() + L * 2.0 ** -25 * pm * 16 + 2.0 ** -25
-        assert ((out.double() - w).abs() <= tol).all()
-        assert (lse.double() - z.logsumexp(-1).permute(0, 2, 1, 3).reshape(1, T, 2 * G)).abs().max() < 1e-3
+
+        def rows(x):
+            return torch.einsum("htgs,shd->thgd", p, x).reshape(T, Hkv * G, D)
+
+        w, a = rows(v), rows(v.abs())
+        # Scores off by (D + 8) 2^-23 sum |q k|; probabilities and result rounded to the type, in fp16 those below its
+        # normal range by 2^-25 of the largest, whose share of the sum is p.max(), and values are below 16; sums of S terms.
+        ds = (D + 8) * 2.0 ** -23 * torch.einsum("thgd,shd->htgs", q.abs(), k.abs()).max() / math.sqrt(D)
+        rel = 2 * ds + 2.0 ** -19 + 2 * S * 2.0 ** -24
+        pm = p.amax(-1).permute(1, 0, 2).reshape(T, Hkv * G, 1)
+        tol = (UNIT[dt] + rel) * a + UNIT[dt] * w.abs() + (S * 2.0 ** -25 * pm * 16 + 2.0 ** -25) * (dt == "fp16")
+        assert ((out[b].double() - w).abs() <= tol).all()
+        want = z.logsumexp(-1).permute(1, 0, 2).reshape(T, Hkv * G)
+        assert (lse[b].double() - want).abs().max() < 1e-3
 
 
 @gpu
