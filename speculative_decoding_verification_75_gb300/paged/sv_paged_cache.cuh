@@ -124,6 +124,31 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_write_kernel(const MovePar
   }
 }
 
+// Eight 4-bit codes times their scale as 16-bit numbers, exactly: a code's bits are a
+// fraction of 64 (bf16: 16), pairs are 16 bits apart.
+template <typename O>
+__device__ __forceinline__ uint4 values8(uint32_t w, uint32_t s) {
+  const uint32_t sv2 = s > SV_KV_I4_MAX_SCALE ? 0x7fff7fffu : O::kIsBf16 ? s * 0x00100010u + 0x38803880u : s * 0x00800080u + 0x04000400u;
+  constexpr uint32_t mask = O::kIsBf16 ? 0x00780078u : 0x00f000f0u, base = O::kIsBf16 ? 0x41804180u : 0x54005400u;
+  uint32_t y[4];                                   // elements i and i + 4
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int up = (O::kIsBf16 ? 3 : 4) - 4 * i;
+    const uint32_t x = up > 0 ? w << up : w >> -up;
+    uint32_t u;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(u) : "r"(x), "n"(mask), "r"(base));
+    if constexpr (O::kIsBf16) {
+      asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(u) : "r"(u), "r"(0xc1c0c1c0u));     // - 24
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y[i]) : "r"(u), "r"(sv2));
+    } else {
+      asm("add.rn.f16x2 %0, %1, %2;" : "=r"(u) : "r"(u), "r"(0xd480d480u));      // - 72
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[i]) : "r"(u), "r"(sv2));
+    }
+  }
+  return make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410), __byte_perm(y[0], y[1], 0x7632),
+                    __byte_perm(y[2], y[3], 0x7632));
+}
+
 // kv_read.  C: the cache's type, O: the output's.
 template <typename C, typename O>
 __global__ void __launch_bounds__(kMoveThreads) sv_kv_read_kernel(const MoveParams p) {
@@ -158,6 +183,13 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_read_kernel(const MovePara
   for (int i = 0; i < kMoveTokens; ++i) {
     if (i >= cnt) break;
     if (slot[i].data < 0) continue;
+    uint8_t *d = dst + i * step;
+    if constexpr (C::kBits == 4 && O::kBits == 16) {
+      if (p.vec) {
+        *reinterpret_cast<uint4 *>(d) = values8<O>(raw[i].x, sc[i]);
+        continue;
+      }
+    }
     float f[8];
     unpack8<C>(&raw[i], f);
     if constexpr (C::kScaled) {
@@ -165,7 +197,6 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_read_kernel(const MovePara
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] *= m;
     }
-    uint8_t *d = dst + i * step;
     if (p.vec) {
       pack8<O>(d, f);
     } else {

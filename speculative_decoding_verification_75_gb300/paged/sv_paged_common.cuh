@@ -178,7 +178,7 @@ template <>
 __device__ __forceinline__ void unpack8<I4>(const void *p, float (&f)[8]) {
   const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(static_cast<int>(w >> (4 * i) & 15u) - 8);
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float((w >> (4 * i) & 15u) | 0x4b000000u) - 8388616.f;   // 2^23 + c
 }
 
 template <typename E>

@@ -5,11 +5,11 @@
 // first R elements turn in pairs (a, b) by the angle of the token's position:
 // (a cos - b sin, b cos + a sin); pairs are (i, i + R / 2) or (2 i, 2 i + 1).
 //
-// Bound by HBM where there are many tokens: every element is read and written
-// once.  A lane holds 8 adjacent elements (16 bytes) of a row, D / 8 lanes a row;
-// the sum of squares and a pair's other half come by shuffles.  A warp takes
-// several rows of one token, so that the angles and weights of its 8 columns stay
-// in registers, and has the loads of kRopeRows rows in flight.
+// Every element is read and written once.  A lane holds 8 adjacent elements (16 bytes)
+// of a row, D / 8 lanes a row; the sum of squares and a pair's other half come by
+// shuffles.  A warp takes several steps of one token, each of a few rows of one kind
+// (queries, keys or values), so that the angles of its 8 columns stay in registers,
+// arithmetic is on pairs, and the loads of the next kRopeRows steps are in flight.
 #pragma once
 
 #include "sv_paged_quant.cuh"
@@ -18,7 +18,7 @@ namespace svp {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeRows = 4;
-constexpr int kRopeWarps = 152 * 32;   // warps that a batch is spread over at least
+constexpr int kRopeWarps = 152 * 48;   // warps that a batch is spread over at least
 
 struct RopeParams {
   Cache c;                       // c.k NULL: none
@@ -30,10 +30,11 @@ struct RopeParams {
   const float *cos_sin;          // [P, R]: R / 2 cosines, R / 2 sines
   const int32_t *positions;      // [B, T]
   const int64_t *slots;          // [B, T] or NULL
-  float eps;
+  float eps, inv_d;              // inv_d: 1 / D
   int B, T, Hq, Hkv, D, R, P;
   int lanes;                     // of a row: a power of two, at least D / 8
-  int rows, steps, runs;         // rows of a token; of a warp, in groups of 32 / lanes; warps of a token
+  int steps_q, steps_k, steps;   // of 32 / lanes rows of one kind: queries, keys, all of a token
+  int per, runs;                 // steps of a warp, warps of a token
   int vec;                       // rows on 16-byte boundaries
   uint32_t *status;
 };
@@ -52,7 +53,7 @@ __device__ __forceinline__ void store16(uint8_t *d, const uint4 &v, bool vec) {
 // Q: type of queries, keys and values; C: the cache's (Q: its own type, or no
 // cache); kPairs: neighbours turn together.
 template <typename Q, typename C, bool kPairs>
-__global__ void __launch_bounds__(kRopeThreads) sv_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 2) sv_rope_kernel(const RopeParams p) {
   sv::pdl_wait();
   sv::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -61,6 +62,38 @@ __global__ void __launch_bounds__(kRopeThreads) sv_rope_kernel(const RopeParams 
   if (token >= static_cast<int64_t>(p.B) * p.T) return;        // whole warps
   const int run = static_cast<int>(task - token * p.runs);
   const int b = static_cast<int>(token / p.T), t = static_cast<int>(token - static_cast<int64_t>(b) * p.T);
+  const int ch = lane & (p.lanes - 1), group = 32 / p.lanes, sub = lane / p.lanes;
+  const bool in = ch < p.D / 8;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  const int s_begin = run * p.per, s_end = min(s_begin + p.per, p.steps);
+  const int s_k = p.steps_q, s_v = p.steps_q + p.steps_k;      // first steps of keys and values
+  // Where the steps' rows come from: a pointer that moves on by a step's rows.
+  const uint8_t *src = nullptr;
+  int64_t src_step = 0;
+  int src_left = 0;              // rows of the kind from the lane's on
+  const auto aim = [&](int s) {
+    const bool is_q = s < s_k, is_k = s < s_v;
+    const int row = (s - (is_q ? 0 : is_k ? s_k : s_v)) * group + sub;
+    const int64_t head = is_q ? p.qsh : is_k ? p.ksh : p.vsh;
+    src = (is_q ? p.q + b * p.qsb + t * p.qst : is_k ? p.k + b * p.ksb + t * p.kst : p.v + b * p.vsb + t * p.vst) +
+          row * head + ch * 16;
+    src_step = group * head;
+    src_left = in ? (is_q ? p.Hq : p.Hkv) - row : 0;
+  };
+  uint4 raw[kRopeRows];
+  const auto fetch = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < kRopeRows; ++i) {
+      const int s = s0 + i;
+      raw[i] = none;
+      if (s >= s_end) continue;                                // the same for the warp
+      if (s == s_begin || s == s_k || s == s_v) aim(s);
+      if (src_left > 0) raw[i] = load16(src, p.vec);
+      src += src_step;
+      src_left -= group;
+    }
+  };
+  fetch(s_begin);                // on its way while the token's place and angles are looked up
 
   // The token's angle and its place in the cache.
   const int pos = ld32(p.positions + token);
@@ -69,25 +102,23 @@ __global__ void __launch_bounds__(kRopeThreads) sv_rope_kernel(const RopeParams 
     const uint2 w = ld64(p.slots + token);
     const int64_t slot = static_cast<int64_t>(static_cast<uint64_t>(w.y) << 32 | w.x);
     if (slot < 0) return;                                      // no token here
-    const int64_t id = slot / p.c.bs;
+    const int64_t id = slot < 0x80000000ll ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.c.bs) : slot / p.c.bs;
     if (id >= p.c.num_blocks) {
       if (run == 0 && lane == 0) report(p.status, SV_KV_BAD_BLOCK);
       return;
     }
     const int row = static_cast<int>(slot - id * p.c.bs);
-    at = id * p.c.block_bytes + static_cast<int64_t>(row) * (p.D / 8 * C::kBits);
-    sat = id * p.c.sblock_bytes + static_cast<int64_t>(row) * (p.D / SV_KV_GROUP);
+    at = id * p.c.block_bytes + static_cast<int64_t>(row) * (p.D / 8 * C::kBits) + ch * C::kBits;
+    sat = id * p.c.sblock_bytes + static_cast<int64_t>(row) * (p.D / SV_KV_GROUP) + ch / 4;
   }
   if (p.R > 0 && (pos < 0 || pos >= p.P)) {
     if (run == 0 && lane == 0) report(p.status, SV_KV_BAD_LENGTH);
     return;
   }
-  const int ch = lane & (p.lanes - 1), group = 32 / p.lanes, sub = lane / p.lanes;
-  const bool in = ch < p.D / 8;
-  // The lane's angles: cs[e], sn[e] of element e; the partner of element e is
-  // element e of lane `mate`, or (kPairs) its neighbour.  sn has the sign of the
+  // The lane's angles: cs[e], sn[e] of elements 2 e and 2 e + 1; an element's partner is
+  // the same one of lane `mate`, or (kPairs) its neighbour.  sn has the sign of the
   // partner's term.
-  float cs[8] = {}, sn[8] = {};
+  uint64_t cs[4] = {}, sn[4] = {};
   const int turned = min(max(p.R - 8 * ch, 0), 8);             // of the lane's elements, the first ones
   const float *angles = p.cos_sin + static_cast<int64_t>(pos) * p.R;
   int mate = lane;
@@ -98,9 +129,8 @@ __global__ void __launch_bounds__(kRopeThreads) sv_rope_kernel(const RopeParams 
       if (2 * e < turned) {
         const float c = __uint_as_float(static_cast<uint32_t>(ld32(reinterpret_cast<const int32_t *>(angles + j))));
         const float s = __uint_as_float(static_cast<uint32_t>(ld32(reinterpret_cast<const int32_t *>(angles + p.R / 2 + j))));
-        cs[2 * e] = cs[2 * e + 1] = c;
-        sn[2 * e] = -s;
-        sn[2 * e + 1] = s;
+        cs[e] = pair2(c, c);
+        sn[e] = pair2(-s, s);
       }
     }
   } else {
@@ -109,85 +139,119 @@ __global__ void __launch_bounds__(kRopeThreads) sv_rope_kernel(const RopeParams 
       const bool low = ch < half;
       mate = low ? lane + half : lane - half;
       const float *a = angles + (low ? ch : ch - half) * 8;
+      const float sign = low ? -1.f : 1.f;
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const uint4 c = ld128(a + e), s = ld128(a + p.R / 2 + e);
-        const uint32_t cu[4] = {c.x, c.y, c.z, c.w}, su[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          cs[e + k] = __uint_as_float(cu[k]);
-          sn[e + k] = low ? -__uint_as_float(su[k]) : __uint_as_float(su[k]);
-        }
+      for (int e = 0; e < 4; e += 2) {
+        const uint4 c = ld128(a + 2 * e), s = ld128(a + p.R / 2 + 2 * e);
+        cs[e] = pair2(__uint_as_float(c.x), __uint_as_float(c.y));
+        cs[e + 1] = pair2(__uint_as_float(c.z), __uint_as_float(c.w));
+        sn[e] = pair2(sign * __uint_as_float(s.x), sign * __uint_as_float(s.y));
+        sn[e + 1] = pair2(sign * __uint_as_float(s.z), sign * __uint_as_float(s.w));
       }
     }
   }
-  const uint4 none = make_uint4(0, 0, 0, 0);
   const uint4 wq = p.qw && in ? ld128(p.qw + ch * 16) : none, wk = p.kw && in ? ld128(p.kw + ch * 16) : none;
-  const int r0 = run * p.steps * group;
+  // Where the rows go, likewise: the output, and the cache's place of the row's head.
+  uint8_t *to = nullptr, *cell = nullptr, *cell_s = nullptr;
+  int64_t to_step = 0;
+  const int64_t cell_step = static_cast<int64_t>(group) * p.c.bs * (p.D / 8 * C::kBits);
+  const int64_t cell_s_step = static_cast<int64_t>(group) * p.c.bs * (p.D / SV_KV_GROUP);
+  int left = 0;
+  const auto aim_out = [&](int s) {
+    const bool is_q = s < s_k, is_k = s < s_v;
+    const int row = (s - (is_q ? 0 : is_k ? s_k : s_v)) * group + sub;
+    left = in ? (is_q ? p.Hq : p.Hkv) - row : 0;
+    const int64_t head = is_q ? p.qosh : p.kosh;
+    to = is_q ? p.qo + b * p.qosb + t * p.qost : is_k && p.ko ? p.ko + b * p.kosb + t * p.kost : nullptr;
+    if (to) to += row * head + ch * 16;
+    to_step = to ? group * head : 0;
+    if (!is_q && p.slots) {
+      cell = (is_k ? p.c.k : p.c.v) + at + static_cast<int64_t>(row) * p.c.bs * (p.D / 8 * C::kBits);
+      if (C::kScaled) cell_s = (is_k ? p.c.ks : p.c.vs) + sat + static_cast<int64_t>(row) * p.c.bs * (p.D / SV_KV_GROUP);
+    }
+  };
+  const bool normed = p.qw || p.kw;
 #pragma unroll 1
-  for (int s0 = 0; s0 < p.steps; s0 += kRopeRows) {
-    uint4 raw[kRopeRows];
+  for (int s0 = s_begin; s0 < s_end; s0 += kRopeRows) {
+    uint4 now[kRopeRows];
 #pragma unroll
-    for (int i = 0; i < kRopeRows; ++i) {
-      const int r = r0 + (s0 + i) * group + sub;
-      raw[i] = none;
-      if (in && s0 + i < p.steps && r < p.rows) {
-        const uint8_t *src = r < p.Hq ? p.q + b * p.qsb + t * p.qst + r * p.qsh
-                             : r < p.Hq + p.Hkv ? p.k + b * p.ksb + t * p.kst + (r - p.Hq) * p.ksh
-                                                : p.v + b * p.vsb + t * p.vst + (r - p.Hq - p.Hkv) * p.vsh;
-        raw[i] = load16(src + ch * 16, p.vec);
+    for (int i = 0; i < kRopeRows; ++i) now[i] = raw[i];
+    if (s0 + kRopeRows < s_end) fetch(s0 + kRopeRows);         // the next steps', meanwhile
+    // The steps' sums of squares side by side: alone each is a chain of shuffles.
+    float ss[kRopeRows];
+    if (normed && s0 < s_v) {
+#pragma unroll
+      for (int i = 0; i < kRopeRows; ++i) {
+        float f[8];
+        unpack8<Q>(&now[i], f);
+        uint64_t s2 = mul_pair(pair2(f[0], f[1]), pair2(f[0], f[1]));
+#pragma unroll
+        for (int e = 2; e < 8; e += 2) s2 = fma_pair(pair2(f[e], f[e + 1]), pair2(f[e], f[e + 1]), s2);
+        ss[i] = lower(s2) + upper(s2);
       }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        if (o >= p.lanes) break;
+#pragma unroll
+        for (int i = 0; i < kRopeRows; ++i) ss[i] += __shfl_xor_sync(kFull, ss[i], o);
+      }
+#pragma unroll
+      for (int i = 0; i < kRopeRows; ++i) ss[i] = rsqrtf(fmaf(ss[i], p.inv_d, p.eps));   // off by 2^-22
     }
 #pragma unroll
     for (int i = 0; i < kRopeRows; ++i) {
-      const int r = r0 + (s0 + i) * group + sub;
-      if (s0 + i >= p.steps || r0 + (s0 + i) * group >= p.rows) break;   // the same for the warp
-      const bool is_q = r < p.Hq, is_k = !is_q && r < p.Hq + p.Hkv, on = in && r < p.rows;
-      if (__any_sync(kFull, on && (is_q || is_k))) {           // not a warp of values alone
-        float x[8];
-        unpack8<Q>(&raw[i], x);
-        const bool norm = is_q ? p.qw != nullptr : p.kw != nullptr;
-        if (p.qw || p.kw) {
-          float ss = 0.f;
+      const int s = s0 + i;
+      if (s >= s_end) break;                                   // the same for the warp
+      if (s == s_begin || s == s_k || s == s_v) aim_out(s);
+      const bool is_q = s < s_k, on = left > 0;
+      if (s < s_v) {
+        float f[8];
+        unpack8<Q>(&now[i], f);
+        uint64_t x[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-          for (int o = 1; o < p.lanes; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
-          if (norm) {
-            const float f = 1.f / sqrtf(ss / static_cast<float>(p.D) + p.eps);
-            float w[8];
-            const uint4 ww = is_q ? wq : wk;
-            unpack8<Q>(&ww, w);
+        for (int e = 0; e < 4; ++e) x[e] = pair2(f[2 * e], f[2 * e + 1]);
+        if (is_q ? p.qw != nullptr : p.kw != nullptr) {
+          const uint64_t r2 = pair2(ss[i], ss[i]);
+          float w[8];
+          unpack8<Q>(is_q ? &wq : &wk, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * f * w[e];
+          for (int e = 0; e < 4; ++e) x[e] = mul_pair(mul_pair(x[e], r2), pair2(w[2 * e], w[2 * e + 1]));
+        }
+        if (p.R > 0) {
+          uint64_t y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t other = kPairs ? pair2(upper(x[e]), lower(x[e]))
+                                          : pair2(__shfl_sync(kFull, lower(x[e]), mate), __shfl_sync(kFull, upper(x[e]), mate));
+            y[e] = fma_pair(other, sn[e], mul_pair(x[e], cs[e]));
           }
-        }
-        float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float other = kPairs ? x[e ^ 1] : __shfl_sync(kFull, x[e], mate);
-          y[e] = e < turned ? fmaf(other, sn[e], x[e] * cs[e]) : x[e];   // not x + 0 * other: it may be infinite
+          for (int e = 0; e < 4; ++e)
+            if (2 * e < turned) x[e] = y[e];                   // not x + 0 * other: it may be infinite
         }
-        if (is_q || is_k) pack8<Q>(&raw[i], y);
-      }
-      if (on && is_q) store16(p.qo + b * p.qosb + t * p.qost + r * p.qosh + ch * 16, raw[i], p.vec);
-      if (on && is_k && p.ko) store16(p.ko + b * p.kosb + t * p.kost + (r - p.Hq) * p.kosh + ch * 16, raw[i], p.vec);
-      if (p.slots && __any_sync(kFull, on && !is_q)) {
-        const int h = is_k ? r - p.Hq : r - p.Hq - p.Hkv;
-        const bool put = on && !is_q;
-        uint8_t *dst = (is_k ? p.c.k : p.c.v) + at + static_cast<int64_t>(h) * p.c.bs * (p.D / 8 * C::kBits) + ch * C::kBits;
-        if constexpr (C::kScaled) {
-          typename Codes<C>::type codes;
-          const uint32_t sc = quantise8<Q>(raw[i], codes);
-          if (put) {
-            *reinterpret_cast<typename Codes<C>::type *>(dst) = codes;
-            if ((ch & 3) == 0)
-              (is_k ? p.c.ks : p.c.vs)[sat + static_cast<int64_t>(h) * p.c.bs * (p.D / SV_KV_GROUP) + ch / 4] =
-                  static_cast<uint8_t>(sc);
-          }
-        } else {
-          if (put) *reinterpret_cast<uint4 *>(dst) = raw[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[2 * e] = lower(x[e]);
+          f[2 * e + 1] = upper(x[e]);
         }
+        pack8<Q>(&now[i], f);
       }
+      if (on && to) store16(to, now[i], p.vec);
+      to += to_step;
+      left -= group;
+      if (is_q || !p.slots) continue;
+      if constexpr (C::kScaled) {
+        typename Codes<C>::type codes;
+        const uint32_t sc = quantise8<Q>(now[i], codes);
+        if (on) {
+          *reinterpret_cast<typename Codes<C>::type *>(cell) = codes;
+          if ((ch & 3) == 0) *cell_s = static_cast<uint8_t>(sc);
+        }
+        cell_s += cell_s_step;
+      } else {
+        if (on) *reinterpret_cast<uint4 *>(cell) = now[i];
+      }
+      cell += cell_step;
     }
   }
 }

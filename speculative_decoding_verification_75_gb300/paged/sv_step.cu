@@ -49,8 +49,8 @@ sv_status kv_reserve(const sv_kv_reserve_args *a, sv_stream_t stream) {
   int ranks = 1;
   while (ranks < kReserveCluster && ranks * (kReserveThreads / p.lanes) < p.B) ranks *= 2;
   while (ranks < kReserveCluster && (p.B + ranks - 1) / ranks > kReserveRequests) ranks *= 2;
-  p.per = (p.B + ranks - 1) / ranks;
   const int64_t tokens = a->B * a->T;
+  p.per = (p.B + ranks - 1) / ranks;
   p.fused = tokens <= int64_t{kReserveThreads} * ranks * kFusedTokens;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks);
@@ -145,20 +145,24 @@ sv_status qk_norm_rope(const sv_qk_norm_rope_args *a, sv_stream_t stream) {
   p.Hq = static_cast<int>(a->num_heads);
   p.Hkv = static_cast<int>(a->num_kv_heads);
   p.D = static_cast<int>(D);
+  p.inv_d = 1.f / static_cast<float>(D);
   p.R = static_cast<int>(R);
   p.P = static_cast<int>(a->num_positions);
   p.status = a->status;
   p.lanes = 1;
   while (p.lanes < D / 8) p.lanes *= 2;
-  p.rows = p.Hq + p.Hkv * (cached ? 2 : 1);
-  if (p.rows == 0) return SV_OK;
-  // A warp's rows: as many as leave kRopeWarps warps, whole turns of kRopeRows.
+  // Steps of whole rows of a kind; a warp's: as many as leave kRopeWarps warps, whole
+  // turns of kRopeRows.
+  const int group = 32 / p.lanes;
+  p.steps_q = (p.Hq + group - 1) / group;
+  p.steps_k = (p.Hkv + group - 1) / group;
+  p.steps = p.steps_q + p.steps_k * (cached ? 2 : 1);
+  if (p.steps == 0) return SV_OK;
   const int64_t tokens = a->B * a->T;
-  const int groups = (p.rows + 32 / p.lanes - 1) / (32 / p.lanes);
-  int64_t steps = std::min<int64_t>(std::max<int64_t>(tokens * groups / kRopeWarps, 1), groups);
-  if (steps > kRopeRows) steps = (steps + kRopeRows - 1) / kRopeRows * kRopeRows;
-  p.steps = static_cast<int>(steps);
-  p.runs = (groups + p.steps - 1) / p.steps;
+  int64_t per = std::min<int64_t>(std::max<int64_t>(tokens * p.steps / kRopeWarps, 1), p.steps);
+  if (per > kRopeRows) per = (per + kRopeRows - 1) / kRopeRows * kRopeRows;
+  p.per = static_cast<int>(per);
+  p.runs = (p.steps + p.per - 1) / p.per;
   const int64_t blocks = (tokens * p.runs + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (blocks > INT_MAX) return SV_ERR_INVALID_ARG;
   const int64_t cache = cached ? a->cache.dtype : a->dtype;
