@@ -10,6 +10,8 @@
 // shuffles.  A warp takes several steps of one token, each of a few rows of one kind
 // (queries, keys or values), so that the angles of its 8 columns stay in registers,
 // arithmetic is on pairs, and the loads of the next kRopeRows steps are in flight.
+// The columns' cosines and sines carry the weights, so that an element takes two
+// products, and the norm's factor comes last.
 #pragma once
 
 #include "sv_paged_quant.cuh"
@@ -115,42 +117,63 @@ __global__ void __launch_bounds__(kRopeThreads, 2) sv_rope_kernel(const RopePara
     if (run == 0 && lane == 0) report(p.status, SV_KV_BAD_LENGTH);
     return;
   }
-  // The lane's angles: cs[e], sn[e] of elements 2 e and 2 e + 1; an element's partner is
-  // the same one of lane `mate`, or (kPairs) its neighbour.  sn has the sign of the
-  // partner's term.
-  uint64_t cs[4] = {}, sn[4] = {};
+  // A row's elements 2 e, 2 e + 1 become x * own[e] + (their partners) * mate_by[e]: the
+  // angles' cosines times the weights, and the sines, with the sign of the partner's
+  // term, times the partner's weight.  A partner is the same element of lane `mate`, or
+  // (kPairs) the neighbour.
+  uint64_t own[4] = {}, mate_by[4] = {};
   const int turned = min(max(p.R - 8 * ch, 0), 8);             // of the lane's elements, the first ones
+  const int half = p.R / 16;                                   // lanes of a half
+  const bool low = ch < half;
+  const int mate = kPairs || !turned ? lane : low ? lane + half : lane - half;
   const float *angles = p.cos_sin + static_cast<int64_t>(pos) * p.R;
-  int mate = lane;
-  if (kPairs) {
+  const auto weigh = [&](const uint8_t *weight) {
+    float c[8], s[8], w[8], wm[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int j = ch * 4 + e;
-      if (2 * e < turned) {
-        const float c = __uint_as_float(static_cast<uint32_t>(ld32(reinterpret_cast<const int32_t *>(angles + j))));
-        const float s = __uint_as_float(static_cast<uint32_t>(ld32(reinterpret_cast<const int32_t *>(angles + p.R / 2 + j))));
-        cs[e] = pair2(c, c);
-        sn[e] = pair2(-s, s);
-      }
+    for (int e = 0; e < 8; ++e) {
+      c[e] = w[e] = 1.f;
+      s[e] = 0.f;
     }
-  } else {
-    const int half = p.R / 16;                                 // lanes of a half
-    if (turned) {
-      const bool low = ch < half;
-      mate = low ? lane + half : lane - half;
+    if (kPairs) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        if (e < turned) {
+          const float *a = angles + ch * 4 + e / 2;
+          c[e] = c[e + 1] = __uint_as_float(static_cast<uint32_t>(ld32(reinterpret_cast<const int32_t *>(a))));
+          s[e + 1] = __uint_as_float(static_cast<uint32_t>(ld32(reinterpret_cast<const int32_t *>(a + p.R / 2))));
+          s[e] = -s[e + 1];
+        }
+      }
+    } else if (turned) {
       const float *a = angles + (low ? ch : ch - half) * 8;
       const float sign = low ? -1.f : 1.f;
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const uint4 c = ld128(a + 2 * e), s = ld128(a + p.R / 2 + 2 * e);
-        cs[e] = pair2(__uint_as_float(c.x), __uint_as_float(c.y));
-        cs[e + 1] = pair2(__uint_as_float(c.z), __uint_as_float(c.w));
-        sn[e] = pair2(sign * __uint_as_float(s.x), sign * __uint_as_float(s.y));
-        sn[e + 1] = pair2(sign * __uint_as_float(s.z), sign * __uint_as_float(s.w));
+      for (int e = 0; e < 8; e += 4) {
+        const uint4 x = ld128(a + e), y = ld128(a + p.R / 2 + e);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w}, z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          c[e + k] = __uint_as_float(u[k]);
+          s[e + k] = sign * __uint_as_float(z[k]);
+        }
       }
     }
-  }
-  const uint4 wq = p.qw && in ? ld128(p.qw + ch * 16) : none, wk = p.kw && in ? ld128(p.kw + ch * 16) : none;
+    if (weight && in) {
+      const uint4 x = ld128(weight + ch * 16);
+      unpack8<Q>(&x, w);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wm[e] = kPairs ? w[e ^ 1] : w[e];
+    if (!kPairs && weight && turned) {
+      const uint4 x = ld128(weight + (low ? ch + half : ch - half) * 16);
+      unpack8<Q>(&x, wm);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      own[e] = pair2(c[2 * e] * w[2 * e], c[2 * e + 1] * w[2 * e + 1]);
+      mate_by[e] = pair2(s[2 * e] * wm[2 * e], s[2 * e + 1] * wm[2 * e + 1]);
+    }
+  };
   // Where the rows go, likewise: the output, and the cache's place of the row's head.
   uint8_t *to = nullptr, *cell = nullptr, *cell_s = nullptr;
   int64_t to_step = 0;
@@ -165,6 +188,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) sv_rope_kernel(const RopePara
     to = is_q ? p.qo + b * p.qosb + t * p.qost : is_k && p.ko ? p.ko + b * p.kosb + t * p.kost : nullptr;
     if (to) to += row * head + ch * 16;
     to_step = to ? group * head : 0;
+    if (is_k) weigh(is_q ? p.qw : p.kw);
     if (!is_q && p.slots) {
       cell = (is_k ? p.c.k : p.c.v) + at + static_cast<int64_t>(row) * p.c.bs * (p.D / 8 * C::kBits);
       if (C::kScaled) cell_s = (is_k ? p.c.ks : p.c.vs) + sat + static_cast<int64_t>(row) * p.c.bs * (p.D / SV_KV_GROUP);
@@ -205,29 +229,27 @@ __global__ void __launch_bounds__(kRopeThreads, 2) sv_rope_kernel(const RopePara
       if (s == s_begin || s == s_k || s == s_v) aim_out(s);
       const bool is_q = s < s_k, on = left > 0;
       if (s < s_v) {
-        float f[8];
+        float f[8], g[8];
         unpack8<Q>(&now[i], f);
+        if (kPairs) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] = f[e ^ 1];
+        } else if (p.R > 0) {
+          const uint4 o = make_uint4(__shfl_sync(kFull, now[i].x, mate), __shfl_sync(kFull, now[i].y, mate),
+                                     __shfl_sync(kFull, now[i].z, mate), __shfl_sync(kFull, now[i].w, mate));
+          unpack8<Q>(&o, g);
+        }
         uint64_t x[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = pair2(f[2 * e], f[2 * e + 1]);
-        if (is_q ? p.qw != nullptr : p.kw != nullptr) {
-          const uint64_t r2 = pair2(ss[i], ss[i]);
-          float w[8];
-          unpack8<Q>(is_q ? &wq : &wk, w);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = mul_pair(mul_pair(x[e], r2), pair2(w[2 * e], w[2 * e + 1]));
-        }
+        for (int e = 0; e < 4; ++e) x[e] = mul_pair(pair2(f[2 * e], f[2 * e + 1]), own[e]);
         if (p.R > 0) {
-          uint64_t y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint64_t other = kPairs ? pair2(upper(x[e]), lower(x[e]))
-                                          : pair2(__shfl_sync(kFull, lower(x[e]), mate), __shfl_sync(kFull, upper(x[e]), mate));
-            y[e] = fma_pair(other, sn[e], mul_pair(x[e], cs[e]));
-          }
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (2 * e < turned) x[e] = y[e];                   // not x + 0 * other: it may be infinite
+            if (2 * e < turned) x[e] = fma_pair(pair2(g[2 * e], g[2 * e + 1]), mate_by[e], x[e]);   // else it may be infinite
+        }
+        if (is_q ? p.qw != nullptr : p.kw != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = mul_pair(x[e], pair2(ss[i], ss[i]));
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
