@@ -1,11 +1,12 @@
 """Build ``lib/libspecverify.so`` (the CUDA verification library) in-tree.
 
-Three translation units (the verification step, the paged KV cache, what a step
-does before its attention), compiled in parallel for sm_103a only and linked, and beside them ``lib/_svkv.*.so``,
-the native module of ``kv.py`` (plain C++ against the installed PyTorch).  The
-results are git-ignored; every machine that runs the library builds them from
-source.  The library needs nvcc alone: where the module cannot be built (no g++,
-no PyTorch headers) it is installed all the same.
+Four translation units (the verification step, the paged KV cache, what a step
+does before its attention, attention over 4 bits), compiled in parallel for
+sm_103a only and linked, and beside them ``lib/_svkv.*.so``, the native module of
+``kv.py`` (plain C++ against the installed PyTorch).  The results are git-ignored;
+every machine that runs the library builds them from source.  The library needs
+nvcc alone: where the module cannot be built (no g++, no PyTorch headers) it is
+installed all the same.
 """
 from __future__ import annotations
 
@@ -112,8 +113,8 @@ def _build_binding(run, tag: str) -> None:
         run(binding_command(tmp))
         os.replace(tmp, path)
     except (OSError, subprocess.CalledProcessError) as e:
-        warnings.warn(f"{path.name} could not be built, kv_write, kv_read, kv_compact and "
-                      f"tree_attention are not available from Python: {e}")
+        warnings.warn(f"{path.name} could not be built, the functions of kv.py are not "
+                      f"available from Python: {e}")
 
 
 def build(force: bool = False, verbose: bool = False) -> Path:

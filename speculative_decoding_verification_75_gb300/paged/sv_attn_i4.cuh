@@ -30,13 +30,28 @@
 // rows' references m are shared by the 128 keys and live in shared memory; P is
 // 2^(x - m), and only when a score exceeds its reference by more than 2^8 (a vote of
 // the group, once a tile) are the references raised and O^T's columns rescaled; that
-// path also does the first tile of a unit and the tiles that hold new tokens, with
-// their masks.  A thread's parts of the rows' sums are columns of tensor memory, not
-// registers: then every loop over rows has one copy of its body.  (Unrolled, the
-// code of all roles together missed the instruction cache: 642 us for 128 requests.)
+// path also does the first tile of a unit.  A thread's parts of the rows' sums are
+// columns of tensor memory, not registers: then every loop over rows has one copy of
+// its body.  (Unrolled, the code of all roles together missed the instruction cache:
+// 642 us for 128 requests, 382 so.)
+//
+// Roles.  K, V, their products and the softmax are pipelined through two places each
+// (P: three) in tensor or shared memory; even and odd tiles have producers and widening
+// warps of their own, for each is a chain of latencies.  (One producer for K and one for
+// V took 1800 cycles a tile and bound the kernel; copies by the widening warps
+// themselves, without producers, were no faster: 384 us for 128 requests, 364 so.)
 //
 // Work, ranges, cut units, marked units and the second kernel are those of
 // sv_attn_tc.cuh, with one range for a thread block.
+//
+// Measured, both kernels together:
+//   128 x 6 tokens, 64 heads on 8 of 128, 500-8000 keys  364 us, 1.7 TB/s: a softmax
+//                                                warp's chain, about 1300 cycles a tile
+//                                                (wait, vote, fence) and 400 per 8 rows
+//   16 trees of 64, 32 on 8, 1000-8000 keys      208 us, 268 TFLOP/s: the same; units of
+//                                                64 rows take the keys four times
+//   131071 keys, 1 token, 64 on 8                57 us, 2.5 TB/s: the same chain
+//   500 keys, 1 token, 14 on 2 of 64             10 us: start, first data, join
 #pragma once
 
 #include "sv_attn_tc.cuh"

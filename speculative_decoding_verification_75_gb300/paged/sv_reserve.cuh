@@ -8,7 +8,9 @@
 //
 // Bound by latencies (lengths -> table -> sum over the requests -> free list ->
 // table -> slots): one launch, whose thread blocks form one cluster and exchange
-// their sums through shared memory.
+// their sums through shared memory (8 requests of 6 tokens: 5.7 us; 256 trees of 64
+// nodes: 7.5 us and 5.8 us of a second kernel, on all SMs, for the slots and positions:
+// with 8 on each thread of the cluster the one kernel takes 14 us).
 #pragma once
 
 #include "sv_paged_common.cuh"
