@@ -106,20 +106,37 @@ __global__ void __launch_bounds__(kMoveThreads) sv_kv_write_kernel(const MovePar
   uint8_t *dsc = C::kScaled
                      ? (q.is_v ? p.c.vs : p.c.ks) + static_cast<int64_t>(q.h) * p.c.bs * srow + q.d8 / 4
                      : nullptr;
+  if constexpr (C::kBits == 4) {
 #pragma unroll
-  for (int i = 0; i < kMoveTokens; ++i) {
-    if (i >= cnt) break;  // the same for every thread
-    const Slot s = slot[i];
-    const bool put = q.on && s.data >= 0;
-    if constexpr (C::kScaled) {
-      typename Codes<C>::type codes;
-      const uint32_t sc = quantise8<Q>(raw[i], codes);
-      if (put) {
-        *reinterpret_cast<typename Codes<C>::type *>(dst + s.data) = codes;
-        if ((q.d8 & 3) == 0) dsc[s.scale] = static_cast<uint8_t>(sc);
+    for (int i = 0; i < kMoveTokens; i += 4) {
+      if (i >= cnt) break;  // the same for every thread
+      uint32_t codes[4];
+      const uint32_t sc = quantise4x8<Q>(raw + i, codes);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!q.on || i + j >= cnt) continue;
+        const int64_t at = slot[i + j].data;
+        if (at >= 0) *reinterpret_cast<uint32_t *>(dst + at) = codes[j];
       }
-    } else {
-      if (put) *reinterpret_cast<uint4 *>(dst + s.data) = raw[i];
+      const int mine = i + (threadIdx.x & 3);
+      if (q.on && mine < cnt && slot[mine].scale >= 0) dsc[slot[mine].scale] = static_cast<uint8_t>(sc);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kMoveTokens; ++i) {
+      if (i >= cnt) break;  // the same for every thread
+      const Slot s = slot[i];
+      const bool put = q.on && s.data >= 0;
+      if constexpr (C::kScaled) {
+        typename Codes<C>::type codes;
+        const uint32_t sc = quantise8<Q>(raw[i], codes);
+        if (put) {
+          *reinterpret_cast<typename Codes<C>::type *>(dst + s.data) = codes;
+          if ((q.d8 & 3) == 0) dsc[s.scale] = static_cast<uint8_t>(sc);
+        }
+      } else {
+        if (put) *reinterpret_cast<uint4 *>(dst + s.data) = raw[i];
+      }
     }
   }
 }
