@@ -26,7 +26,7 @@
 //      4 g + i, whose scale is q's.
 // fp16 numbers are kept at 1/16 of their value: 72 f is then a number of the type.
 //
-// Softmax.  A thread has one key and half of the rows: two groups of four warps.  The
+// Softmax.  A thread has one key and every second eight rows: two groups of four warps.  The
 // rows' references m are shared by the 128 keys and live in shared memory; P is
 // 2^(x - m), and only when a score exceeds its reference by more than 2^8 (a vote of
 // the group, once a tile) are the references raised and O^T's columns rescaled; that
@@ -45,10 +45,10 @@
 // sv_attn_tc.cuh, with one range for a thread block.
 //
 // Measured, both kernels together:
-//   128 x 6 tokens, 64 heads on 8 of 128, 500-8000 keys  364 us, 1.7 TB/s: a softmax
+//   128 x 6 tokens, 64 heads on 8 of 128, 500-8000 keys  358 us, 1.7 TB/s: a softmax
 //                                                warp's chain, about 1300 cycles a tile
 //                                                (wait, vote, fence) and 400 per 8 rows
-//   16 trees of 64, 32 on 8, 1000-8000 keys      208 us, 268 TFLOP/s: the same; units of
+//   16 trees of 64, 32 on 8, 1000-8000 keys      215 us, 260 TFLOP/s: the same; units of
 //                                                64 rows take the keys four times
 //   131071 keys, 1 token, 64 on 8                57 us, 2.5 TB/s: the same chain
 //   500 keys, 1 token, 14 on 2 of 64             10 us: start, first data, join
@@ -329,15 +329,17 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attn_i4_kernel(const __grid_co
     uint32_t tiles = 0;
     const int swizzle = (my & 7) << 4;
     uint8_t *prow = sp + my * 128;                  // this key's place in the tile's P
+    const int mine = (my / kChunk * 2 + grp) * kChunk + my % kChunk;   // the row that the thread looks after
 #pragma unroll 1
     while (walk.on) {
       const Walk sg = walk;
       const Req &r = sg.r;
       const int nt = sg.t1 - sg.t0, seg = sg.seg;
       const int row0 = sg.mp * p.unit_rows, rows = rows_of(sg);
-      // The group's rows [g0, g1) of the unit; none of them may be real.
-      const int half = (rows + kUnit - 1) / kUnit * (kUnit / 2), g0 = grp * half;
-      const int g1 = g0 < rows ? g0 + half : g0;
+      // The group's rows of the unit: every second eight, from g0 on, whatever the unit's
+      // size: a group may be done with a unit before the other one, and what it then
+      // writes (references, sums) must not be the other's.  There may be none.
+      const int g0 = grp * kChunk, g1 = (rows + kChunk - 1) / kChunk * kChunk;
       const int full_end = sg.new0();               // every row sees these
       const uint32_t col_o = lanes + S::kColO, col_l = lanes + S::kColL;
 #pragma unroll 1
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attn_i4_kernel(const __grid_co
             }
           }
         }
-        if (g1 == g0) {                             // no row: in step with the other group, no more
+        if (g0 >= rows) {                           // no row: in step with the other group, no more
           if (ok && !(ok = wait_for(&bars.s_full[buf], round, err))) refs.dead[grp] = 1;   // seen below by all
           if (ok && lane == 0) sv::mbar_arrive(sv::smem_addr(&bars.p_ready[tiles & 3]));
           prow += S::kPBytes;
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attn_i4_kernel(const __grid_co
           // A row that has seen nothing yet has the largest float for its -m: any score
           // above -inf then asks for a reference.
 #pragma unroll 1
-          for (int row = g0; row < g1; row += kChunk) {
+          for (int row = g0; row < g1; row += 2 * kChunk) {
             uint32_t x[kChunk], l[kChunk];
             tc_ld8(col_s + row, x);
             tc_ld8(col_l + row, l);
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attn_i4_kernel(const __grid_co
           tc_wait_st();
           if (good) {
 #pragma unroll 1
-            for (int row = g0; row < g1; row += kChunk) {
+            for (int row = g0; row < g1; row += 2 * kChunk) {
               uint32_t x[kChunk];
               tc_ld8(col_s + row, x);
               if (fast) {
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attn_i4_kernel(const __grid_co
             ok = false;
             break;
           }
-          const int row = g0 + my;
+          const int row = mine;
           bool up = false;
           if (row < g1) {
             const float mt = fmaxf(fmaxf(refs.top[0][row], refs.top[1][row]), fmaxf(refs.top[2][row], refs.top[3][row]));
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attn_i4_kernel(const __grid_co
           up = vote(grp, up);
           tc_fence_after();
 #pragma unroll 1
-          for (int row = g0; row < g1; row += kChunk) {
+          for (int row = g0; row < g1; row += 2 * kChunk) {
             uint32_t x[kChunk], l[kChunk], pk[kChunk / 2];
             if (j > 0) {
               tc_ld8(col_l + row, l);
@@ -524,12 +526,12 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attn_i4_kernel(const __grid_co
         prow += S::kPBytes;
         if (prow >= raw) prow -= kPlaces * S::kPBytes;
       }
-      if (!ok && g1 > g0) break;                    // the whole group
+      if (!ok && g0 < rows) break;                   // the whole group
       next_segment(a, unit, walk);
 
       // The warp's part of the rows' sums: a butterfly whose halves keep half of the rows each.
 #pragma unroll 1
-      for (int row = g0; row < g1; row += kChunk) {
+      for (int row = g0; row < g1; row += 2 * kChunk) {
         uint32_t l[kChunk];
         tc_ld8(col_l + row, l);
         tc_wait_ld(l);
@@ -566,9 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attn_i4_kernel(const __grid_co
         const int t = (row0 + row) / a.G, g = row0 + row - t * a.G;
         return (static_cast<int64_t>(sg.b) * a.bt.T + t) * a.Hq + sg.h * a.G + g;
       };
-      const int end = min(g1, rows);                // of the group's real rows
-      if (g0 + my < end) {
-        const int row = g0 + my;
+      if (mine < rows) {
+        const int row = mine;
         const float l = (refs.top[0][row] + refs.top[1][row]) + (refs.top[2][row] + refs.top[3][row]);
         const float m = l == 0.f ? -INFINITY : refs.m[row];
         // What O is multiplied by; 0 where the row has seen nothing.
@@ -587,21 +588,21 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attn_i4_kernel(const __grid_co
       if (bad && whole) marked = true;
       group_sync(grp);
       const int dim = 32 * wq + 4 * (lane & 7) + (lane >> 3);
-      if (!bad && wq < S::kGroups && g0 < end) {
-        uint8_t *to = a.out + (out_row(g0) * D + dim) * 2;
-        int head = (row0 + g0) % a.G;
+      if (!bad && wq < S::kGroups && g0 < rows) {
         float *const part = whole ? nullptr : slot + static_cast<size_t>(dim >> 2) * p.slot_rows * 4 + (dim & 3);
 #pragma unroll 1
-        for (int row = g0; row < end; row += kChunk) {
+        for (int row = g0; row < rows; row += 2 * kChunk) {
           uint32_t o[kChunk];
           tc_ld8(col_o + row, o);
           tc_wait_ld(o);
           const float4 f0 = *reinterpret_cast<const float4 *>(&refs.factor[row]);
           const float4 f1 = *reinterpret_cast<const float4 *>(&refs.factor[row + 4]);
           const float fs[kChunk] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+          uint8_t *to = a.out + (out_row(row) * D + dim) * 2;
+          int head = (row0 + row) % a.G;
 #pragma unroll
           for (int k = 0; k < kChunk; ++k) {
-            if (row + k < end) {
+            if (row + k < rows) {
               const float y = fs[k] == 0.f ? 0.f : __uint_as_float(o[k]) * fs[k];   // not 0 * O: it may be NaN
               if (whole) {
                 store1<Q>(to, y);

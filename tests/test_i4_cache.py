@@ -435,6 +435,23 @@ def test_long_contexts(B, Hkv, D, G, T, L, dt):
 
 
 @gpu
+@pytest.mark.parametrize("T,G,D,dt", [(3, 8, 64, "bf16"), (9, 8, 128, "fp16"), (7, 4, 64, "fp16"), (64, 1, 128, "bf16")])
+def test_units_of_different_sizes_follow_each_other(T, G, D, dt):
+    """A thread block's units of few and many rows in turn: nothing of one may reach the one before, however
+    its warps are timed, so every run gives the same."""
+    rng = np.random.default_rng(T)
+    B, Hkv = 64, 8
+    L = [int(x) for x in rng.integers(100, 200, B)]
+    n = [int(x) for x in rng.integers(1, T + 1, B)]
+    s = attn_setup(rng, B, T, Hkv * G, Hkv, D, 16, L, n, dt, False)
+    want = check(s, dt)
+    for _ in range(12):
+        out = torch.full_like(want, 9.0)
+        run(s, out)
+        assert torch.equal(out, want)
+
+
+@gpu
 def test_graph_streams_and_shared_workspace():
     """Captured and replayed on new contents; on a side stream; one workspace for several sizes."""
     sv, _, kv = _pkg()
