@@ -13,10 +13,11 @@
 // The columns' cosines and sines carry the weights, so that an element takes two
 // products, and the norm's factor comes last.
 //
-// Measured: 8 prompts of up to 4096 tokens, 32 heads on 8, into a bf16 cache: 111 us, 5.5
-// TB/s, by the bytes in flight (with 4 steps a turn and 16 warps of 128 registers on an
-// SM 145; one step a turn and 32 warps 130); 128 x 6 tokens, 64 heads on 8: 9.5 us, in one
-// wave of warps (10.8 with twice as many, each with half of the steps).
+// Measured: 8 prompts of up to 4096 tokens, 32 heads on 8, into a bf16 cache: 115 us, 5.3
+// TB/s, by its instructions (issue slots 81 % busy, 28 warps of 72 registers on an SM; with
+// 4 steps a turn and 16 warps of 128 registers 145, one step a turn and 32 warps 130);
+// 128 x 6 tokens, 64 heads on 8: 9.7 us (10.8 with twice as many warps, each with half of
+// the steps).
 #pragma once
 
 #include "sv_paged_quant.cuh"
@@ -37,7 +38,8 @@ struct RopeParams {
   const float *cos_sin;          // [P, R]: R / 2 cosines, R / 2 sines
   const int32_t *positions;      // [B, T]
   const int64_t *slots;          // [B, T] or NULL
-  float eps, inv_d;              // inv_d: 1 / D
+  float eps, root_eps, inv_d;    // root_eps: eps^(1/2), inv_d: 1 / D
+  float least;                   // kLeastSquares, or 0 where eps is kLeastEps or more
   int B, T, Hq, Hkv, D, R, P;
   int lanes;                     // of a row: a power of two, at least D / 8
   int steps_q, steps_k, steps;   // of 32 / lanes rows of one kind: queries, keys, all of a token
@@ -55,6 +57,49 @@ __device__ __forceinline__ void store16(uint8_t *d, const uint4 &v, bool vec) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     *reinterpret_cast<uint16_t *>(d + 2 * i) = static_cast<uint16_t>(u[i >> 1] >> (16 * (i & 1)));
+}
+
+// bf16 reaches as far as fp32: a row's squares may leave it, and so may its products with
+// the weights, before the norm's factor.  Where a lane's squares sum up to kMostSquares
+// at most neither does, for weights below 2^64 (others are taken at 2^-64, and the factor
+// at 2^64): |x| <= 2^40, |x w| <= 2^104.  Nor is anything lost below 2^-149 while the
+// factor is at most 2^15, which eps holds; where eps is below 2^-30, kLeastSquares.  Rows
+// outside are moved by a power of two first.  (The check costs prompts 111 -> 115 us,
+// drafts 9.5 -> 9.7; in line, where registers for it left 6 blocks on an SM instead of 7,
+// 119 and 125.)
+constexpr uint32_t kHeavy = (127u + 64u) << 7;   // 2^64 in bf16
+constexpr float kMostSquares = 0x1p80f, kLeastSquares = 0x1p-20f, kLeastEps = 0x1p-30f;
+
+__device__ __forceinline__ float squares8(const float (&f)[8]) {
+  uint64_t s2 = mul_pair(pair2(f[0], f[1]), pair2(f[0], f[1]));
+#pragma unroll
+  for (int e = 2; e < 8; e += 2) s2 = fma_pair(pair2(f[e], f[e + 1]), pair2(f[e], f[e + 1]), s2);
+  return lower(s2) + upper(s2);
+}
+
+// A row moved by the power of two that takes the larger of its largest magnitude and
+// eps^(1/2) to 2^57, exactly but for what lies 2^180 below that, and its lane's sum of
+// squares, to which the row's first lane adds what eps becomes beside itself (eps is added
+// to the mean later: at most 2^100, where that is 2^106 at least).  By the whole warp.
+struct Moved {
+  uint4 row;
+  float squares;
+};
+__device__ __noinline__ Moved tame(uint4 row, float root_eps, float eps, int D, int lanes, bool first) {
+  uint32_t big = largest8<BF16>(row);
+#pragma unroll 1
+  for (int o = 1; o < lanes; o <<= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
+  big = max(big, __float_as_uint(root_eps) >> 16);
+  const int e = 184 - static_cast<int>(big >> 7);
+  const float r1 = __uint_as_float(static_cast<uint32_t>(127 + (e >> 1)) << 23);
+  const float r2 = __uint_as_float(static_cast<uint32_t>(127 + e - (e >> 1)) << 23);
+  float f[8];
+  unpack8<BF16>(&row, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = f[i] * r1 * r2;
+  pack8<BF16>(&row, f);
+  const float root = root_eps * r1 * r2;
+  return Moved{row, squares8(f) + (first ? fmaf(root, root, -eps) * static_cast<float>(D) : 0.f)};
 }
 
 // Q: type of queries, keys and values; C: the cache's (Q: its own type, or no
@@ -133,8 +178,10 @@ __global__ void __launch_bounds__(kRopeThreads, 6) sv_rope_kernel(const RopePara
   const bool low = ch < half;
   const int mate = kPairs || !turned ? lane : low ? lane + half : lane - half;
   const float *angles = p.cos_sin + static_cast<int64_t>(pos) * p.R;
+  float lift = 1.f;                                            // the weights are at 1 / lift
   const auto weigh = [&](const uint8_t *weight) {
     float c[8], s[8], w[8], wm[8];
+    bool heavy = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       c[e] = w[e] = 1.f;
@@ -167,12 +214,24 @@ __global__ void __launch_bounds__(kRopeThreads, 6) sv_rope_kernel(const RopePara
     if (weight && in) {
       const uint4 x = ld128(weight + ch * 16);
       unpack8<Q>(&x, w);
+      heavy = Q::kIsBf16 && largest8<Q>(x) >= kHeavy;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) wm[e] = kPairs ? w[e ^ 1] : w[e];
     if (!kPairs && weight && turned) {
       const uint4 x = ld128(weight + (low ? ch + half : ch - half) * 16);
       unpack8<Q>(&x, wm);
+    }
+    if (Q::kIsBf16) {
+      lift = 1.f;
+      if (__any_sync(kFull, heavy)) {
+        lift = 0x1p64f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          w[e] *= 0x1p-64f;
+          wm[e] *= 0x1p-64f;
+        }
+      }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -214,10 +273,25 @@ __global__ void __launch_bounds__(kRopeThreads, 6) sv_rope_kernel(const RopePara
       for (int i = 0; i < kRopeRows; ++i) {
         float f[8];
         unpack8<Q>(&now[i], f);
-        uint64_t s2 = mul_pair(pair2(f[0], f[1]), pair2(f[0], f[1]));
+        ss[i] = squares8(f);
+      }
+      if constexpr (Q::kIsBf16) {
+        float top = ss[0], low = ss[0];
 #pragma unroll
-        for (int e = 2; e < 8; e += 2) s2 = fma_pair(pair2(f[e], f[e + 1]), pair2(f[e], f[e + 1]), s2);
-        ss[i] = lower(s2) + upper(s2);
+        for (int i = 1; i < kRopeRows; ++i) {
+          top = fmaxf(top, ss[i]);
+          low = fminf(low, ss[i]);
+        }
+        if (__any_sync(kFull, top > kMostSquares || low < p.least)) {
+#pragma unroll
+          for (int i = 0; i < kRopeRows; ++i) {
+            if (s0 + i < s_k ? p.qw != nullptr : s0 + i < s_v && p.kw) {   // the same for the warp
+              const Moved y = tame(now[i], p.root_eps, p.eps, p.D, p.lanes, ch == 0);
+              now[i] = y.row;
+              ss[i] = y.squares;
+            }
+          }
+        }
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -254,8 +328,9 @@ __global__ void __launch_bounds__(kRopeThreads, 6) sv_rope_kernel(const RopePara
             if (2 * e < turned) x[e] = fma_pair(pair2(g[2 * e], g[2 * e + 1]), mate_by[e], x[e]);   // else it may be infinite
         }
         if (is_q ? p.qw != nullptr : p.kw != nullptr) {
+          const float by = Q::kIsBf16 ? ss[i] * lift : ss[i];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = mul_pair(x[e], pair2(ss[i], ss[i]));
+          for (int e = 0; e < 4; ++e) x[e] = mul_pair(x[e], pair2(by, by));
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {

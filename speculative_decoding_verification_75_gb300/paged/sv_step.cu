@@ -140,6 +140,8 @@ sv_status qk_norm_rope(const sv_qk_norm_rope_args *a, sv_stream_t stream) {
   p.positions = a->positions;
   p.slots = a->slots;
   p.eps = static_cast<float>(a->eps);
+  p.root_eps = static_cast<float>(std::sqrt(a->eps));
+  p.least = p.eps < kLeastEps ? kLeastSquares : 0.f;
   p.B = static_cast<int>(a->B);
   p.T = static_cast<int>(a->T);
   p.Hq = static_cast<int>(a->num_heads);

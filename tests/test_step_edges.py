@@ -1,0 +1,97 @@
+"""Calls of a step's operators at the edges of what they take."""
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as ref
+import step_ref as sref
+from test_paged_kv import DEV, gpu, i32
+from test_step_ops import TD, angles
+
+
+def _pkg():
+    import speculative_decoding_verification_75_gb300 as sv
+    from speculative_decoding_verification_75_gb300 import api, kv
+    return sv, api, kv
+
+
+# ------------------------------------------------- rows at the ends of fp32 ----
+
+def close_bf16(got, x, w, cs, pos, eps, pairs):
+    """fp32's roundings as step_ref derives them, one rounding to bf16 (half a step, 2^-134 where it is subnormal)."""
+    want, tol = sref.norm_rope(ref.to64(x), None if w is None else ref.to64(w), cs.astype(np.float64), pos, eps, pairs)
+    tol = tol + 2.0 ** -8 * (np.abs(want) + tol) + 2.0 ** -134
+    got = ref.to64(got)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) / tol).max())
+
+
+@gpu
+@pytest.mark.parametrize("D,R,pairs", [(64, 64, False), (128, 64, True), (96, 32, False), (8, 0, False), (256, 256, False)])
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-30])
+def test_norms_of_rows_near_the_ends_of_fp32(D, R, pairs, eps):
+    """Rows whose squares fp32 does not hold, too large and too small; rows of one turn that are ordinary."""
+    sv, _, _ = _pkg()
+    rng = np.random.default_rng(D)
+    e = np.array([0, 63, 64, 70, 100, 124, 0, -3, -20, -64, -70, -100, -122, 5, 50, -50])
+    x = rng.standard_normal((2, 8, 12, D)).clip(-3.9, 3.9) * 2.0 ** rng.permutation(np.resize(e, (2 * 8 * 12)))\
+        .reshape(2, 8, 12, 1)
+    x = torch.from_numpy(x).bfloat16().to(DEV)
+    x[0, 0, 0, :] = 3e38
+    x[0, 1, 1, :2] = torch.tensor([-3.3e38, 1e-30], device=DEV).bfloat16()
+    q, k = x.split([9, 3], 2)
+    cs, pos = angles(50, R), rng.integers(0, 50, (2, 8))
+    wq, wk = (torch.from_numpy(1 + 0.3 * rng.standard_normal(D)).bfloat16().to(DEV) for _ in range(2))
+    f = (torch.from_numpy(cs).to(DEV), i32(pos))
+    out, ko = sv.qk_norm_rope(q, k, *f, wq, wk, eps=eps, interleaved=pairs)
+    close_bf16(out, q, wq, cs, pos, eps, pairs)
+    close_bf16(ko, k, wk, cs, pos, eps, pairs)
+    # Only one of the two has a norm: the other is the same as without any.
+    out, ko = sv.qk_norm_rope(q, k, *f, None, wk, eps=eps, interleaved=pairs)
+    close_bf16(ko, k, wk, cs, pos, eps, pairs)
+    assert torch.equal(out, sv.qk_norm_rope(q, k, *f, eps=eps, interleaved=pairs)[0])
+
+
+@gpu
+@pytest.mark.parametrize("big", [2.0 ** 70, 2.0 ** 100, 2.0 ** 120, 2.0 ** -70, 2.0 ** -100])
+@pytest.mark.parametrize("D,R,pairs", [(64, 64, False), (80, 40, True)])
+def test_norms_with_weights_near_the_ends_of_fp32(big, D, R, pairs):
+    sv, _, _ = _pkg()
+    rng = np.random.default_rng(D)
+    x = rng.standard_normal((1, 6, 5, D)) * 2.0 ** rng.integers(-10, 34, (1, 6, 5, 1))
+    x = torch.from_numpy(x).bfloat16().to(DEV)
+    x[0, 0, 0] *= 2.0 ** 80
+    q, k = x.split([3, 2], 2)
+    cs, pos = angles(50, R), rng.integers(0, 50, (1, 6))
+    w = torch.from_numpy((1 + 0.3 * rng.standard_normal(D)) * big).bfloat16().to(DEV)
+    f = (torch.from_numpy(cs).to(DEV), i32(pos))
+    out, ko = sv.qk_norm_rope(q, k, *f, w, w, eps=1e-6, interleaved=pairs)
+    close_bf16(out, q, w, cs, pos, 1e-6, pairs)
+    close_bf16(ko, k, w, cs, pos, 1e-6, pairs)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_norms_of_rows_that_are_not_finite(dt):
+    """An infinity's row: x / inf is 0 for what is finite, and NaN for the infinity; a NaN's row is NaN; others stay."""
+    sv, _, _ = _pkg()
+    rng = np.random.default_rng(2)
+    x = torch.from_numpy(rng.standard_normal((1, 2, 6, 64)) * 4).to(TD[dt]).to(DEV)
+    clean = x.clone()
+    x[0, 0, 1, 5] = float("inf")
+    x[0, 1, 2, 40] = float("nan")
+    big = 2.0 ** 100 if dt == "bf16" else 60000.0
+    x[0, 0, 1, 6] = big
+    w = torch.full((64,), big, dtype=TD[dt], device=DEV)
+    cs = torch.zeros(1, 0, device=DEV)
+    pos = i32([[0, 0]])
+    q, k = x.split([4, 2], 2)
+    out, _ = sv.qk_norm_rope(q, k, cs, pos, w, w)
+    want, _ = sv.qk_norm_rope(*clean.split([4, 2], 2), cs, pos, w, w)
+    nan = torch.zeros_like(out, dtype=torch.bool)
+    nan[0, 0, 1, 5] = True
+    nan[0, 1, 2] = True
+    assert torch.equal(out.isnan(), nan)
+    zero = torch.zeros_like(nan)
+    zero[0, 0, 1] = True
+    assert (out[zero & ~nan] == 0).all() and torch.equal(out[~zero & ~nan], want[~zero & ~nan])
