@@ -51,6 +51,8 @@ sv_status attn_i4(const sv_tree_attention_args *a, const AttnParams &ap, sv_stre
   if (!make_map(p.kmap, c, c.k, SV_I4, p.box) || !make_map(p.vmap, c, c.v, SV_I4, p.box)) return SV_OK;
   p.c = std::max(std::fabs(ap.scale_log2), kLeast);
   p.negate = ap.scale_log2 < 0.f;
+  // Scores are taken in units of kUndo: an infinite factor would make NaN of those of 0.
+  if (a->dtype == SV_F16 && !std::isfinite(p.c * i4::kUndo<F16>)) return SV_OK;
   *taken = true;
   p.grid = std::min(nsm, kMaxGrid);
   p.ranges = static_cast<int>(std::min<int64_t>(p.grid, units * most));

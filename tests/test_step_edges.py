@@ -5,6 +5,7 @@ import torch
 
 import paged_ref as ref
 import step_ref as sref
+from test_i4_cache import attn_setup, check
 from test_paged_kv import DEV, gpu, i32
 from test_step_ops import TD, angles
 
@@ -13,6 +14,19 @@ def _pkg():
     import speculative_decoding_verification_75_gb300 as sv
     from speculative_decoding_verification_75_gb300 import api, kv
     return sv, api, kv
+
+
+# ---------------------------------------------- attention over 4 bits ----
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("scale", [1e38, -2.3e38, 2.2e37])
+def test_scores_of_zero_with_a_factor_near_the_largest(D, dt, scale):
+    """A zero score is zero whatever it is multiplied by: the mean of the values."""
+    s = attn_setup(np.random.default_rng(D), 2, 3, 8, 2, D, 16, [300, 20], [3, 2], dt, False)
+    s["q"].zero_()
+    check(s, dt, scale=scale)
 
 
 # ------------------------------------------------- rows at the ends of fp32 ----
