@@ -276,8 +276,9 @@ SV_API sv_status sv_kv_reserve(const sv_kv_reserve_args *args, sv_stream_t strea
  *
  *   query, key, value [B, T, num_heads or num_kv_heads, head_dim] of `dtype`
  *             (SV_BF16 or SV_F16), strides as in sv_kv_write;
- *   out, key_out  like query and key; may be them (in place), but must not overlap
- *             them otherwise.  key_out may be NULL where there is a cache.
+ *   out, key_out  like query and key; may be them (in place, of the same strides),
+ *             but must not overlap them, each other or value otherwise (refused where
+ *             they begin at one place).  key_out may be NULL where there is a cache.
  *   q_weight, k_weight  [head_dim] of `dtype`, 16-byte aligned, or NULL: no norm.
  *   cos_sin   [num_positions, rotary_dim] fp32: rotary_dim / 2 cosines, then the
  *             sines; 16-byte aligned (interleaved: 4).

@@ -112,6 +112,15 @@ sv_status qk_norm_rope(const sv_qk_norm_rope_args *a, sv_stream_t stream) {
     if (!aligned(x, 2)) return SV_ERR_INVALID_ARG;
     vec = vec && aligned(x, 16);
   }
+  // In place, or apart: other threads still read what a result written elsewhere covers.
+  const auto apart = [&](const void *x, const int64_t (&sx)[3], const void *y, const int64_t (&sy)[3], int64_t heads) {
+    return x != y || ((a->B == 1 || sx[0] == sy[0]) && (a->T == 1 || sx[1] == sy[1]) && (heads == 1 || sx[2] == sy[2]));
+  };
+  if ((any_q && !apart(a->out, a->out_stride, a->query, a->query_stride, a->num_heads)) ||
+      (any_k && a->key_out && !apart(a->key_out, a->key_out_stride, a->key, a->key_stride, a->num_kv_heads)) ||
+      (any_q && any_k && (a->out == a->key || a->out == a->key_out || a->key_out == a->query)) ||
+      (cached && any_k && ((any_q && a->out == a->value) || a->key_out == a->value)))
+    return SV_ERR_INVALID_ARG;
   // Vectors of four angles, where a lane's eight are adjacent.
   if (!aligned(a->positions, 4) || !aligned(a->slots, 8) || !aligned(a->cos_sin, a->interleaved ? 4 : 16) ||
       !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16))

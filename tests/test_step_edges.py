@@ -7,7 +7,7 @@ import paged_ref as ref
 import step_ref as sref
 from test_i4_cache import attn_setup, check
 from test_paged_kv import DEV, gpu, i32
-from test_step_ops import TD, angles
+from test_step_ops import ROPE, TD, angles
 
 
 def _pkg():
@@ -109,3 +109,31 @@ def test_norms_of_rows_that_are_not_finite(dt):
     zero = torch.zeros_like(nan)
     zero[0, 0, 1] = True
     assert (out[zero & ~nan] == 0).all() and torch.equal(out[~zero & ~nan], want[~zero & ~nan])
+
+
+# ------------------------------------------- a rotation's arguments ----
+
+def rope_words(p, **over):
+    f = dict(k=0, v=0, ks=0, vs=0, layer=0, block=0, slayer=0, sblock=0, layers=0, blocks=0, heads=0, bs=0, D=0,
+             cdtype=0, tables=0, max_blocks=0,
+             q=p, key=p, val=0, qb=1024, qt=256, qh=64, kb=512, kt=128, kh=64, vb=0, vt=0, vh=0,
+             out=p, kout=p, ob=1024, ot=256, oh=64, kob=512, kot=128, koh=64, qw=0, kw=0, cs=p, pos=p, slots=0,
+             eps=1e-6, P=10, R=64, pairs=0, B=2, T=4, Hq=4, Hkv=2, hd=64, dtype=1, status=0)
+    f.update(over)
+    return ROPE.pack(ROPE.size, *f.values())
+
+
+def test_results_of_a_rotation_in_one_place_are_refused():
+    """Queries and keys that would be written over each other, or over what other threads still read."""
+    _, api, _ = _pkg()
+    lib = api.load_library()
+    a, b, c, d, v = (i << 20 for i in range(1, 6))
+    for over in (dict(out=a, kout=a), dict(out=b, kout=d), dict(out=c, kout=a), dict(out=a, ot=512, kout=d),
+                 dict(out=a, oh=128, kout=d), dict(out=a, ob=2048, kout=d), dict(out=c, kout=b, koh=128)):
+        words = rope_words(a, key=b, cs=a, pos=a, **over)
+        assert lib.sv_qk_norm_rope(words, None) == api.SV_ERR_INVALID_ARG, over
+    cache = dict(k=8 * a, v=9 * a, block=2048, layers=1, blocks=8, heads=2, bs=16, D=64, cdtype=1, slots=a, val=v, vb=512,
+                 vt=128, vh=64)
+    for over in (dict(out=v, kout=d), dict(out=c, kout=v), dict(out=c, kout=a)):
+        words = rope_words(a, key=b, cs=a, pos=a, **{**cache, **over})
+        assert lib.sv_qk_norm_rope(words, None) == api.SV_ERR_INVALID_ARG, over
