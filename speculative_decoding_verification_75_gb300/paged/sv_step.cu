@@ -95,7 +95,10 @@ sv_status qk_norm_rope(const sv_qk_norm_rope_args *a, sv_stream_t stream) {
   RopeParams p = {};
   const bool cached = a->slots != nullptr;
   if (cached) {
-    if (const sv_status s = take_cache(a->cache, 0, false, p.c)) return s;
+    sv_kv_cache c = a->cache;
+    c.block_tables = nullptr;
+    c.max_blocks = 0;
+    if (const sv_status s = take_cache(c, 0, false, p.c)) return s;
     if (!scaled(a->cache.dtype) && a->cache.dtype != a->dtype) return SV_ERR_UNSUPPORTED_DTYPE;
     if (a->cache.num_kv_heads != a->num_kv_heads || a->cache.head_dim != D) return SV_ERR_INVALID_ARG;
     bool same;  // keys turn, values do not
@@ -106,7 +109,7 @@ sv_status qk_norm_rope(const sv_qk_norm_rope_args *a, sv_stream_t stream) {
   if (!a->positions || (R > 0 && !a->cos_sin) || (any_q && (!a->query || !a->out)) ||
       (any_k && (!a->key || (cached ? !a->value : !a->key_out))))
     return SV_ERR_INVALID_ARG;
-  const void *const rows[] = {a->query, a->key, a->value, a->out, a->key_out};
+  const void *const rows[] = {a->query, a->key, cached ? a->value : nullptr, a->out, a->key_out};
   bool vec = true;
   for (const void *x : rows) {
     if (!aligned(x, 2)) return SV_ERR_INVALID_ARG;

@@ -137,3 +137,26 @@ def test_results_of_a_rotation_in_one_place_are_refused():
     for over in (dict(out=v, kout=d), dict(out=c, kout=v), dict(out=c, kout=a)):
         words = rope_words(a, key=b, cs=a, pos=a, **{**cache, **over})
         assert lib.sv_qk_norm_rope(words, None) == api.SV_ERR_INVALID_ARG, over
+
+
+@gpu
+def test_a_rotation_without_a_cache_looks_at_neither_it_nor_values():
+    sv, api, _ = _pkg()
+    lib = api.load_library()
+    x = torch.randn(2, 4, 6, 64, device=DEV).bfloat16()
+    q, k = (t.contiguous() for t in x.split([4, 2], 2))
+    cs, pos = torch.from_numpy(angles(10, 64)).to(DEV), i32(np.arange(8).reshape(2, 4))
+    want = sv.qk_norm_rope(q, k, cs, pos)
+    out, ko = torch.zeros_like(q), torch.zeros_like(k)
+    p = dict(q=q.data_ptr(), key=k.data_ptr(), out=out.data_ptr(), kout=ko.data_ptr(), cs=cs.data_ptr(),
+             pos=pos.data_ptr(), cdtype=77, bs=-3, tables=5, vb=-1)
+    assert lib.sv_qk_norm_rope(rope_words(0, **p, val=3), torch.cuda.current_stream().cuda_stream) == api.SV_OK
+    assert torch.equal(out, want[0]) and torch.equal(ko, want[1])
+    # With a cache its block tables are not.
+    kc, vc = (torch.zeros(2, 2, 8, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    slots = torch.arange(8, device=DEV).view(2, 4)
+    p = dict(p, k=kc.data_ptr(), v=vc.data_ptr(), block=1024, layers=1, blocks=2, heads=2, bs=8, D=64, cdtype=1, tables=5,
+             max_blocks=-2, slots=slots.data_ptr(), val=k.data_ptr(), vb=512, vt=128, vh=64)
+    assert lib.sv_qk_norm_rope(rope_words(0, **p), torch.cuda.current_stream().cuda_stream) == api.SV_OK
+    assert torch.equal(kc[0].transpose(0, 1).reshape(2, 4, 2, 64), want[1]) and torch.equal(
+        vc[0].transpose(0, 1).reshape(2, 4, 2, 64), k)
