@@ -5,7 +5,7 @@ import torch
 
 import paged_ref as ref
 import step_ref as sref
-from test_i4_cache import attn_setup, check
+from test_i4_cache import attn_setup, check, run
 from test_paged_kv import DEV, gpu, i32
 from test_step_ops import ROPE, TD, angles
 
@@ -18,6 +18,94 @@ def _pkg():
 
 # ---------------------------------------------- attention over 4 bits ----
 
+def grow(s, lo, hi):
+    """Scale bytes of k from lo at a request's first key to hi at its last one."""
+    bs = s["c"][2].shape[2]
+    for b, (L, n) in enumerate(zip(s["L"], s["n"])):
+        for pos in range(L + n):
+            s["c"][2][int(s["tables"][b, pos // bs]), :, pos % bs] = lo + (hi - lo) * pos // max(L + n - 1, 1)
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("loud", [None, 0, 1, 2])
+def test_references_rise_along_ranges_of_many_tiles(D, dt, loud):
+    """Some 700 tiles of 128 keys in at most 152 ranges: most tiles are not a range's first.  Keys grow 512 times
+    along a request, so that late tiles exceed a row's reference by 2^8 (2^15) again and again, the last ones by more than
+    2^100; with `loud` only in that token's rows, which are one chunk of eight rows of one softmax group."""
+    rng = np.random.default_rng(D + (loud or 0))
+    L = [int(x) for x in rng.integers(2500, 3100, 4)]
+    s = attn_setup(rng, 4, 3, 64, 8, D, 64, L, [3] * 4, dt, False)
+    if loud is not None:
+        quiet = [t for t in range(3) if t != loud]
+        s["q"][:, quiet] *= 2.0 ** -10
+    grow(s, 88, 160)
+    out = check(s, dt)
+    for _ in range(3):
+        assert torch.equal(run(s), out)
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_rows_that_see_their_first_key_late(D, dt, monkeypatch):
+    """Trees without committed tokens: nodes from 128 on see no key of the first tile, some none at all, and the
+    first that they see is far above what a reference of nothing allows.
+
+    Besides the other roundings: where a reference rises by more than 2^126, the factor of what was summed below it is
+    a zero of fp32.  A probability is at most 2^8 of its reference then (fp16: 2^15, of 2^7 times it), and the largest one of
+    the raised reference is at least 1 of l: of S keys S 2^(8 - 126) max |v| is lost at most.  (A bf16 result showed it
+    where the likely key's value is 0 and the others' products are 2^-120.)"""
+    plain = ref.attention
+
+    def attention(q, cache, *args):
+        w, wl, tol, *rest = plain(q, cache, *args)
+        return w, wl, tol + q.shape[1] * 2.0 ** -118 * np.abs(cache.v).max(), *rest
+
+    monkeypatch.setattr(ref, "attention", attention)
+    rng = np.random.default_rng(D)
+    B, T, H = 40, 300, 2
+    n = [int(x) for x in rng.integers(260, T + 1, B)]
+    s = attn_setup(rng, B, T, H, H, D, 16, [0] * B, n, dt, False)
+    m = np.broadcast_to(np.eye(T, dtype=bool), (B, T, T)).copy()
+    m |= rng.random((B, T, T)) < 0.02
+    m[:, 128:, :128] &= rng.random((B, T - 128, 1)) < 0.3
+    m[:, 200:, :256] &= rng.random((B, T - 200, 1)) < 0.3
+    m[:, 150:160] = False
+    s["mask"] = m
+    s["c"][2][:] = torch.from_numpy(rng.integers(60, 150, tuple(s["c"][2].shape)).astype(np.uint8)).to(DEV)
+    out = check(s, dt)
+    assert (out[:, 150:160] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dt,T", [("bf16", 4), ("fp16", 4), ("bf16", 11)])
+@pytest.mark.parametrize("why", ["value", "key", "block"])
+def test_marked_units_among_others_of_a_range(D, dt, T, why):
+    """Units of a few tiles, several of them whole in a range; of some requests a new token's group is NaN for one
+    head, or a block is missing.  What stands before and behind them in a range comes out as without them."""
+    rng = np.random.default_rng(D + T)
+    B, Hkv, G = 40, 8, 4
+    L = [int(x) for x in rng.integers(0, 300, B)]
+    n = [int(x) for x in rng.integers(1, T + 1, B)]
+    s = attn_setup(rng, B, T, Hkv * G, Hkv, D, 16, L, n, dt, False)
+    clean = run(s, torch.full_like(s["q"], 9.0))
+    hit = np.zeros((B, Hkv), dtype=bool)
+    for b in rng.choice(B, 14, replace=False):
+        if why == "block":
+            s["tables"][b, rng.integers(0, -(-(L[b] + n[b]) // 16))] = -1
+            hit[b] = True
+        else:
+            h, pos = rng.integers(Hkv), L[b] + n[b] - 1
+            s["c"][3 if why == "value" else 2][int(s["tables"][b, pos // 16]), h, pos % 16, rng.integers(D // 32)] = 255
+            hit[b, h] = True
+    out = check(s, dt)
+    same = torch.from_numpy(~np.repeat(hit, G, 1)).to(DEV)[:, None].expand(B, T, Hkv * G)
+    assert torch.equal(out[same], clean[same])
+
+
 @gpu
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
@@ -27,6 +115,36 @@ def test_scores_of_zero_with_a_factor_near_the_largest(D, dt, scale):
     s = attn_setup(np.random.default_rng(D), 2, 3, 8, 2, D, 16, [300, 20], [3, 2], dt, False)
     s["q"].zero_()
     check(s, dt, scale=scale)
+
+
+@gpu
+def test_blocks_past_32_bit_offsets():
+    """Blocks of a cache of 4 bits 2^33 elements apart: written by both operators, attended to, moved, read back."""
+    sv, _, _ = _pkg()
+    rng = np.random.default_rng(1)
+    H, bs, D = 2, 16, 64
+    stride = (1 << 32) + 16 * 64                               # bytes
+    sstride = (1 << 31) + 4096
+    store = [torch.zeros(stride + H * bs * D // 2, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    sstore = [torch.zeros(sstride + H * bs * D // 32, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    far = [x.as_strided((2, H, bs, D // 2), (stride, bs * D // 2, D // 2, 1)) for x in store]
+    far += [x.as_strided((2, H, bs, D // 32), (sstride, bs * D // 32, D // 32, 1)) for x in sstore]
+    near = [torch.zeros(x.shape, dtype=torch.uint8, device=DEV) for x in far]
+    x = torch.from_numpy(rng.standard_normal((1, 20, 4 + 2 * H, D))).bfloat16().to(DEV)
+    q, key, value = x.split([4, H, H], 2)
+    t, L = i32([[0, 1]]), i32([5])
+    cs, pos = torch.from_numpy(angles(40, D)).to(DEV), i32([list(range(5, 25))])
+    got = []
+    for k, v, ks, vs in (far, near):
+        kw = dict(k_scale=ks, v_scale=vs)
+        sv.kv_write(key, value, k, v, t, L, **kw)
+        a = sv.kv_read(k, v, t, i32([20]), L, max_len=20, **kw)
+        o, _ = sv.qk_norm_rope(q, key, cs, pos, value=value, k_cache=k, v_cache=v, slots=pos.long(), **kw)
+        y = sv.tree_attention(o, k, v, t, L, **kw)
+        sv.kv_compact(i32([[0, 12, 19]]), i32([3]), L, t, k, v, **kw)
+        got.append((*a, o, y, k, v, ks, vs))
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and a.any()
 
 
 # ------------------------------------------------- rows at the ends of fp32 ----
