@@ -83,8 +83,9 @@ def kv_reserve(seq_lens: torch.Tensor, new_lens: Optional[torch.Tensor],
     where there is none; positions [B, T] int32, seq_lens[b] + i, or by the depth
     of node i in ``tree_mask`` ([B, T, T] or [T, T] bool, as for
     ``tree_attention``); reserved [B] int32, the new tokens that have places
-    (new_lens[b], or 0), which is the new_lens of the calls that follow.  T is
-    ``max_new``, or that of ``slots`` or ``tree_mask``."""
+    (new_lens[b], or 0), which is the new_lens of the calls that follow,
+    ``kv_rollback`` among them (its num_accepted at most that); it may be the
+    tensor new_lens itself.  T is ``max_new``, or that of ``slots`` or ``tree_mask``."""
     rc, *res = (_native or load_binding()).kv_reserve(
         seq_lens, new_lens, block_tables, block_size, free_list, free_count, tree_mask, max_new,
         slots, positions, reserved, status, None if stream is None else stream.cuda_stream)

@@ -6,8 +6,8 @@ import torch
 import paged_ref as ref
 import step_ref as sref
 from test_i4_cache import attn_setup, check, run
-from test_paged_kv import DEV, gpu, i32
-from test_step_ops import ROPE, TD, angles
+from test_paged_kv import DEV, gpu, i32, make_tables
+from test_step_ops import ROPE, TD, angles, reserve
 
 
 def _pkg():
@@ -278,3 +278,103 @@ def test_a_rotation_without_a_cache_looks_at_neither_it_nor_values():
     assert lib.sv_qk_norm_rope(rope_words(0, **p), torch.cuda.current_stream().cuda_stream) == api.SV_OK
     assert torch.equal(kc[0].transpose(0, 1).reshape(2, 4, 2, 64), want[1]) and torch.equal(
         vc[0].transpose(0, 1).reshape(2, 4, 2, 64), k)
+
+
+# --------------------------------------------------------------- reserve ----
+
+@gpu
+@pytest.mark.parametrize("B,T", [(256, 64), (256, 65), (2100, 7)])
+def test_trees_of_many_requests(B, T):
+    """More tokens than the kernel of the blocks places itself: a second one does, by the mask too."""
+    rng = np.random.default_rng(T)
+    bs = 16
+    L, n = rng.integers(0, 100, B), rng.integers(0, T + 1, B)
+    n[0] = T
+    mask = np.broadcast_to(np.eye(T, dtype=bool), (B, T, T)).copy()
+    par = (rng.random((B, T)) * np.maximum(np.arange(T), 1)).astype(int)
+    for i in range(1, T):
+        mask[:, i] |= mask[np.arange(B), par[:, i]]
+    mask[:, :, T // 2:] |= rng.random((B, T, T - T // 2)) < 0.3     # columns past n among them: they do not count
+    mask[0, 3] = False
+    held = -(-L // bs)
+    width = -(-(100 + T) // bs) + 1
+    tables = make_tables(rng, held, int(held.sum()) + 1, width)
+    want = int((-(-(L + n) // bs) - held).sum())
+    free = 10 ** 6 + rng.permutation(want + 5)
+    _, _, res, _, _, st = reserve(L, n, tables, bs, free, want, mask, T)
+    assert st == 0 and np.array_equal(res, n)
+    reserve(L, n, tables, bs, free, want, mask[1], T)               # one mask for all
+    _, _, res, _, _, st = reserve(L, n, tables, bs, free, want // 2, mask, T)
+    assert st == sref.NO_BLOCKS and 0 < (res > 0).sum() < B
+
+
+@gpu
+@pytest.mark.parametrize("B,T", [(9001, 1), (9001, 2), (32768, 1), (4097, 3)])
+@pytest.mark.parametrize("short", [False, True])
+def test_more_requests_than_threads(B, T, short):
+    """Each thread block's prefix sums go on over several rounds of its threads."""
+    rng = np.random.default_rng(B + T)
+    bs = 2
+    L, n = rng.integers(0, 9, B), rng.integers(0, T + 1, B)
+    held = -(-L // bs) + rng.integers(0, 2, B)
+    tables = make_tables(rng, held, int(held.sum()) + 1, 8)
+    want = int(np.maximum(-(-(L + n) // bs) - held, 0).sum())
+    free = 10 ** 6 + rng.permutation(want + 3)
+    reserve(L, n, tables, bs, free, want * 2 // 3 if short else want, T=T)
+
+
+@gpu
+@pytest.mark.parametrize("B,T", [(5, 6), (700, 40)])
+def test_counts_reserved_in_place(B, T):
+    """`reserved` may be new_lens itself."""
+    sv, _, _ = _pkg()
+    rng = np.random.default_rng(B)
+    L, n = rng.integers(0, 60, B), rng.integers(0, T + 1, B)
+    held = -(-L // 16)
+    tables = make_tables(rng, held, int(held.sum()) + 1, 8)
+    want = int((-(-(L + n) // 16) - held).sum())
+    free = i32(10 ** 6 + rng.permutation(want))
+    a = (i32(L), i32(n), i32(tables), 16, free, i32([want // 2]))
+    b = (i32(L), i32(n), i32(tables), 16, free, i32([want // 2]))
+    x, y = sv.kv_reserve(*a, max_new=T), sv.kv_reserve(*b, max_new=T, reserved=b[1])
+    assert y[2] is b[1]
+    for u, v in zip((*x, a[2], a[5]), (*y, b[2], b[5])):
+        assert torch.equal(u, v)
+
+
+# ------------------------------------------------- a step without blocks ----
+
+@gpu
+def test_a_step_in_which_blocks_run_out():
+    """Requests that get no blocks sit the step out: the calls that follow take `reserved` for their new tokens, and
+    nothing of theirs changes."""
+    sv, _, kv = _pkg()
+    rng = np.random.default_rng(4)
+    B, T, Hq, Hkv, D, bs = 4, 5, 8, 2, 64, 4
+    L, n = np.array([3, 8, 6, 4]), np.array([5, 5, 2, 5])
+    tables = np.full((B, 5), -1)
+    for b, row in enumerate(([0], [1, 2], [3, 4], [5])):
+        tables[b, :len(row)] = row
+    pool = 9
+    tab, seq, free, count = i32(tables), i32(L), i32([6, 7, 8, -1, -1, -1]), i32([2])
+    cache = [torch.zeros(pool, Hkv, bs, d, dtype=torch.uint8, device=DEV) for d in (D // 2, D // 2, 2, 2)]
+    kw = dict(k_scale=cache[2], v_scale=cache[3])
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    slots, pos, new = sv.kv_reserve(seq, i32(n), tab, bs, free, count, max_new=T, status=status)
+    assert new.tolist() == [5, 0, 2, 0] and status.item() == kv.SV_KV_NO_BLOCKS and count.item() == 1
+    status.zero_()
+    x = torch.from_numpy(rng.standard_normal((B, T, Hq + 2 * Hkv, D))).bfloat16().to(DEV)
+    q, k, v = x.split([Hq, Hkv, Hkv], 2)
+    before = q.clone()
+    out, _ = sv.qk_norm_rope(q, k, torch.from_numpy(angles(20, D)).to(DEV), pos, out=q, value=v, k_cache=cache[0],
+                             v_cache=cache[1], slots=slots, status=status, **kw)
+    assert torch.equal(out[1], before[1]) and torch.equal(out[3], before[3])
+    y = torch.full((B, T, Hq, D), 9.0, dtype=torch.bfloat16, device=DEV)
+    sv.tree_attention(out, cache[0], cache[1], tab, seq, None, new, out=y, status=status, **kw)
+    assert (y[1] == 9).all() and (y[3] == 9).all() and y[0].isfinite().all()
+    kept = torch.minimum(i32([3, 1, 2, 4]), new)            # what a verification of all would keep
+    sv.kv_compact(i32([[0, 1, 2, 3]] * B), kept, seq, tab, cache[0], cache[1], status=status, **kw)
+    sv.kv_rollback(kept, seq, tab, bs, free, count, new, gamma_max=T, status=status)
+    assert status.item() == 0 and seq.tolist() == [6, 8, 8, 4]
+    want = [[0, 7], [1, 2], [3, 4], [5]]
+    assert [[b for b in row if b >= 0] for row in tab.tolist()] == want and count.item() == 1
