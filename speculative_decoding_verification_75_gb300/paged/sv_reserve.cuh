@@ -8,9 +8,9 @@
 //
 // Bound by latencies (lengths -> table -> sum over the requests -> free list ->
 // table -> slots): one launch, whose thread blocks form one cluster and exchange
-// their sums through shared memory (8 requests of 6 tokens: 5.7 us; 256 trees of 64
-// nodes: 7.5 us and 5.8 us of a second kernel, on all SMs, for the slots and positions:
-// with 8 on each thread of the cluster the one kernel takes 14 us).
+// their sums through shared memory, and which also places the tokens while its threads
+// have few; else a second kernel on all SMs does.  In a graph of calls: 8 requests of 6
+// tokens 3.0 us, 256 trees of 64 nodes 7.6 us (38 us by the one kernel).
 #pragma once
 
 #include "sv_paged_common.cuh"
@@ -20,7 +20,11 @@ namespace svp {
 constexpr int kReserveThreads = 512;
 constexpr int kReserveCluster = 8;        // thread blocks at most
 constexpr int kReserveRequests = 4096;    // of a thread block
-constexpr int kFusedTokens = 4;           // of a thread, at most, where the same kernel places them
+// Tokens of a thread, at most, where the same kernel places them: one kernel against two
+// takes 3.0 and 3.9 us for 48 tokens, 3.7 and 4.5 for 2 on each thread, 4.5 for 4, 6.1 and
+// 4.8 for 8; of trees, whose nodes read a row of the mask each, 3.4 and 4.3 us for 48, 4.4
+// and 4.8 for 1.5, 7.7 and 6.6 for 2 (of 64 nodes), 5.5 and 5.1 for 3 (of 6).
+constexpr float kFusedTokens = 4, kFusedNodes = 1.5f;
 
 struct ReserveParams {
   const int32_t *seq_lens, *new_lens, *free_list;

@@ -26,7 +26,7 @@ namespace svp {
 
 constexpr int kRopeThreads = 128;
 constexpr int kRopeRows = 2;
-constexpr int kRopeWarps = 152 * 24;   // warps that a batch is spread over: what is resident
+constexpr int kRopeWarps = 152 * 24;   // warps that a batch is spread over: 24 (of the fewest registers 28) fit an SM
 
 struct RopeParams {
   Cache c;                       // c.k NULL: none

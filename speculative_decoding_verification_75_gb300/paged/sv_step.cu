@@ -51,7 +51,7 @@ sv_status kv_reserve(const sv_kv_reserve_args *a, sv_stream_t stream) {
   while (ranks < kReserveCluster && (p.B + ranks - 1) / ranks > kReserveRequests) ranks *= 2;
   const int64_t tokens = a->B * a->T;
   p.per = (p.B + ranks - 1) / ranks;
-  p.fused = tokens <= int64_t{kReserveThreads} * ranks * kFusedTokens;
+  p.fused = tokens <= static_cast<int64_t>(kReserveThreads * ranks * (p.mask ? kFusedNodes : kFusedTokens));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks);
   cfg.blockDim = dim3(kReserveThreads);
@@ -165,8 +165,9 @@ sv_status qk_norm_rope(const sv_qk_norm_rope_args *a, sv_stream_t stream) {
   p.status = a->status;
   p.lanes = 1;
   while (p.lanes < D / 8) p.lanes *= 2;
-  // Steps of whole rows of a kind; a warp's: as many as leave kRopeWarps warps, whole
-  // turns of kRopeRows.
+  // Steps of whole rows of a kind; a warp's: as many as leave kRopeWarps warps, rounded
+  // down and then to whole turns of kRopeRows.  (128 x 6 tokens of 40 steps: 8 of 8.4, 3840
+  // warps, 9.7 us; rounded up 10, fewer than kRopeWarps warps, 10.7 us.)
   const int group = 32 / p.lanes;
   p.steps_q = (p.Hq + group - 1) / group;
   p.steps_k = (p.Hkv + group - 1) / group;

@@ -283,7 +283,7 @@ def test_a_rotation_without_a_cache_looks_at_neither_it_nor_values():
 # --------------------------------------------------------------- reserve ----
 
 @gpu
-@pytest.mark.parametrize("B,T", [(256, 64), (256, 65), (2100, 7)])
+@pytest.mark.parametrize("B,T", [(256, 64), (256, 65), (2100, 7), (1500, 4)])
 def test_trees_of_many_requests(B, T):
     """More tokens than the kernel of the blocks places itself: a second one does, by the mask too."""
     rng = np.random.default_rng(T)
