@@ -203,7 +203,8 @@ SV_API sv_status sv_kv_compact(const sv_kv_compact_args *args, sv_stream_t strea
  * one of their blocks is missing, a new token's value is not finite, or, e4m3,
  * scales lie further apart than 2^15 (k: of 64 keys, v: below the first ones',
  * or 2^7 above); zeros with s = 7, as sv_kv_write leaves them, do not count.  Over
- * SV_I4 rows are taken 64 at a time, and scales do not matter.
+ * SV_I4 rows are taken 64 at a time, and scales do not matter.  What lies 2^118
+ * below a row's largest probability may count as nothing.
  */
 typedef struct {
     uint64_t struct_bytes;

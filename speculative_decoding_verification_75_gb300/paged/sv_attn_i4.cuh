@@ -8,7 +8,7 @@
 // 128 keys and 128 (64) dimensions in tensor-memory lanes and N = 16 .. 64 query
 // rows in columns.  With queries in the lanes a chain of six tokens and eight heads
 // fills 48 of 128, and 128 keys take 1024 cycles of the tensor cores; so they take
-// 24 N, 384 for that chain and 128 for a token.
+// 8 N, 384 for that chain and 128 for a token.
 //
 // Widening.  Both cache operands go from shared memory through registers into
 // tensor memory, as the products' A operand: nothing is written back to shared
@@ -33,13 +33,17 @@
 // path also does the first tile of a unit.  A thread's parts of the rows' sums are
 // columns of tensor memory, not registers: then every loop over rows has one copy of
 // its body.  (Unrolled, the code of all roles together missed the instruction cache:
-// 642 us for 128 requests, 382 so.)
+// 642 us for 128 requests, where the loops then took 382.)
+// P has the type of the queries, as both operands of a product have one type: half a
+// step of 2^-8 in bf16, whose range keeps what lies far below the largest, 2^-11 in fp16.
+// The sums take the fp32 values.  Results are off from 64 bits by 0.0023 for trees (one
+// rounding to bf16: 0.0017), 0.00026 in fp16 (0.00021), in the mean relative to them.
 //
 // Roles.  K, V, their products and the softmax are pipelined through two places each
 // (P: three) in tensor or shared memory; even and odd tiles have producers and widening
 // warps of their own, for each is a chain of latencies.  (One producer for K and one for
 // V took 1800 cycles a tile and bound the kernel; copies by the widening warps
-// themselves, without producers, were no faster: 384 us for 128 requests, 364 so.)
+// themselves, without producers, were no faster: 384 us for 128 requests, 364 with them.)
 //
 // Work, ranges, cut units, marked units and the second kernel are those of
 // sv_attn_tc.cuh, with one range for a thread block.
@@ -49,8 +53,10 @@
 //                                                warp's chain, about 1300 cycles a tile
 //                                                (wait, vote, fence) and 400 per 8 rows
 //   16 trees of 64, 32 on 8, 1000-8000 keys      215 us, 260 TFLOP/s: the same; units of
-//                                                64 rows take the keys four times
-//   131071 keys, 1 token, 64 on 8                57 us, 2.5 TB/s: the same chain
+//                                                64 rows take the keys four times (e4m3:
+//                                                108 us, each key widened once)
+//   131071 keys, 1 token, 64 on 8                57 us, 2.5 TB/s: the same chain, in one
+//                                                group: 8 rows leave the other none
 //   500 keys, 1 token, 14 on 2 of 64             10 us: start, first data, join
 #pragma once
 
