@@ -23,7 +23,6 @@ __device__ __forceinline__ uint32_t halves8(const uint4 &raw) {
   for (int i = 0; i < 4; ++i) big = __vmaxu2(big, u[i] & 0x7fff7fffu);
   return big;
 }
-template <typename Q>
 __device__ __forceinline__ uint32_t largest8(const uint4 &raw) {
   const uint32_t big = halves8(raw);
   return max(big & 0xffffu, big >> 16);
@@ -38,7 +37,7 @@ template <typename Q>
 __device__ __forceinline__ uint32_t quantise8(const uint4 &raw, uint2 &codes) {
   const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
   constexpr uint32_t kInf = Q::kIsBf16 ? 0x7f80u : 0x7c00u;
-  uint32_t big = largest8<Q>(raw);
+  uint32_t big = largest8(raw);
   const bool odd = __any_sync(kFull, big >= kInf);
   if (odd) {                                       // the largest finite magnitude
     big = 0;
@@ -73,25 +72,6 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 &raw, uint2 &codes) {
   }
   codes = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
   return static_cast<uint32_t>(e + 127);
-}
-
-// Two fp32 at once.
-__device__ __forceinline__ uint64_t pair2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float lower(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float upper(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
 }
 
 // A group's scale as codes of 4 bits have it: f, the smallest with amax <= 7 f, its byte,
@@ -132,12 +112,12 @@ __device__ __forceinline__ void limit8(float (&x)[8], float f, bool odd) {
 // at most 11 bits): rounded to 2^-13 first, by the sum with 1536, the former are exact
 // and go to the even one, and the others stay on their side.
 __device__ __forceinline__ uint32_t codes4(const float (&x)[8], float inv) {
-  const uint64_t inv2 = pair2(inv, inv), one2 = pair2(1.f, 1.f), fine2 = pair2(1536.f, 1536.f);
-  const uint64_t up2 = pair2(12582920.f - 1536.f, 12582920.f - 1536.f);
+  const uint64_t inv2 = f2_pack(inv, inv), one2 = f2_pack(1.f, 1.f), fine2 = f2_pack(1536.f, 1536.f);
+  const uint64_t up2 = f2_pack(12582920.f - 1536.f, 12582920.f - 1536.f);
   uint32_t codes = 0;
 #pragma unroll
   for (int i = 3; i >= 0; --i) {
-    const uint64_t y = fma_pair(fma_pair(pair2(x[2 * i], x[2 * i + 1]), inv2, fine2), one2, up2);
+    const uint64_t y = f2_fma(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), inv2, fine2), one2, up2);
     codes = (codes * 16u + static_cast<uint32_t>(y >> 32)) * 16u + static_cast<uint32_t>(y);
   }
   return codes - 0x4b400000u * 0x11111111u;      // the sums' upper bits; the codes are 1 .. 15
@@ -145,7 +125,7 @@ __device__ __forceinline__ uint32_t codes4(const float (&x)[8], float inv) {
 
 template <typename Q>
 __device__ __forceinline__ uint32_t quantise8(const uint4 &raw, uint32_t &codes) {
-  uint32_t big = largest8<Q>(raw);
+  uint32_t big = largest8(raw);
   big = max(big, __shfl_xor_sync(kFull, big, 1));
   big = max(big, __shfl_xor_sync(kFull, big, 2));
   const Scale4 sc = scale4<Q>(big);

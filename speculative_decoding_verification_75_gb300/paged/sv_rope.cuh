@@ -71,10 +71,12 @@ constexpr uint32_t kHeavy = (127u + 64u) << 7;   // 2^64 in bf16
 constexpr float kMostSquares = 0x1p80f, kLeastSquares = 0x1p-20f, kLeastEps = 0x1p-30f;
 
 __device__ __forceinline__ float squares8(const float (&f)[8]) {
-  uint64_t s2 = mul_pair(pair2(f[0], f[1]), pair2(f[0], f[1]));
+  uint64_t s2 = f2_mul(f2_pack(f[0], f[1]), f2_pack(f[0], f[1]));
 #pragma unroll
-  for (int e = 2; e < 8; e += 2) s2 = fma_pair(pair2(f[e], f[e + 1]), pair2(f[e], f[e + 1]), s2);
-  return lower(s2) + upper(s2);
+  for (int e = 2; e < 8; e += 2) s2 = f2_fma(f2_pack(f[e], f[e + 1]), f2_pack(f[e], f[e + 1]), s2);
+  float a, b;
+  f2_unpack(s2, a, b);
+  return a + b;
 }
 
 // A row moved by the power of two that takes the larger of its largest magnitude and
@@ -86,7 +88,7 @@ struct Moved {
   float squares;
 };
 __device__ __noinline__ Moved tame(uint4 row, float root_eps, float eps, int D, int lanes, bool first) {
-  uint32_t big = largest8<BF16>(row);
+  uint32_t big = largest8(row);
 #pragma unroll 1
   for (int o = 1; o < lanes; o <<= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
   big = max(big, __float_as_uint(root_eps) >> 16);
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6) sv_rope_kernel(const RopePara
     if (weight && in) {
       const uint4 x = ld128(weight + ch * 16);
       unpack8<Q>(&x, w);
-      heavy = Q::kIsBf16 && largest8<Q>(x) >= kHeavy;
+      heavy = Q::kIsBf16 && largest8(x) >= kHeavy;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) wm[e] = kPairs ? w[e ^ 1] : w[e];
@@ -235,8 +237,8 @@ __global__ void __launch_bounds__(kRopeThreads, 6) sv_rope_kernel(const RopePara
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      own[e] = pair2(c[2 * e] * w[2 * e], c[2 * e + 1] * w[2 * e + 1]);
-      mate_by[e] = pair2(s[2 * e] * wm[2 * e], s[2 * e + 1] * wm[2 * e + 1]);
+      own[e] = f2_pack(c[2 * e] * w[2 * e], c[2 * e + 1] * w[2 * e + 1]);
+      mate_by[e] = f2_pack(s[2 * e] * wm[2 * e], s[2 * e + 1] * wm[2 * e + 1]);
     }
   };
   // Where the rows go, likewise: the output, and the cache's place of the row's head.
@@ -321,22 +323,19 @@ __global__ void __launch_bounds__(kRopeThreads, 6) sv_rope_kernel(const RopePara
         }
         uint64_t x[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = mul_pair(pair2(f[2 * e], f[2 * e + 1]), own[e]);
+        for (int e = 0; e < 4; ++e) x[e] = f2_mul(f2_pack(f[2 * e], f[2 * e + 1]), own[e]);
         if (p.R > 0) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (2 * e < turned) x[e] = fma_pair(pair2(g[2 * e], g[2 * e + 1]), mate_by[e], x[e]);   // else it may be infinite
+            if (2 * e < turned) x[e] = f2_fma(f2_pack(g[2 * e], g[2 * e + 1]), mate_by[e], x[e]);   // else it may be infinite
         }
         if (is_q ? p.qw != nullptr : p.kw != nullptr) {
           const float by = Q::kIsBf16 ? ss[i] * lift : ss[i];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = mul_pair(x[e], pair2(by, by));
+          for (int e = 0; e < 4; ++e) x[e] = f2_mul(x[e], f2_pack(by, by));
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f[2 * e] = lower(x[e]);
-          f[2 * e + 1] = upper(x[e]);
-        }
+        for (int e = 0; e < 4; ++e) f2_unpack(x[e], f[2 * e], f[2 * e + 1]);
         pack8<Q>(&now[i], f);
       }
       if (on && to) store16(to, now[i], p.vec);
