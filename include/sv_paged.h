@@ -274,6 +274,7 @@ SV_API sv_status sv_kv_reserve(const sv_kv_reserve_args *args, sv_stream_t strea
  * then its first rotary_dim elements turn, in pairs (a, b), by the angle of the
  * token's position: (a cos - b sin, b cos + a sin), in fp32, rounded once.  Rows and
  * weights may have any size: squares and products that fp32 does not hold are not formed.
+ * (Beside a weight of 2^64 or more those below 2^-62 may count as 0.)
  *
  *   query, key, value [B, T, num_heads or num_kv_heads, head_dim] of `dtype`
  *             (SV_BF16 or SV_F16), strides as in sv_kv_write;

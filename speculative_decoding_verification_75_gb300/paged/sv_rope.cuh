@@ -61,8 +61,9 @@ __device__ __forceinline__ void store16(uint8_t *d, const uint4 &v, bool vec) {
 
 // bf16 reaches as far as fp32: a row's squares may leave it, and so may its products with
 // the weights, before the norm's factor.  Where a lane's squares sum up to kMostSquares
-// at most neither does, for weights below 2^64 (others are taken at 2^-64, and the factor
-// at 2^64): |x| <= 2^40, |x w| <= 2^104.  Nor is anything lost below 2^-149 while the
+// at most neither does, for weights below 2^64 (with others a head's weights are taken at
+// 2^-64, and the factor at 2^64; what is below 2^-62 beside these may become 0): |x| <=
+// 2^40, |x w| <= 2^104.  Nor is anything lost below 2^-149 while the
 // factor is at most 2^15, which eps holds; where eps is below 2^-30, kLeastSquares.  Rows
 // outside are moved by a power of two first.  (The check costs prompts 111 -> 115 us,
 // drafts 9.5 -> 9.7; in line, where registers for it left 6 blocks on an SM instead of 7,
