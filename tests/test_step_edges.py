@@ -229,6 +229,34 @@ def test_norms_of_rows_that_are_not_finite(dt):
     assert (out[zero & ~nan] == 0).all() and torch.equal(out[~zero & ~nan], want[~zero & ~nan])
 
 
+@gpu
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "i4"])
+def test_rows_near_the_ends_of_fp32_into_the_cache(kind):
+    """The cache gets what kv_write of the rounded rows puts there; rows of values, of any size, are not touched."""
+    sv, _, _ = _pkg()
+    rng = np.random.default_rng(7)
+    B, T, H, D, bs = 2, 8, 3, 64, 16
+    x = rng.standard_normal((B, T, 3 * H, D)) * 2.0 ** rng.choice([0, 1, 64, 100, -70, -110], (B, T, 3 * H, 1))
+    q, k, v = torch.from_numpy(x).bfloat16().to(DEV).split([H, H, H], 2)
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(D)).bfloat16().to(DEV)
+    cs, tab, L = torch.from_numpy(angles(20, D)).to(DEV), i32([[1], [0]]), i32([0, 3])
+    pos = L[:, None] + torch.arange(T, dtype=torch.int32, device=DEV)
+    slots = tab.long() * bs + pos
+    dt, d = {"bf16": (torch.bfloat16, D), "e4m3": (torch.float8_e4m3fn, D), "i4": (torch.uint8, D // 2)}[kind]
+    got, want = ([torch.zeros(2, H, bs, d, dtype=torch.bfloat16, device=DEV).to(dt) for _ in range(2)] for _ in range(2))
+    sc = [[torch.zeros(2, H, bs, D // 32, dtype=torch.uint8, device=DEV) if kind != "bf16" else None for _ in range(2)]
+          for _ in range(2)]
+    for eps in (0.0, 1e-6):
+        _, ko = sv.qk_norm_rope(q, k, cs, pos, w, w, eps=eps)
+        assert ko.isfinite().all()
+        sv.kv_write(ko, v, *want, tab, L, k_scale=sc[0][0], v_scale=sc[0][1])
+        sv.qk_norm_rope(q, k, cs, pos, w, w, eps=eps, value=v, k_cache=got[0], v_cache=got[1], slots=slots,
+                        k_scale=sc[1][0], v_scale=sc[1][1])
+        for a, b in zip(got, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert kind == "bf16" or all(torch.equal(a, b) for a, b in zip(*sc))
+
+
 # ------------------------------------------- a rotation's arguments ----
 
 def rope_words(p, **over):
